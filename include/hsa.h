@@ -254,6 +254,80 @@ hsa_status hsa_backward_varlen(const hsa_bf16 *Qs, const hsa_bf16 *Q, const hsa_
                                float *dL, float *dQs, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Paged cache: bookkeeping, writing, and the attention of a batch that shares a long prefix (no
+ * counterpart on the pages: many requests about ONE long document, whose keys and values are held once).
+ *
+ * A page holds 64 tokens (one chunk) of every key head; a pool is Kp, Vp [num_pages, Hkv, 64, D] bf16.
+ * Token position i of a request lives in page block_table[b][i / 64] at row i % 64; its SLOT is
+ * page * 64 + i % 64. p(n) = ceil(n / 64) below. Every length and table is device memory, so a captured
+ * graph follows them as they change. Batches of up to HSA_PAGED_MAX_BATCH requests.
+ * ------------------------------------------------------------------------------------------- */
+#define HSA_PAGED_MAX_BATCH 8192
+
+/* Block tables and slot maps of one serving step, from the requests' lengths; one launch, no workspace.
+ *
+ *   cache_len   [B] int64              tokens that request b holds now (c)
+ *   new_len     [B] int32              n > 0: tokens it adds in this step; 0: idle; < 0: it is finished
+ *   block_table [B, max_pages] int32   in/out: entries [0, p(c)) are read, entries [p(c), p(c + n)) written
+ *   free_pages  [num_free] int32       in/out: a ring of free page ids
+ *   pool        [3] int64              {taken, returned, -}: the ring's free entries are those of index
+ *                                      taken .. returned - 1 (mod num_free); a pool of F free pages starts
+ *                                      as num_free >= F, {0, F, 0}
+ *   pool_out    [3] int64              {taken, returned, requests refused} afterwards; may be `pool` itself
+ *   total_len   [B] int64              lengths afterwards: c + n, c (idle or refused), 0 (finished); may be
+ *                                      `cache_len` itself
+ *   cu_new      [B + 1] int32          running sums of the positive n: request b's new tokens are rows
+ *                                      cu_new[b] .. cu_new[b + 1] - 1 of the packed step (sums of 2^31 or
+ *                                      more are stored as 2^31 - 1)
+ *   slots       [max_tokens] int64     slot of each packed row; -1 for rows of refused requests and for the
+ *                                      rows behind the last one
+ * Pages are taken in request order. A request that adds tokens is refused, and nothing of it changes, if
+ * its cache_len is outside [0, 64 * max_pages], if c + n does not fit its table, if its rows pass
+ * max_tokens, or if it needs pages and the sum of the pages needed up to and including it is more than
+ * the pool holds. A finished request's p(c) pages go to the ring's end, for later steps (its table entries
+ * stay as they are); one with an invalid cache_len keeps it and counts as refused. Outputs other than the
+ * pairs named above must not overlap anything. Requires B * max_pages < 2^31, 1 <= num_free < 2^30.
+ * 16-byte alignment is not needed: each array is aligned to its element. */
+hsa_status hsa_page_plan(const int64_t *cache_len, const int32_t *new_len, int B, int32_t *block_table, int max_pages,
+                         int32_t *free_pages, int num_free, const int64_t *pool, int64_t *pool_out,
+                         int64_t *total_len, int32_t *cu_new, int64_t *slots, int max_tokens, void *stream);
+
+/* Writes packed key/value rows into their slots.
+ *
+ *   K, V    rows [n, Hkv, D] bf16; a token's heads are contiguous and tokens are k_stride / v_stride elements
+ *           apart (multiples of 8, >= Hkv * D when n > 1: slices of a fused projection are taken as they are)
+ *   slots   [n] int64; a row whose slot is outside [0, 64 * num_pages) is skipped
+ *   Kp, Vp  the pools; they must not overlap K, V or each other
+ * Two rows with the same slot leave an unspecified mixture of the two there. n = 0 is a valid call. */
+hsa_status hsa_page_append(const hsa_bf16 *K, int64_t k_stride, const hsa_bf16 *V, int64_t v_stride,
+                           const int64_t *slots, int n, int Hkv, int D, int page, hsa_bf16 *Kp, hsa_bf16 *Vp,
+                           int num_pages, void *stream);
+
+/* Softmax attention of a decode batch whose requests share a prefix: row (b, h, i) attends to the prefix's
+ * tokens and then request b's own, up to its own position (dense causal attention, not HSA's selection).
+ *
+ *   q             [B, H, Tq, D] bf16        the last Tq tokens of each request (their rows already appended);
+ *                                           query head h reads key head h / (H / Hkv)
+ *   Kp, Vp        [num_pages, Hkv, 64, D]   the pools
+ *   prefix_table  [max_prefix_pages] int32  the prefix's pages; prefix_len [1] int64 its tokens, P
+ *   block_table   [B, max_pages] int32      each request's own pages; own_len [B] int64 its own tokens, n
+ *   out           [B, H, Tq, D] bf16        softmax(scale q K^T) V, rounded to nearest-even from fp32
+ *   lse           [B, H, Tq] fp32           optional (NULL): log of the sum of exp(scale q K^T)
+ * Token i sits at position P + n - Tq + i and sees the positions up to its own. A request with n < 0 is
+ * an empty row of a padded batch. Rows that see nothing get out = 0, lse = -inf. Lengths beyond the
+ * tables are cut to them (P <= 0: no prefix); the tokens of a page whose id is outside [0, num_pages) are left out. What
+ * lies behind a length in its last page may be anything, NaN included; visible tokens must be finite.
+ * max_prefix_pages or max_pages may be 0 (its table may then be NULL). H / Hkv * Tq <= 1024, 1 <= Tq <= 64.
+ * Each prefix page is read once for up to 256 rows (request, query head, token) of its key head. */
+size_t hsa_prefix_decode_workspace_size(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages, int max_pages);
+
+hsa_status hsa_prefix_decode(const hsa_bf16 *q, const hsa_bf16 *Kp, const hsa_bf16 *Vp, int num_pages,
+                             const int32_t *prefix_table, int max_prefix_pages, const int64_t *prefix_len,
+                             const int32_t *block_table, int max_pages, const int64_t *own_len, int B, int H, int Hkv,
+                             int Tq, int D, int page, float scale, hsa_bf16 *out, float *lse, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Self-test of the bounded device waits (no counterpart on the pages; failure detection).
  *
  * Every kernel waits on mbarriers with a bounded number of probes; a wait that runs out records the

@@ -2,7 +2,7 @@
 // launches on the caller's stream. Nothing here allocates device memory or computes any part of the
 // operator (hsa_workspace_status alone synchronises, by its definition); every step of HSA runs in the
 // kernels of decode.cu / prefill.cu / score_wide.cu / score_tc.cu / attn_tc.cu / backward.cu / bwd_tc.cu / qknorm.cu /
-// varlen.cu.
+// varlen.cu / page.cu / prefix.cu.
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -557,6 +557,127 @@ hsa_status hsa_backward_varlen(const hsa_bf16 *Qs, const hsa_bf16 *Q, const hsa_
     if (e == cudaSuccess) e = hsa::launch_varlen_rows(l.dL, dL, l.cuN, B, Hkv, Tp / 64, frow, false, false, 0u, s);
     if (e == cudaSuccess && Qs) e = hsa::launch_varlen_rows(l.dQs, dQs, cu_seqlens, B, H, Tp, frow, false, false, 0u, s);
     return cuda_status(e, "hsa_backward_varlen");
+}
+
+}  // extern "C"
+
+// ---- paged cache ----
+
+// Pages are one chunk; the batch bound is that of the kernels' shared-memory tables.
+static hsa_status check_paged(int Hkv, int D, int page, int num_pages) {
+    if (Hkv < 1) return fail(HSA_ERR_INVALID_ARG, "Hkv must be >= 1 (got %d)", Hkv);
+    if (D < 1) return fail(HSA_ERR_INVALID_ARG, "D must be >= 1 (got %d)", D);
+    if (page < 1) return fail(HSA_ERR_INVALID_ARG, "page must be >= 1 (got %d)", page);
+    if (num_pages < 1) return fail(HSA_ERR_INVALID_ARG, "num_pages must be >= 1 (got %d)", num_pages);
+    if (D != 64 && D != 128) return fail(HSA_ERR_UNSUPPORTED, "head dim D=%d not supported (64 or 128)", D);
+    if (page != hsa::kChunk) return fail(HSA_ERR_UNSUPPORTED, "page=%d not supported (64 only)", page);
+    if ((double)num_pages * Hkv * page >= 2147483647.0)
+        return fail(HSA_ERR_UNSUPPORTED, "num_pages * Hkv * 64 must stay below 2^31");
+    return HSA_OK;
+}
+
+static hsa_status check_batch(int B, int max_pages) {
+    if (B < 1) return fail(HSA_ERR_INVALID_ARG, "B must be >= 1 (got %d)", B);
+    if (max_pages < 0) return fail(HSA_ERR_INVALID_ARG, "max_pages must be >= 0 (got %d)", max_pages);
+    if (B > HSA_PAGED_MAX_BATCH)
+        return fail(HSA_ERR_UNSUPPORTED, "B=%d not supported (max %d)", B, HSA_PAGED_MAX_BATCH);
+    if ((double)B * max_pages >= 2147483647.0)
+        return fail(HSA_ERR_UNSUPPORTED, "B * max_pages must stay below 2^31");
+    return HSA_OK;
+}
+
+static bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+extern "C" {
+
+hsa_status hsa_page_plan(const int64_t *cache_len, const int32_t *new_len, int B, int32_t *block_table, int max_pages,
+                         int32_t *free_pages, int num_free, const int64_t *pool, int64_t *pool_out,
+                         int64_t *total_len, int32_t *cu_new, int64_t *slots, int max_tokens, void *stream) {
+    g_last_error.clear();
+    hsa_status st = check_batch(B, max_pages);
+    if (st != HSA_OK) return st;
+    if (max_pages < 1) return fail(HSA_ERR_INVALID_ARG, "max_pages must be >= 1 (got %d)", max_pages);
+    if (max_tokens < 0) return fail(HSA_ERR_INVALID_ARG, "max_tokens must be >= 0 (got %d)", max_tokens);
+    if (num_free < 1) return fail(HSA_ERR_INVALID_ARG, "num_free must be >= 1 (got %d)", num_free);
+    if (num_free >= (1 << 30)) return fail(HSA_ERR_UNSUPPORTED, "num_free must stay below 2^30 (got %d)", num_free);
+    if (!cache_len || !new_len || !block_table || !free_pages || !pool || !pool_out || !total_len || !cu_new ||
+        (max_tokens > 0 && !slots))
+        return fail(HSA_ERR_INVALID_ARG, "pointers must not be NULL");
+    if (!aligned_to(cache_len, 8) || !aligned_to(pool, 8) || !aligned_to(pool_out, 8) || !aligned_to(total_len, 8) ||
+        !aligned_to(slots, 8) || !aligned_to(new_len, 4) || !aligned_to(block_table, 4) || !aligned_to(free_pages, 4) ||
+        !aligned_to(cu_new, 4))
+        return fail(HSA_ERR_INVALID_ARG, "pointers must be aligned to their elements");
+    if (static_cast<const void *>(block_table) == free_pages || static_cast<const void *>(cache_len) == new_len ||
+        static_cast<const void *>(cu_new) == new_len || static_cast<const void *>(slots) == cache_len ||
+        slots == total_len)
+        return fail(HSA_ERR_INVALID_ARG, "only total_len = cache_len and pool_out = pool may share memory");
+    hsa::PagePlanArgs a{cache_len, new_len, B, block_table, max_pages, free_pages, num_free, pool,
+                        pool_out,  total_len, cu_new, slots, max_tokens};
+    return cuda_status(hsa::launch_page_plan(a, static_cast<cudaStream_t>(stream)), "hsa_page_plan");
+}
+
+hsa_status hsa_page_append(const hsa_bf16 *K, int64_t k_stride, const hsa_bf16 *V, int64_t v_stride,
+                           const int64_t *slots, int n, int Hkv, int D, int page, hsa_bf16 *Kp, hsa_bf16 *Vp,
+                           int num_pages, void *stream) {
+    g_last_error.clear();
+    hsa_status st = check_paged(Hkv, D, page, num_pages);
+    if (st != HSA_OK) return st;
+    if (n < 0) return fail(HSA_ERR_INVALID_ARG, "n must be >= 0 (got %d)", n);
+    if (n == 0) return HSA_OK;
+    if (!K || !V || !slots || !Kp || !Vp) return fail(HSA_ERR_INVALID_ARG, "pointers must not be NULL");
+    if (!aligned16(K) || !aligned16(V) || !aligned16(Kp) || !aligned16(Vp) || !aligned_to(slots, 8))
+        return fail(HSA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned (slots 8-byte)");
+    if (n > 1 && (k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D))
+        return fail(HSA_ERR_INVALID_ARG, "row strides must be multiples of 8 and at least Hkv * D (got %lld, %lld)",
+                    (long long)k_stride, (long long)v_stride);
+    if (Kp == Vp) return fail(HSA_ERR_INVALID_ARG, "Kp and Vp must not share memory");
+    return cuda_status(hsa::launch_page_append(K, k_stride, V, v_stride, slots, n, Hkv, D, Kp, Vp, num_pages,
+                                               static_cast<cudaStream_t>(stream)),
+                       "hsa_page_append");
+}
+
+size_t hsa_prefix_decode_workspace_size(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages, int max_pages) {
+    if (B < 1 || B > HSA_PAGED_MAX_BATCH || H < 1 || Hkv < 1 || H % Hkv != 0 || Tq < 1 || Tq > 64 ||
+        (int64_t)(H / Hkv) * Tq > 1024 || D < 1 || max_prefix_pages < 0 || max_pages < 0)
+        return 0;
+    return hsa::prefix_workspace(B, H, Hkv, Tq, D, max_prefix_pages, max_pages);
+}
+
+hsa_status hsa_prefix_decode(const hsa_bf16 *q, const hsa_bf16 *Kp, const hsa_bf16 *Vp, int num_pages,
+                             const int32_t *prefix_table, int max_prefix_pages, const int64_t *prefix_len,
+                             const int32_t *block_table, int max_pages, const int64_t *own_len, int B, int H, int Hkv,
+                             int Tq, int D, int page, float scale, hsa_bf16 *out, float *lse, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    g_last_error.clear();
+    hsa_status st = check_paged(Hkv, D, page, num_pages);
+    if (st != HSA_OK) return st;
+    if ((st = check_batch(B, max_pages)) != HSA_OK) return st;
+    if (H < 1 || H % Hkv != 0)
+        return fail(HSA_ERR_INVALID_ARG, "H (%d) must be a positive multiple of Hkv (%d)", H, Hkv);
+    if (Tq < 1 || Tq > 64) return fail(HSA_ERR_INVALID_ARG, "Tq must be in [1, 64] (got %d)", Tq);
+    if ((int64_t)(H / Hkv) * Tq > 1024)
+        return fail(HSA_ERR_UNSUPPORTED, "H / Hkv * Tq = %lld not supported (max 1024)", (long long)(H / Hkv) * Tq);
+    if (max_prefix_pages < 0) return fail(HSA_ERR_INVALID_ARG, "max_prefix_pages must be >= 0");
+    if (max_prefix_pages >= (1 << 25) || max_pages >= (1 << 25))
+        return fail(HSA_ERR_UNSUPPORTED, "tables must stay below 2^25 pages (2^31 tokens)");
+    if ((double)B * H * Tq * D >= 2147483647.0) return fail(HSA_ERR_UNSUPPORTED, "B*H*Tq*D must stay below 2^31");
+    if (!q || !Kp || !Vp || !own_len || !out || (max_prefix_pages > 0 && (!prefix_table || !prefix_len)) ||
+        (max_pages > 0 && !block_table))
+        return fail(HSA_ERR_INVALID_ARG, "q, Kp, Vp, the lengths, their tables and out must not be NULL");
+    if (!aligned16(q) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(out) || !aligned_to(lse, 4) ||
+        !aligned_to(prefix_table, 4) || !aligned_to(block_table, 4) || !aligned_to(prefix_len, 8) ||
+        !aligned_to(own_len, 8))
+        return fail(HSA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned (lengths, tables and lse to their elements)");
+    const size_t need = hsa::prefix_workspace(B, H, Hkv, Tq, D, max_prefix_pages, max_pages);
+    if ((st = check_ws(workspace, workspace_bytes, need)) != HSA_OK) return st;
+    hsa::PrefixArgs a{};
+    a.q = q; a.Kp = Kp; a.Vp = Vp; a.num_pages = num_pages;
+    a.prefix_table = prefix_table; a.max_prefix_pages = max_prefix_pages; a.prefix_len = prefix_len;
+    a.block_table = block_table; a.max_pages = max_pages; a.own_len = own_len;
+    a.B = B; a.H = H; a.Hkv = Hkv; a.Tq = Tq; a.D = D;
+    a.scale = resolve_scale(scale, D);
+    a.out = out; a.lse = lse; a.workspace = workspace;
+    return cuda_status(hsa::launch_prefix_decode(a, static_cast<cudaStream_t>(stream)), "hsa_prefix_decode");
 }
 
 }  // extern "C"

@@ -173,6 +173,45 @@ cudaError_t launch_chunk_offsets(const int32_t *cu, int B, int32_t *cuN, cudaStr
 cudaError_t launch_varlen_rows(const void *src, void *dst, const int32_t *cu, int B, int Hs, int Tp, int row_bytes,
                                bool pack, bool fill_pad, uint32_t fill, cudaStream_t s);
 
+// Paged cache (page.cu). Pages of kChunk tokens; arguments as in include/hsa.h.
+struct PagePlanArgs {
+    const int64_t *cache_len;
+    const int32_t *new_len;
+    int B;
+    int32_t *block_table;
+    int max_pages;
+    int32_t *free_pages;
+    int num_free;
+    const int64_t *pool;
+    int64_t *pool_out, *total_len;
+    int32_t *cu_new;
+    int64_t *slots;
+    int max_tokens;
+};
+cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t s);
+cudaError_t launch_page_append(const uint16_t *K, int64_t k_stride, const uint16_t *V, int64_t v_stride,
+                               const int64_t *slots, int n, int Hkv, int D, uint16_t *Kp, uint16_t *Vp, int num_pages,
+                               cudaStream_t s);
+
+// Attention of a decode batch over a shared prefix and the requests' own pages (prefix.cu).
+struct PrefixArgs {
+    const uint16_t *q, *Kp, *Vp;
+    int num_pages;
+    const int32_t *prefix_table;
+    int max_prefix_pages;
+    const int64_t *prefix_len;
+    const int32_t *block_table;
+    int max_pages;
+    const int64_t *own_len;
+    int B, H, Hkv, Tq, D;
+    float scale;
+    uint16_t *out;
+    float *lse;
+    void *workspace;
+};
+size_t prefix_workspace(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages, int max_pages);
+cudaError_t launch_prefix_decode(const PrefixArgs &a, cudaStream_t s);
+
 // Message returned by hsa_last_error() on the calling thread.
 void set_last_error(const char *msg);
 

@@ -47,6 +47,11 @@ SIGNATURES = {
     "hsa_backward_varlen_workspace_size": ([_I, _I, _I, _I, _I, _I, _I, _U], _SZ),
     "hsa_backward_varlen": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _U, _P, _P,
                              _P, _P, _P, _P, _SZ, _P], _I),
+    "hsa_page_plan": ([_P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _I, _P], _I),
+    "hsa_page_append": ([_P, _I64, _P, _I64, _P, _I, _I, _I, _I, _P, _P, _I, _P], _I),
+    "hsa_prefix_decode_workspace_size": ([_I, _I, _I, _I, _I, _I, _I], _SZ),
+    "hsa_prefix_decode": ([_P, _P, _P, _I, _P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P],
+                          _I),
     "hsa_selftest_bounded_wait": ([_P, _SZ, _U, _P], _I),
     "hsa_profile_enable": ([_I], _I),
     "hsa_profile_summary": ([ctypes.c_char_p, _SZ], _I),
@@ -392,6 +397,120 @@ def hsa_backward_varlen(Q, K, V, L, out, dout, sel_idx, sel_w, cu_seqlens, max_s
                                    fl, _ptr(dQ), _ptr(dK), _ptr(dV), dlp, _ptr(dQs), wp, wn, _stream(dev, stream))
     _check("hsa_backward_varlen", st)
     return (dQ, dK, dV, dL) if Qs is None else (dQ, dK, dV, dL, dQs)
+
+
+def _on(dev, stream):
+    """The call's device and stream made current, so that what it allocates belongs to that stream."""
+    return torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)
+
+
+def hsa_page_plan(cache_len, new_len, block_table, free_pages, pool, max_tokens, cu_new=None, slots=None,
+                  total_len=None, pool_out=None, stream=None):
+    """Block tables and slot maps of one serving step, from the requests' lengths, all on the device.
+
+    cache_len [B] int64: tokens each request holds; new_len [B] int32: tokens it adds (0: idle, < 0: finished);
+    block_table [B, max_pages] int32 and free_pages [num_free] int32 (the ring of free pages) are updated in
+    place, and so is pool [3] int64 {taken, returned, refused} unless ``pool_out`` is given; total_len may be
+    cache_len itself. Returns (cu_new [B + 1] int32, slots [max_tokens] int64, total_len [B] int64); the
+    number of refused requests is in pool[2] (pool_out[2])."""
+    dev = cache_len.device
+    B, width = block_table.shape
+    pool_out = pool if pool_out is None else pool_out
+    with _on(dev, stream):
+        if cu_new is None:
+            cu_new = torch.empty((B + 1,), dtype=torch.int32, device=dev)
+        if slots is None:
+            slots = torch.empty((max_tokens,), dtype=torch.int64, device=dev)
+        if total_len is None:
+            total_len = torch.empty((B,), dtype=torch.int64, device=dev)
+        _need(cache_len, "cache_len", torch.int64, (B,), dev)
+        _need(new_len, "new_len", torch.int32, (B,), dev)
+        _need(block_table, "block_table", torch.int32, (B, width), dev)
+        _need(free_pages, "free_pages", torch.int32, (free_pages.numel(),), dev)
+        _need(pool, "pool", torch.int64, (3,), dev)
+        _need(pool_out, "pool_out", torch.int64, (3,), dev)
+        _need(cu_new, "cu_new", torch.int32, (B + 1,), dev)
+        _need(slots, "slots", torch.int64, (max_tokens,), dev)
+        _need(total_len, "total_len", torch.int64, (B,), dev)
+        st = lib().hsa_page_plan(_ptr(cache_len), _ptr(new_len), B, _ptr(block_table), width, _ptr(free_pages),
+                                 free_pages.numel(), _ptr(pool), _ptr(pool_out), _ptr(total_len), _ptr(cu_new),
+                                 _ptr(slots) if max_tokens else None, max_tokens, _stream(dev, stream))
+    _check("hsa_page_plan", st)
+    return cu_new, slots, total_len
+
+
+def _rows(t, name, dev):
+    """[n, Hkv, D] bf16 rows whose heads are contiguous; returns the distance between tokens in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    n, heads, D = t.shape
+    if n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name} must hold each token's heads contiguously")
+    return t.stride(0) if n > 1 else heads * D
+
+
+def hsa_page_append(K, V, slots, Kp, Vp, stream=None):
+    """Writes key/value rows into their slots of the page pools. K, V [n, Hkv, D] bf16, a token's heads
+    contiguous (slices of a fused projection are taken as they are); slots [n] int64 (a row whose slot is
+    outside the pool is skipped); Kp, Vp [num_pages, Hkv, 64, D] bf16, updated in place and returned."""
+    dev = Kp.device
+    n, Hkv, D = K.shape
+    pages = Kp.shape[0]
+    ks, vs = _rows(K, "K", dev), _rows(V, "V", dev)
+    if tuple(V.shape) != (n, Hkv, D):
+        raise ValueError(f"V must have shape {(n, Hkv, D)}, got {tuple(V.shape)}")
+    _need(slots, "slots", torch.int64, (n,), dev)
+    _need(Kp, "Kp", torch.bfloat16, (pages, Hkv, 64, D), dev)
+    _need(Vp, "Vp", torch.bfloat16, (pages, Hkv, 64, D), dev)
+    with _on(dev, stream):
+        st = lib().hsa_page_append(_ptr(K), ks, _ptr(V), vs, _ptr(slots), n, Hkv, D, 64, _ptr(Kp), _ptr(Vp), pages,
+                                   _stream(dev, stream))
+    _check("hsa_page_append", st)
+    return Kp, Vp
+
+
+def hsa_prefix_decode_workspace_size(B, H, Hkv, D, max_prefix_pages, max_pages, Tq=1):
+    return int(lib().hsa_prefix_decode_workspace_size(B, H, Hkv, Tq, D, max_prefix_pages, max_pages))
+
+
+def hsa_prefix_decode(q, Kp, Vp, prefix_table, prefix_len, block_table, own_len, scale=0.0, out=None, lse=None,
+                      workspace=None, stream=None):
+    """Softmax attention of a decode batch whose requests share a prefix, the prefix computed once for all.
+
+    q [B, H, D] (or [B, H, Tq, D]: the last Tq tokens of each request) bf16; Kp, Vp [num_pages, Hkv, 64, D]
+    bf16; prefix_table [max_prefix_pages] int32 and prefix_len [1] int64: the shared tokens; block_table
+    [B, max_pages] int32 and own_len [B] int64: each request's own (negative: an empty row of a padded batch,
+    out = 0 and lse = -inf). Returns (out shaped like q, lse fp32 without the last dimension)."""
+    dev = q.device
+    multi = q.dim() == 4
+    B, H, D = q.shape[0], q.shape[1], q.shape[-1]
+    Tq = q.shape[2] if multi else 1
+    pages, Hkv = Kp.shape[0], Kp.shape[1]
+    npre, width = prefix_table.numel(), block_table.shape[1]
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        _need(q, "q", torch.bfloat16, q.shape, dev)
+        _need(Kp, "Kp", torch.bfloat16, (pages, Hkv, 64, D), dev)
+        _need(Vp, "Vp", torch.bfloat16, (pages, Hkv, 64, D), dev)
+        _need(prefix_table, "prefix_table", torch.int32, (npre,), dev)
+        _need(prefix_len, "prefix_len", torch.int64, (1,), dev)
+        _need(block_table, "block_table", torch.int32, (B, width), dev)
+        _need(own_len, "own_len", torch.int64, (B,), dev)
+        _need(out, "out", torch.bfloat16, q.shape, dev)
+        _need(lse, "lse", torch.float32, q.shape[:-1], dev)
+        wp, wn = _aligned(_workspace(hsa_prefix_decode_workspace_size(B, H, Hkv, D, npre, width, Tq), dev, workspace))
+        st = lib().hsa_prefix_decode(_ptr(q), _ptr(Kp), _ptr(Vp), pages, _ptr(prefix_table) if npre else None, npre,
+                                     _ptr(prefix_len), _ptr(block_table) if width else None, width, _ptr(own_len), B, H,
+                                     Hkv, Tq, D, 64, float(scale), _ptr(out), _ptr(lse), wp, wn, _stream(dev, stream))
+    _check("hsa_prefix_decode", st)
+    return out, lse
 
 
 def hsa_profile_enable(on=True):

@@ -302,6 +302,19 @@ def test_prefix_decode_repeats_bit_for_bit_and_ignores_the_workspace():
         assert torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefix_decode_long_runs_and_many_short_segments_back_to_back(D):
+    """Runs of many tiles and segments of an odd number of them, so that the copies' ring goes round many times with
+    its slots changing hands between the two streams; many calls without a pause between them."""
+    own = [1 + 61 * i % 700 for i in range(40)]
+    q, Kp, Vp, pre, prefix, table, own, scale = decode_case(33, B=40, H=2, Hkv=2, Tq=1, D=D, prefix=40000, own=own)
+    args = [torch.tensor(x, device=DEV) for x in (pre, [prefix], table, own)]
+    got = [hsa.hsa_prefix_decode(q, Kp, Vp, *args) for _ in range(60)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, got[0][0]) and torch.equal(l, got[0][1]) for o, l in got)
+    check_decode(q, Kp, Vp, pre, prefix, table, own, scale)
+
+
 def test_prefix_decode_follows_its_lengths_in_a_captured_graph():
     """Two graphs share a workspace and are replayed in turn while lengths and tables change on the device."""
     q, Kp, Vp, pre, prefix, table, own, scale = decode_case(30, B=6, H=8, Hkv=2, Tq=1, D=64, prefix=3000, own=[5, 64, 900, 1, 130, -1], poison=False)

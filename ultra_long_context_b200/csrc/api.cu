@@ -658,8 +658,8 @@ hsa_status hsa_prefix_decode(const hsa_bf16 *q, const hsa_bf16 *Kp, const hsa_bf
     if ((int64_t)(H / Hkv) * Tq > 1024)
         return fail(HSA_ERR_UNSUPPORTED, "H / Hkv * Tq = %lld not supported (max 1024)", (long long)(H / Hkv) * Tq);
     if (max_prefix_pages < 0) return fail(HSA_ERR_INVALID_ARG, "max_prefix_pages must be >= 0");
-    if (max_prefix_pages >= (1 << 25) || max_pages >= (1 << 25))
-        return fail(HSA_ERR_UNSUPPORTED, "tables must stay below 2^25 pages (2^31 tokens)");
+    if (max_prefix_pages >= (1 << 24) || max_pages >= (1 << 24))
+        return fail(HSA_ERR_UNSUPPORTED, "tables must stay below 2^24 pages (2^30 tokens)");
     if ((double)B * H * Tq * D >= 2147483647.0) return fail(HSA_ERR_UNSUPPORTED, "B*H*Tq*D must stay below 2^31");
     if (!q || !Kp || !Vp || !own_len || !out || (max_prefix_pages > 0 && (!prefix_table || !prefix_len)) ||
         (max_pages > 0 && !block_table))

@@ -1,0 +1,290 @@
+// prefix.cuh -- how the shared-prefix decode divides its work: shared by its kernels (prefix_few.cu,
+// prefix_wide.cu) and the join of their partials (prefix.cu).
+//
+// For a query row q and its visible keys, out = sum_k exp(s_k - m) v_k / sum_k exp(s_k - m) with
+// s = scale q.k. The keys are cut into tiles of 128 (two pages). A SEGMENT is a run of tiles of one page list
+// (the prefix's, or a request's own) for one key head and up to 256 query rows: all rows of the batch that read
+// the key head, for the prefix; the request's own rows, for its own pages. Over a segment a row keeps its running
+// maximum m, sum l = sum exp(s - m) and output O = sum exp(s - m) v, and the segments' (m, l, O) of a row are
+// joined at the end. So every prefix page is read once for up to 256 rows, and both kinds of work are the same.
+#pragma once
+
+#include <cuda.h>
+
+#include "launch.h"
+#include "tc.cuh"
+
+namespace hsa {
+
+constexpr int kPfTile = 128;      // keys per tile = 2 pages
+constexpr int kPfRows = 256;      // rows per segment at most
+constexpr int kPfFewRows = 64;    // segments of up to this many rows go to the few-rows kernel
+constexpr int kPfCtas = 148;      // at most: one per SM; the workspace is sized for it
+constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per head and row group)
+// Costs in half tiles: a tile, and what a segment's start and end take beside its tiles
+constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 1;
+
+// The division of one kernel's work; every CTA computes the same, CTA 0 stores it for the join.
+//   prefix: per key head and row group, `nsplit` runs of `run` tiles; segment i goes to CTA i % ctas, the row
+//   groups of one run next to each other (they read the same keys at about the same time, through L2);
+//   own: the stretches of all (request, key head, row group), weight = cost of their tiles + kPfOwnCost each, laid
+//   end to end on an axis, and the axis cut into one interval per CTA such that prefix and own work
+//   add up evenly: the first `lo_ctas` CTAs, which have one prefix segment more, get `cap_lo`, the others `cap_hi`.
+struct PfPlan {
+    int ctas, P, tiles, run, nsplit, items, lo_ctas, pad;  // P: the prefix's tokens
+    int64_t cap_lo, cap_hi, axis;
+    __device__ int64_t start(int i) const {
+        const int64_t x = i <= lo_ctas ? i * cap_lo : lo_ctas * cap_lo + (i - lo_ctas) * cap_hi;
+        return x < axis ? x : axis;
+    }
+    __device__ int cta_of(int64_t x) const {
+        return x < lo_ctas * cap_lo ? (int)(x / cap_lo) : lo_ctas + (int)((x - lo_ctas * cap_lo) / cap_hi);
+    }
+};
+
+// Sizes that follow from the call's arguments alone.
+struct PfDims {
+    int Rp, Rgp;           // prefix rows per key head, in groups of kPfRows
+    int Ro, Rgo;           // own rows per request and key head
+    int strideP, strideO;  // rows of one segment's partials (two streams of few rows keep one each)
+    int max_items, max_slots, blocks;  // blocks: of 32 requests
+    PfDims(int B, int H, int Hkv, int Tq, int max_prefix_pages) {
+        Ro = H / Hkv * Tq;
+        Rp = B * Ro;
+        Rgp = (Rp + kPfRows - 1) / kPfRows;
+        Rgo = (Ro + kPfRows - 1) / kPfRows;
+        strideP = Rp <= kPfTile ? 2 * Rp : kPfRows;
+        strideO = Ro <= kPfTile ? 2 * Ro : kPfRows;
+        const int units = Hkv * Rgp, tiles = (max_prefix_pages + 1) / 2;
+        int ns = kPfItems / units;
+        ns = ns < 1 ? 1 : ns;
+        ns = ns < tiles ? ns : tiles;
+        max_items = units * ns;
+        max_slots = B * Hkv * Rgo + kPfCtas;
+        blocks = (B + 31) / 32;
+    }
+};
+
+struct PfWork {
+    int32_t *err;
+    PfPlan *planP, *planO;   // of the kernel that takes the prefix / the own pages
+    int32_t *status;         // [2][kPfCtas]: a kernel's CTAs; nonzero where a wait ran out
+    int32_t *bcum;           // [blocks + 1] weights of the requests before each block
+    float *Op, *mlp;         // prefix partials [max_items][strideP][D], [..][2] (m * scale * log2(e), l)
+    float *Oo, *mlo;         // own partials [max_slots][strideO][D], [..][2]
+};
+
+__device__ __forceinline__ int64_t pf_clamp_len(int64_t n, int pages) { return min(n, (int64_t)pages * kChunk); }
+__device__ __forceinline__ int pf_tiles(int64_t n) { return n > 0 ? (int)((n + kPfTile - 1) / kPfTile) : 0; }
+__device__ __forceinline__ int pf_weight(int64_t n) { return n > 0 ? kPfTileCost * pf_tiles(n) + kPfOwnCost : 0; }
+// Tile boundary of a place on a stretch: 0 at its start, the number of tiles at its end, never decreasing.
+__device__ __forceinline__ int pf_tile_at(int64_t at) { return (int)(max(at - kPfOwnCost + kPfTileCost - 1, (int64_t)0) / kPfTileCost); }
+
+struct PfSeg {
+    int h, b;            // key head; request (own segments; -1: prefix)
+    int r0, nr;          // its rows among the key head's (prefix) or the request's (own)
+    int tile0, nt;       // run of tiles
+    int len;             // tokens of the sequence
+    int part;            // index of its partials
+    const int32_t *table;
+};
+
+// Walks a CTA's segments; by a whole warp, its lanes holding the lengths of a block of 32 requests.
+struct PfWalk {
+    const PrefixArgs &a;
+    const PfPlan &p;
+    const int32_t *bcum;
+    const PfDims &d;
+    int item, lane, blk, len, weight, before;
+    int64_t x, end;
+    __device__ PfWalk(const PrefixArgs &a_, const PfPlan &p_, const int32_t *bcum_, const PfDims &d_)
+        : a(a_), p(p_), bcum(bcum_), d(d_), item(blockIdx.x), lane(threadIdx.x & 31), blk(-1), len(0), weight(0), before(0),
+          x(p_.start(blockIdx.x)), end(p_.start(blockIdx.x + 1)) {}
+    __device__ void load_block(int k) {
+        blk = k;
+        const int b = 32 * k + lane;
+        const int64_t n = b < a.B ? pf_clamp_len(a.own_len[b], a.max_pages) : -1;
+        len = n > 0 ? (int)n : 0;
+        weight = pf_weight(n);
+        int sum = weight;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        before = bcum[k] + sum - weight;
+    }
+    __device__ bool next(PfSeg &s) {
+        if (item < p.items) {
+            const int rg = item % d.Rgp, k = item / d.Rgp % p.nsplit;
+            s.h = item / d.Rgp / p.nsplit;
+            s.b = -1;
+            s.r0 = rg * kPfRows;
+            s.nr = min(kPfRows, d.Rp - s.r0);
+            s.tile0 = k * p.run;
+            s.nt = min(p.run, p.tiles - s.tile0);
+            s.len = p.P;
+            s.part = item;
+            s.table = a.prefix_table;
+            item += p.ctas;
+            return true;
+        }
+        const int hr_n = a.Hkv * d.Rgo;
+        while (x < end) {
+            const int xw = (int)(x / hr_n);  // on the axis of the requests' weights alone
+            int lo = 0, hi = d.blocks;       // the block that holds it (blocks of no weight are passed over)
+            while (hi - lo > 1) {
+                const int m = (lo + hi) >> 1;
+                if (bcum[m] <= xw) lo = m;
+                else hi = m;
+            }
+            if (lo != blk) load_block(lo);
+            const unsigned at_or_before = __ballot_sync(0xffffffffu, weight > 0 && before <= xw);
+            const int l = 31 - __clz(at_or_before);
+            const int w = __shfl_sync(0xffffffffu, weight, l);
+            const int64_t rest = x - (int64_t)__shfl_sync(0xffffffffu, before, l) * hr_n;
+            s.len = __shfl_sync(0xffffffffu, len, l);
+            const int hr = (int)(rest / w), from = (int)(rest - (int64_t)hr * w);
+            const int to = (int)min((int64_t)w, from + (end - x));
+            x += to - from;
+            const int t0 = pf_tile_at(from), t1 = pf_tile_at(to);
+            if (t1 <= t0) continue;
+            s.b = 32 * lo + l;
+            s.h = hr / d.Rgo;
+            s.r0 = hr % d.Rgo * kPfRows;
+            s.nr = min(kPfRows, d.Ro - s.r0);
+            s.tile0 = t0;
+            s.nt = t1 - t0;
+            s.part = s.b * hr_n + hr + (int)blockIdx.x;
+            s.table = a.block_table + (int64_t)s.b * a.max_pages;
+            return true;
+        }
+        return false;
+    }
+};
+
+// Row rr of a segment: its row in q / out.
+__device__ __forceinline__ int64_t pf_q_row(const PfSeg &s, const PfDims &d, int Hkv, int rr) {
+    const int r = s.r0 + rr;
+    return s.b < 0 ? (int64_t)(r / d.Ro * Hkv + s.h) * d.Ro + r % d.Ro : (int64_t)(s.b * Hkv + s.h) * d.Ro + r;
+}
+
+// Tokens of the segment's sequence that its row rr sees. The empty rows of a padded batch compute something that
+// is never read (no limit, so that they do not slow the others' tiles).
+__device__ __forceinline__ int pf_limit(const PrefixArgs &a, const PfSeg &s, const PfDims &d, int rr) {
+    const int r = s.r0 + rr;
+    const int64_t own = pf_clamp_len(a.own_len[s.b < 0 ? r / d.Ro : s.b], a.max_pages);
+    if (own < 0) return INT32_MAX;
+    const int last = (int)own - a.Tq + r % d.Ro % a.Tq + 1;  // own tokens seen; below 0: prefix tokens not seen
+    return max(0, s.b < 0 ? s.len + min(last, 0) : last);
+}
+// A bound from below for all rows of the segment.
+__device__ __forceinline__ int pf_min_limit(const PrefixArgs &a, const PfSeg &s) { return max(0, s.len - a.Tq + 1); }
+
+// The division of the work, by the whole block of NT threads, into shared memory: the plan and bcum.
+template <int NT>
+__device__ void pf_schedule(const PrefixArgs &a, const PfDims &d, bool prefix, bool own, PfPlan *plan, int32_t *bcum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ctas = gridDim.x;
+    for (int k = warp; k < d.blocks; k += NT / 32) {
+        const int b = 32 * k + lane;
+        const int w = own && b < a.B ? pf_weight(pf_clamp_len(a.own_len[b], a.max_pages)) : 0;
+        const int sum = __reduce_add_sync(0xffffffffu, w);
+        if (lane == 0) bcum[k] = sum;
+    }
+    int64_t plen = 0;
+    if (warp == 0 && prefix && a.max_prefix_pages > 0) plen = pf_clamp_len(a.prefix_len[0], a.max_prefix_pages);
+    __syncthreads();
+    if (warp == 0) {
+        int total = 0;
+        for (int k0 = 0; k0 < d.blocks; k0 += 32) {
+            const int k = k0 + lane, w = k < d.blocks ? bcum[k] : 0;
+            int x = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (k < d.blocks) bcum[k] = total + x - w;
+            total += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) bcum[d.blocks] = total;
+        const int64_t axis = (int64_t)total * a.Hkv * d.Rgo;
+        const int P = plen > 0 ? (int)plen : 0, tiles = pf_tiles(P);
+        const int units = a.Hkv * d.Rgp;
+        PfPlan p{};
+        p.ctas = ctas;
+        p.P = P;
+        p.tiles = tiles;
+        p.axis = axis;
+        p.run = 1;
+        p.nsplit = 1;
+        if (tiles > 0) {
+            // a number of runs per lane: 1 .. 16, and what fills 1/4 .. 4 waves; the one that ends the work soonest,
+            // both kinds of it counted (fewer runs win a tie)
+            const int ns_max = min(max(kPfItems / units, 1), tiles);
+            const int want = lane < 16 ? lane + 1 : (int)((int64_t)(lane - 15) * ctas / 4 / units);
+            const int ns = min(max(want, 1), ns_max);
+            const int run = (tiles + ns - 1) / ns, items = units * ((tiles + run - 1) / run);
+            const int cost = kPfTileCost * run + kPfPrefixCost;
+            const int64_t waves = (int64_t)((items + ctas - 1) / ctas) * cost;
+            const int64_t even = ((int64_t)items * cost + axis + ctas - 1) / ctas;
+            long long key = max(waves, even) * 1024 + ns;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
+            const int best = (int)(key & 1023);
+            p.run = (tiles + best - 1) / best;
+            p.nsplit = (tiles + p.run - 1) / p.run;
+            p.items = units * p.nsplit;
+        }
+        const int64_t cost = kPfTileCost * p.run + kPfPrefixCost;
+        p.lo_ctas = p.items % ctas;
+        const int64_t pc_hi = p.items / ctas * cost, pc_lo = pc_hi + cost;
+        const int hi_ctas = ctas - p.lo_ctas;
+        const int64_t alone = (axis + hi_ctas - 1) / hi_ctas;
+        if (pc_hi + alone <= pc_lo) {  // the CTAs with a prefix segment less take all of it
+            p.cap_lo = 0;
+            p.cap_hi = alone;
+        } else {
+            const int64_t share = (axis + p.lo_ctas * pc_lo + hi_ctas * pc_hi + ctas - 1) / ctas;
+            p.cap_lo = share - pc_lo;
+            p.cap_hi = share - pc_hi;
+        }
+        if (lane == 0) *plan = p;
+    }
+    __syncthreads();
+}
+
+// For the join: what this kernel's CTA 0 knows.
+template <int NT>
+__device__ void pf_publish(const PfDims &d, bool prefix, bool own, const PfPlan *plan, const int32_t *bcum, const PfWork &w) {
+    if (blockIdx.x != 0) return;
+    if (own)
+        for (int k = threadIdx.x; k <= d.blocks; k += NT) w.bcum[k] = bcum[k];
+    if (threadIdx.x == 0 && prefix) *w.planP = *plan;
+    if (threadIdx.x == 0 && own) *w.planO = *plan;
+}
+
+// A bounded wait of a whole warp, with one answer for all lanes: the warp is converged behind it, which the
+// aligned tcgen05 loads and stores that follow need. A probe may suspend the thread for tens of microseconds, so
+// 2^15 of them are seconds.
+__device__ __forceinline__ bool pf_wait(uint32_t mbar, uint32_t parity) {
+    return __all_sync(0xffffffffu, tc::mbar_wait_n(mbar, parity, 1u << 15)) != 0;
+}
+__device__ __forceinline__ bool pf_wait_lane(uint32_t mbar, uint32_t parity) {
+    return tc::mbar_wait_n(mbar, parity, 1u << 15);
+}
+__device__ __forceinline__ bool pf_done(uint32_t mbar, uint32_t parity) {
+    return __all_sync(0xffffffffu, tc::mbar_test(mbar, parity)) != 0;
+}
+__device__ __forceinline__ void pf_cp_async_arrive(uint32_t mbar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(mbar) : "memory");
+}
+
+// The kernels (prefix_few.cu, prefix_wide.cu). prefix / own: the kinds of segments a launch takes; follows: it is
+// launched as the dependent of the other kernel, whose results it does not need.
+cudaError_t launch_prefix_few(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
+                              bool follows, cudaStream_t s);
+cudaError_t launch_prefix_wide(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
+                               cudaStream_t s);
+
+}  // namespace hsa

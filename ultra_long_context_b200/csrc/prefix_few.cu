@@ -1,0 +1,578 @@
+// prefix_few.cu -- segments of up to 64 query rows of the shared-prefix decode: the requests' own pages, and the
+// prefix of small batches. Bound by the bytes of K and V, so everything is laid out to keep copies in flight.
+//
+// Transposed products, keys on the tensor core's 128 rows and the few query rows on its N side, so that no
+// part of an MMA or of the softmax is spent on padding rows:
+//   S^T = K Q^T    (128 keys x N, fp32 in TMEM; thread = key)       P^T = exp2(S^T scale' - m) (bf16, to shared memory)
+//   O^T += V^T P^T (D x N, fp32 in TMEM; thread = dim)
+// A row's maximum m is that of the first tile and moves only when a later logit exceeds it by more than 2^8 (P stays
+// in a comfortable range up to there, and the final quotient cancels m); then, and in a segment's first tile,
+// the warpgroup reduces the maxima over the keys and rescales O^T in TMEM. Every other tile costs a thread N
+// exponentials and one barrier with a vote. Row sums stay per thread until the segment ends.
+//
+// Persistent, warp-specialised, one CTA per SM; the CTA's tiles are numbered through all its segments:
+//   warps 0-3, 4-7  softmax of the tiles n of even / odd number, each with an S^T, P^T, O^T (and m, l) of its own;
+//   warp 8      MMA issuer: S^T(n) as soon as its operands and S^T's buffer are there, O^T(n) as soon as P^T(n) is;
+//   warp 9      walks the segments, announces them to the other warps and copies K and V tiles by TMA, page by
+//               page (64 rows of one head are contiguous);
+//   warp 10     Q rows by cp.async, padded with zero rows to N.
+#include <cuda.h>
+
+#include "prefix.cuh"
+#include "profile.h"
+
+namespace hsa {
+
+constexpr int kFwMmaWarp = 8, kFwTmaWarp = 9, kFwQWarp = 10;
+constexpr int kFwThreads = 32 * (kFwQWarp + 1);
+constexpr int kFwRing = 4;    // announced segments
+constexpr int kFwFlags = 8;   // tiles whose page flags are kept (copies run at most KS tiles ahead of S^T)
+
+// What the other warps know of a segment.
+struct FwSeg {
+    PfSeg s;
+    int n0;  // number of its first tile
+};
+
+template <int D, int NR>  // NR: rows per segment at most
+struct FwSmem {
+    static constexpr int KH = D / 64;                     // 128-byte column blocks of D
+    static constexpr uint32_t OP = KH * 16384;            // one K or V tile [128][D]
+    static constexpr uint32_t QB = KH * NR * 128;         // Q rows [NR][D]
+    static constexpr uint32_t PB = 16384;                 // P^T [128 keys][64 rows]
+    static constexpr int KS = D == 64 ? 4 : 2, VS = D == 64 ? 5 : NR == 64 ? 2 : 3;
+    static_assert(KS + 4 <= kFwFlags, "page flags");
+    static constexpr uint32_t K = 0, V = K + KS * OP, P = V + VS * OP, Q = P + 2 * PB;
+    static constexpr uint32_t BAR = Q + 2 * QB;
+    static constexpr int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = 2 * KS + VS, kQFull = 2 * KS + 2 * VS,
+                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kInfo = kSFull + 2, kPFull = kInfo + 2,
+                         kODone = kPFull + 2, kOEmpty = kODone + 2, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kFwRing,
+                         NBAR = kSegEmpty + kFwRing;
+    static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;
+    static constexpr uint32_t MS = RING + kFwRing * sizeof(FwSeg);        // float[2][NR]: m * scale * log2(e), or -inf
+    static constexpr uint32_t LIM = MS + 2 * NR * 4;                      // int[2][NR]
+    static constexpr uint32_t FLAG = LIM + 2 * NR * 4;                    // int[kFwFlags]
+    static constexpr uint32_t MISC = FLAG + 4 * kFwFlags;                 // TMEM base, bad[2], -
+    static constexpr uint32_t PLAN = (MISC + 16 + 15) / 16 * 16;
+    static constexpr uint32_t BCUM = PLAN + (sizeof(PfPlan) + 15) / 16 * 16;  // int[blocks + 1]
+    static constexpr size_t dyn(int blocks) { return BCUM + 4 * ((size_t)blocks + 1) + 1024; }  // slack: 1 KB alignment
+    // scratch of a warpgroup inside its P^T buffer, used while that holds nothing: float[4][NR], then float[NR]
+    static constexpr uint32_t S_COL = 0, O_COL = 128, TMEM_COLS = 256;
+};
+static_assert(FwSmem<128, 64>::dyn(256) <= 227 * 1024 && FwSmem<128, 32>::dyn(256) <= 227 * 1024 &&
+                  FwSmem<64, 64>::dyn(256) <= 227 * 1024,
+              "shared memory budget");
+
+// Named barrier of a warpgroup that also ORs a predicate.
+__device__ __forceinline__ bool fw_bar_or(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id)
+        : "memory");
+    return r != 0u;
+}
+__device__ __forceinline__ void fw_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixArgs a, const PfDims d, const PfWork w,
+                                                                   const bool take_prefix, const bool take_own,
+                                                                   const bool follows,
+                                                                   const __grid_constant__ CUtensorMap tmK,
+                                                                   const __grid_constant__ CUtensorMap tmV) {
+    using SM = FwSmem<D, NR>;
+    constexpr int KS = SM::KS, VS = SM::VS;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sb = (raw + 1023u) & ~1023u;  // 1 KB aligned (swizzle atoms)
+    unsigned char *s = smem_raw + (sb - raw);
+    FwSeg *s_ring = reinterpret_cast<FwSeg *>(s + SM::RING);
+    float *s_ms = reinterpret_cast<float *>(s + SM::MS);
+    int *s_lim = reinterpret_cast<int *>(s + SM::LIM);
+    int *s_flag = reinterpret_cast<int *>(s + SM::FLAG);
+    volatile int *s_bad = reinterpret_cast<volatile int *>(s + SM::MISC) + 1;  // [2] per warpgroup, [1] any other warp's, too
+    PfPlan *s_plan = reinterpret_cast<PfPlan *>(s + SM::PLAN);
+    int32_t *s_bcum = reinterpret_cast<int32_t *>(s + SM::BCUM);
+    auto bar = [&](int i) { return sb + SM::BAR + 8u * (uint32_t)i; };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == kFwMmaWarp) tc::tmem_alloc(sb + SM::MISC, SM::TMEM_COLS);
+    if (tid == 0) {
+        s_bad[0] = s_bad[1] = s_bad[2] = 0;
+        for (int i = 0; i < KS; ++i) {
+            tc::mbar_init(bar(SM::kKFull + i), 1);
+            tc::mbar_init(bar(SM::kKEmpty + i), 1);
+        }
+        for (int i = 0; i < VS; ++i) {
+            tc::mbar_init(bar(SM::kVFull + i), 1);
+            tc::mbar_init(bar(SM::kVEmpty + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar(SM::kQFull + i), 32);
+            tc::mbar_init(bar(SM::kQEmpty + i), 1);
+            tc::mbar_init(bar(SM::kSFull + i), 1);
+            tc::mbar_init(bar(SM::kInfo + i), 1);
+            tc::mbar_init(bar(SM::kPFull + i), 128);
+            tc::mbar_init(bar(SM::kODone + i), 1);
+            tc::mbar_init(bar(SM::kOEmpty + i), 128);
+        }
+        for (int i = 0; i < kFwRing; ++i) {
+            tc::mbar_init(bar(SM::kSegFull + i), 1);
+            tc::mbar_init(bar(SM::kSegEmpty + i), 10);  // the warps but this ring's writer
+        }
+        tc::fence_mbar_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *reinterpret_cast<uint32_t *>(s + SM::MISC);
+    if (!follows) pdl_wait();  // what precedes the call in its stream is visible from here on
+    pf_schedule<kFwThreads>(a, d, take_prefix, take_own, s_plan, s_bcum);
+    pf_publish<kFwThreads>(d, take_prefix, take_own, s_plan, s_bcum, w);
+    bool ok = true;
+
+    // the next announced segment; nr = 0 ends the walk
+    int seg_no = 0;
+    auto take = [&](FwSeg &g) {
+        const int slot = seg_no % kFwRing;
+        if (!pf_wait(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kFwRing) & 1u)) return false;
+        g = s_ring[slot];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(SM::kSegEmpty + slot));
+        ++seg_no;
+        return true;
+    };
+
+    if (warp == kFwTmaWarp) {
+        // ================= the walk, K and V tiles =================
+        PfWalk walk(a, *s_plan, s_bcum, d);
+        const int pages_all = a.num_pages;
+        int n = 0;
+        bool more = true;
+        while (ok && more) {
+            FwSeg g;
+            more = walk.next(g.s);
+            if (!more) g.s.nr = 0;
+            g.n0 = n;
+            const int slot = seg_no % kFwRing;
+            ok = pf_wait(bar(SM::kSegEmpty + slot), ((uint32_t)(seg_no / kFwRing) & 1u) ^ 1u);
+            if (!ok) break;
+            if (lane == 0) {
+                s_ring[slot] = g;
+                tc::mbar_arrive(bar(SM::kSegFull + slot));
+            }
+            ++seg_no;
+            if (!more) break;
+            const PfSeg &seg = g.s;
+            const int last_page = min((seg.len + kChunk - 1) / kChunk, 2 * (seg.tile0 + seg.nt));
+            auto fetch = [&](int from) {  // this lane's page id of the batch that starts at page `from`
+                const int i = from + lane;
+                return i < last_page ? seg.table[i] : -1;
+            };
+            int ids = fetch(2 * seg.tile0), ids_next = 0;
+            for (int t = 0; t < seg.nt; ++t, ++n) {
+                if (t % 16 == 0) {
+                    if (t > 0) ids = ids_next;
+                    ids_next = fetch(2 * (seg.tile0 + t) + 32);
+                }
+                const int p0 = __shfl_sync(0xffffffffu, ids, 2 * (t & 15)), p1 = __shfl_sync(0xffffffffu, ids, 2 * (t & 15) + 1);
+                if (lane == 0) {
+                    const bool g0 = p0 >= 0 && p0 < pages_all, g1 = p1 >= 0 && p1 < pages_all;
+                    // a page that is not there lies behind the pool's last row: it is filled with zeros
+                    const int y0 = ((g0 ? p0 : pages_all) * a.Hkv + (g0 ? seg.h : 0)) * kChunk;
+                    const int y1 = ((g1 ? p1 : pages_all) * a.Hkv + (g1 ? seg.h : 0)) * kChunk;
+                    const int ks = n % KS, vs = n % VS;
+                    ok = pf_wait_lane(bar(SM::kKEmpty + ks), ((uint32_t)(n / KS) & 1u) ^ 1u);
+                    if (ok) {
+                        const uint32_t dst = sb + SM::K + ks * SM::OP;
+                        s_flag[n % kFwFlags] = (g0 ? 1 : 0) | (g1 ? 2 : 0);
+                        tc::mbar_arrive_expect_tx(bar(SM::kKFull + ks), SM::OP);
+#pragma unroll
+                        for (int h = 0; h < SM::KH; ++h) {
+                            tc::tma_load_2d(dst + h * 16384, &tmK, h * 64, y0, bar(SM::kKFull + ks));
+                            tc::tma_load_2d(dst + h * 16384 + 8192, &tmK, h * 64, y1, bar(SM::kKFull + ks));
+                        }
+                        ok = pf_wait_lane(bar(SM::kVEmpty + vs), ((uint32_t)(n / VS) & 1u) ^ 1u);
+                        if (!ok) pf_wait_lane(bar(SM::kKFull + ks), (uint32_t)(n / KS) & 1u);
+                    }
+                    if (ok) {
+                        const uint32_t dst = sb + SM::V + vs * SM::OP;
+                        tc::mbar_arrive_expect_tx(bar(SM::kVFull + vs), SM::OP);
+#pragma unroll
+                        for (int h = 0; h < SM::KH; ++h) {
+                            tc::tma_load_2d(dst + h * 16384, &tmV, h * 64, y0, bar(SM::kVFull + vs));
+                            tc::tma_load_2d(dst + h * 16384 + 8192, &tmV, h * 64, y1, bar(SM::kVFull + vs));
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                if (!ok) break;
+            }
+        }
+        // every copy has landed before the CTA may exit, however the walk ended
+        for (int i = max(0, n - KS); i < n; ++i) pf_wait(bar(SM::kKFull + i % KS), (uint32_t)(i / KS) & 1u);
+        for (int i = max(0, n - VS); i < n; ++i) pf_wait(bar(SM::kVFull + i % VS), (uint32_t)(i / VS) & 1u);
+    } else if (warp == kFwQWarp) {
+        // ================= Q rows =================
+        constexpr int CPR = D / 8, RPW = 32 / CPR;  // 16-byte chunks per row, rows per warp-wide copy
+        const int rsub = lane / CPR, ch = lane % CPR;
+        FwSeg g;
+        while (true) {
+            const int q = seg_no & 1;
+            const uint32_t use = (uint32_t)(seg_no >> 1);
+            ok = take(g);
+            if (!ok || g.s.nr == 0) break;
+            ok = pf_wait(bar(SM::kQEmpty + q), (use & 1u) ^ 1u);
+            if (!ok) break;
+            const uint32_t dst = sb + SM::Q + q * SM::QB;
+            for (int r = rsub; r < (g.s.nr + 15) / 16 * 16; r += RPW) {
+                const bool in = r < g.s.nr;
+                cp_async16_u32(dst + (ch >> 3) * (NR * 128) + tc::sw128(r, ch & 7),
+                               in ? a.q + pf_q_row(g.s, d, a.Hkv, r) * D + ch * 8 : a.q, in ? 16 : 0);
+            }
+            pf_cp_async_arrive(bar(SM::kQFull + q));  // fires when this thread's copies have landed
+        }
+        cp_async_commit();
+        cp_async_wait<0>();  // nothing in flight when the CTA exits
+    } else if (warp == kFwMmaWarp) {
+        // ================= MMA issuer: the whole warp runs the loop, one elected lane issues =================
+        FwSeg g;
+        bool have = false, end = false;   // is there a segment at next_s; is there none any more
+        int t = 0, q = 0;                 // of next_s: tile of the segment; Q buffer
+        uint32_t quse = 0;
+        int next_s = 0, next_o = 0;       // tiles
+        uint32_t idesc[2] = {0, 0}, tiles[2] = {0, 0}, runs[2] = {0, 0};
+        bool first[2] = {false, false};   // does tile next_o (of the parity) begin a run of its stream in its segment?
+        int k_seen = 0, v_seen = 0, k_slot = 0, v_slot = 0;  // fillings of the slots observed, in order
+        uint32_t k_par = 0, v_par = 0, idle = 0;
+        while (true) {
+            bool progress = false;
+            if (!have && !end) {
+                const int slot = seg_no % kFwRing;
+                if (pf_done(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kFwRing) & 1u)) {
+                    q = seg_no & 1;
+                    quse = (uint32_t)(seg_no >> 1);
+                    take(g);
+                    have = g.s.nr > 0;
+                    end = !have;
+                    t = 0;
+                    progress = true;
+                }
+            }
+            if (end && next_o == next_s) break;
+            if (pf_done(bar(SM::kKFull + k_slot), k_par)) {
+                ++k_seen;
+                if (++k_slot == KS) k_slot = 0, k_par ^= 1u;
+            }
+            if (pf_done(bar(SM::kVFull + v_slot), v_par)) {
+                ++v_seen;
+                if (++v_slot == VS) v_slot = 0, v_par ^= 1u;
+            }
+#pragma unroll
+            for (int sid = 0; sid < 2; ++sid) {  // O^T(next_o)
+                if (next_o >= next_s || (next_o & 1) != sid || next_o >= v_seen) continue;
+                if (!pf_done(bar(SM::kPFull + sid), tiles[sid] & 1u)) continue;
+                if (first[sid] && runs[sid] > 1 && !pf_done(bar(SM::kOEmpty + sid), (runs[sid] - 2) & 1u)) continue;
+                tc::fence_after();
+                const int vs = next_o % VS;
+                const uint32_t sv = sb + SM::V + vs * SM::OP, sp = sb + SM::P + sid * SM::PB;
+                const uint32_t id = idesc[sid] | (1u << 15) | (1u << 16);  // A and B MN-major
+                // the second 64 rows of A: dims 64 .. 127, or, with D = 64, whatever follows the tile (lanes that are not read)
+#pragma unroll
+                for (int k = 0; k < kPfTile / 16; ++k)
+                    tc::mma_bf16_ss_w(tmem + SM::O_COL + sid * 64, tc::desc_mnmajor(sv + k * 2048, 16384),
+                                      tc::desc_mnmajor(sp + k * 2048, 16384), id, first[sid] && k == 0 ? 0u : 1u);
+                tc::commit_w(bar(SM::kODone + sid));
+                tc::commit_w(bar(SM::kVEmpty + vs));
+                first[sid] = false;
+                ++tiles[sid];
+                ++next_o;
+                progress = true;
+            }
+            // S^T(next_s): its buffer is free once P^T of the tile two before is written. The V filling before this
+            // tile's in its slot has landed, so that a softmax wait on the slot's parity, which follows S^T, is exact
+            if (have && next_s < next_o + 2 && next_s < k_seen && next_s - VS < v_seen &&
+                (t > 0 || pf_done(bar(SM::kQFull + q), quse & 1u))) {
+                tc::fence_after();
+                tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
+                const int ks = next_s % KS;
+                const uint32_t sk = sb + SM::K + ks * SM::OP, sq = sb + SM::Q + q * SM::QB;
+                const uint32_t id = tc::idesc_bf16(128, (g.s.nr + 15) / 16 * 16, 0, 0);
+#pragma unroll
+                for (int sid = 0; sid < 2; ++sid) {
+                    if ((next_s & 1) != sid) continue;
+                    if (lane == 0) tc::mbar_arrive(bar(SM::kInfo + sid));  // hands on the page flags that came with K
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * 64,
+                                          tc::desc_kmajor(sk + (k >> 2) * 16384 + (k & 3) * 32),
+                                          tc::desc_kmajor(sq + (k >> 2) * (NR * 128) + (k & 3) * 32), id, k > 0 ? 1u : 0u);
+                    tc::commit_w(bar(SM::kSFull + sid));
+                    idesc[sid] = id;
+                    if (t < 2) {
+                        first[sid] = true;
+                        ++runs[sid];
+                    }
+                }
+                tc::commit_w(bar(SM::kKEmpty + ks));
+                if (++t == g.s.nt) {
+                    tc::commit_w(bar(SM::kQEmpty + q));
+                    have = false;
+                }
+                ++next_s;
+                progress = true;
+            }
+            if (progress) {
+                idle = 0;
+            } else if (++idle > (1u << 25)) {
+                ok = false;
+                break;
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================= softmax of the tiles n % 2 == sid; thread = key, then thread = dim =================
+        const int sid = warp >> 2, r = tid & 127, wq = warp & 3, bid = 1 + sid;
+        const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+        const uint32_t tS = tmem + lane_off + SM::S_COL + sid * 64, tO = tmem + lane_off + SM::O_COL + sid * 64;
+        unsigned char *s_p = s + SM::P + sid * SM::PB;
+        float *s_red = reinterpret_cast<float *>(s_p), *s_f = s_red + 4 * NR;
+        float *ms = s_ms + sid * NR;
+        int *lims = s_lim + sid * NR;
+        const float sl2 = a.scale * 1.4426950408889634f;
+        uint32_t tiles = 0;
+        FwSeg g;
+        // A warp whose wait ran out says so and still comes to the barriers, and the warpgroup leaves together
+        while (true) {
+            if (!take(g)) s_bad[sid] = 1;
+            fw_bar(bid);
+            if (s_bad[sid]) {
+                ok = false;
+                break;
+            }
+            if (g.s.nr == 0) break;
+            const PfSeg &seg = g.s;
+            const int t0 = (sid ^ g.n0) & 1;
+            if (t0 >= seg.nt) continue;
+            const int min_lim = pf_min_limit(a, seg), nc = (seg.nr + 15) / 16;
+            if (r < seg.nr) {
+                lims[r] = pf_limit(a, seg, d, r);
+            } else if (r < NR) {
+                lims[r] = INT32_MAX;
+            }
+            if (r < NR) ms[r] = -INFINITY;
+            float l[NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) l[i] = 0.0f;
+            for (int t = t0; t < seg.nt; t += 2, ++tiles) {
+                const int n = g.n0 + t, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
+                bool good = pf_wait(bar(SM::kInfo + sid), tiles & 1u) && pf_wait(bar(SM::kSFull + sid), tiles & 1u);
+                tc::fence_after();
+                const int flags = s_flag[n % kFwFlags];
+                const bool edge = flags != 3 || base + kPfTile > min_lim;
+                if (edge && good) {
+                    good = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
+                    // a key behind the sequence's end weighs nothing, but 0 x NaN is NaN: its V row becomes zero
+                    if (good && base + r >= seg.len) {
+#pragma unroll
+                        for (int h = 0; h < SM::KH; ++h) {
+                            uint4 *row = reinterpret_cast<uint4 *>(s + SM::V + vs * SM::OP + h * 16384 + r * 128);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    __syncwarp();
+                }
+                const bool page_ok = (flags >> (r >> 6)) & 1;
+                float y[NR];
+                // y = logit * log2(e) - m, -inf where the row does not see the key; false where one is above 8
+                auto logits = [&]() {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < NR / 16; ++c) {
+                        if (c >= nc) break;
+                        float x[16];
+                        tc::tmem_ld16(tS + 16 * c, x);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 m4 = *reinterpret_cast<const float4 *>(ms + 16 * c + i);
+                            y[16 * c + i] = fmaf(x[i], sl2, -m4.x);
+                            y[16 * c + i + 1] = fmaf(x[i + 1], sl2, -m4.y);
+                            y[16 * c + i + 2] = fmaf(x[i + 2], sl2, -m4.z);
+                            y[16 * c + i + 3] = fmaf(x[i + 3], sl2, -m4.w);
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (!(page_ok && base + r < lims[16 * c + i])) y[16 * c + i] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) top = fmaxf(top, y[16 * c + i]);
+                    }
+                    return top <= 8.0f;
+                };
+                bool high = t == t0;  // the first tile sets the maxima
+                if (!high && good) high = !logits();
+                if (!good) s_bad[sid] = 1;
+                const bool any = fw_bar_or(bid, high);
+                if (s_bad[sid]) {
+                    ok = false;
+                    break;
+                }
+                // the O^T product before has read P^T, and O^T is at rest
+                if (tiles > 0) good = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);
+                if (any) {
+                    tc::fence_after();
+                    // maxima over the tile's keys, of logit * log2(e)
+#pragma unroll
+                    for (int c = 0; c < NR / 16; ++c) {
+                        if (c >= nc) break;
+                        float x[16];
+                        tc::tmem_ld16(tS + 16 * c, x);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const bool see = !edge || (page_ok && base + r < lims[16 * c + i]);
+                            const uint32_t u = __reduce_max_sync(0xffffffffu, float_to_ordered(see ? x[i] * sl2 : -INFINITY));
+                            if (lane == i) s_red[wq * NR + 16 * c + i] = ordered_to_float(u);
+                        }
+                    }
+                    fw_bar(bid);
+                    if (r < 16 * nc) {
+                        const float mx = fmaxf(fmaxf(s_red[r], s_red[NR + r]), fmaxf(s_red[2 * NR + r], s_red[3 * NR + r]));
+                        const float old = ms[r];
+                        const bool grow = mx - old > 8.0f;  // from -inf, too; not where nothing is visible yet (-inf, NaN)
+                        s_f[r] = grow ? ex2_approx(old - mx) : 1.0f;
+                        if (grow) ms[r] = mx;
+                    }
+                    fw_bar(bid);
+#pragma unroll
+                    for (int c = 0; c < NR / 16; ++c) {
+                        if (c >= nc) break;
+                        float f[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            f[i] = s_f[16 * c + i];
+                            l[16 * c + i] *= f[i];
+                        }
+                        if (t > t0) {
+                            float o[16];
+                            uint32_t u[16];
+                            tc::tmem_ld16(tO + 16 * c, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * f[i]);
+                            tc::tmem_st16(tO + 16 * c, u);
+                        }
+                    }
+                    logits();
+                    fw_bar(bid);  // the scratch has been read: P^T may go there
+                }
+#pragma unroll
+                for (int c = 0; c < NR / 16; ++c) {
+                    if (c >= nc) break;
+#pragma unroll
+                    for (int hv = 0; hv < 2; ++hv) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = 16 * c + 8 * hv + 2 * i;
+                            const float p0 = ex2_approx(y[e]), p1 = ex2_approx(y[e + 1]);
+                            l[e] += p0;
+                            l[e + 1] += p1;
+                            pk[i] = pack_bf16x2(p0, p1);
+                        }
+                        *reinterpret_cast<uint4 *>(s_p + tc::sw128(r, 2 * c + hv)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                }
+                tc::fence_proxy_async_smem();  // P^T, and V rows made zero
+                tc::fence_before();
+                tc::mbar_arrive(bar(SM::kPFull + sid));
+                if (!good) s_bad[sid] = 1;
+            }
+            if (!ok) break;
+            const bool good = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);
+            if (!good) s_bad[sid] = 1;
+            tc::fence_after();
+            const int64_t at = (int64_t)seg.part * (seg.b < 0 ? d.strideP : d.strideO) + (t0 == 0 ? 0 : seg.nr);
+            float *O = (seg.b < 0 ? w.Op : w.Oo) + at * D;
+#pragma unroll
+            for (int c = 0; c < NR / 16; ++c) {
+                if (c >= nc) break;
+                float o[16];
+                __syncwarp();
+                tc::tmem_ld16(tO + 16 * c, o);
+                if (r < D) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (16 * c + i < seg.nr) O[(size_t)(16 * c + i) * D + r] = o[i];
+                }
+                // the warp's sums of 16 rows: each step halves the rows a lane holds
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = l[16 * c + i];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+#pragma unroll
+                for (int h = 8; h > 0; h >>= 1) {
+                    const bool up = lane & h;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (i < h) {
+                            const float send = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+                            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, h);
+                        }
+                    }
+                }
+                if (lane < 16) s_red[wq * NR + 16 * c + lane] = v[0];
+            }
+            tc::fence_before();
+            tc::mbar_arrive(bar(SM::kOEmpty + sid));
+            fw_bar(bid);
+            if (r < seg.nr) {
+                const float sum = (s_red[r] + s_red[NR + r]) + (s_red[2 * NR + r] + s_red[3 * NR + r]);
+                reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at + r] = make_float2(ms[r], sum);
+            }
+        }
+    }
+    if (!ok) s_bad[2] = 1;
+    tc::fence_before();
+    __syncthreads();
+    if (follows) pdl_wait();  // the kernel before, whose partials the join reads, too
+    pdl_launch_dependents();
+    if (tid == 0) w.status[kPfCtas + blockIdx.x] = s_bad[0] | s_bad[1] | s_bad[2];
+    if (warp == kFwMmaWarp) {
+        tc::fence_after();
+        tc::tmem_dealloc(tmem, SM::TMEM_COLS);
+    }
+}
+
+template <int D, int NR>
+static cudaError_t launch_few(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
+                              bool follows, cudaStream_t s) {
+    CUtensorMap tk, tv;
+    const uint64_t rows = (uint64_t)a.num_pages * a.Hkv * kChunk;
+    if (!make_tmap_bf16(&tk, a.Kp, rows, D, kChunk) || !make_tmap_bf16(&tv, a.Vp, rows, D, kChunk))
+        return cudaErrorInvalidValue;
+    const size_t smem = FwSmem<D, NR>::dyn(d.blocks);
+    cudaError_t e = cudaFuncSetAttribute(prefix_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    HSA_PROF("prefix_few", s);
+    return launch_pdl(prefix_few_kernel<D, NR>, dim3(ctas), dim3(kFwThreads), smem, s, a, d, w, prefix, own, follows, tk, tv);
+}
+
+cudaError_t launch_prefix_few(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
+                              bool follows, cudaStream_t s) {
+    const int rows = prefix ? d.Rp : d.Ro;  // Rp >= Ro
+    if (a.D == 128)
+        return rows <= 16   ? launch_few<128, 16>(a, d, w, ctas, prefix, own, follows, s)
+               : rows <= 32 ? launch_few<128, 32>(a, d, w, ctas, prefix, own, follows, s)
+                            : launch_few<128, 64>(a, d, w, ctas, prefix, own, follows, s);
+    return rows <= 16   ? launch_few<64, 16>(a, d, w, ctas, prefix, own, follows, s)
+           : rows <= 32 ? launch_few<64, 32>(a, d, w, ctas, prefix, own, follows, s)
+                        : launch_few<64, 64>(a, d, w, ctas, prefix, own, follows, s);
+}
+
+}  // namespace hsa

@@ -5,12 +5,15 @@
 
 namespace hsa {
 
-// Joins a row's partials, one warp per row: M = max m_i, out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-constexpr int kPfJoinThreads = 256;
+// Joins a row's partials: M = max m_i, out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i. `wpr` warps of a block (1, 2, 4
+// or 8) share a row's partials, each with a maximum of its own, so that a few rows of many partials are not
+// read one after the other.
+constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const PrefixArgs a, const PfDims d, const PfWork w,
-                                                                     int ctas, bool wide, bool few) {
+                                                                     int ctas, bool wide, bool few, int wpr) {
+    __shared__ float s_acc[kPfJoinWarps][D], s_M[kPfJoinWarps], s_L[kPfJoinWarps];
     pdl_wait();
     const int lane = threadIdx.x & 31;
     if (blockIdx.x == 0 && threadIdx.x < 32) {
@@ -19,8 +22,9 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
         bad = __any_sync(0xffffffffu, bad != 0);
         if (lane == 0) *w.err = bad;
     }
-    const int64_t row = (int64_t)blockIdx.x * (kPfJoinThreads / 32) + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.B * a.H * a.Tq) return;
+    const int warp = threadIdx.x >> 5, wi = warp & (wpr - 1);
+    const int64_t rows = (int64_t)a.B * a.H * a.Tq;
+    const int64_t want = (int64_t)blockIdx.x * (kPfJoinWarps / wpr) + warp / wpr, row = min(want, rows - 1);
     const PfPlan p = *w.planP, po = *w.planO;
     const int b = (int)(row / ((int64_t)a.H * a.Tq)), hr_n = a.Hkv * d.Rgo;
     const int rem = (int)(row % ((int64_t)a.H * a.Tq)), h = rem / d.Ro, ro = rem % d.Ro;
@@ -76,7 +80,7 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
     };
     const float2 *mlp = reinterpret_cast<const float2 *>(w.mlp), *mlo = reinterpret_cast<const float2 *>(w.mlo);
     float M = -INFINITY;
-    for (int idx = lane; idx < total; idx += 32) {
+    for (int idx = wi + wpr * lane; idx < total; idx += 32 * wpr) {
         const int64_t at = place(idx);
         if (at >= 0) M = fmaxf(M, (idx < np * per ? mlp : mlo)[at].x);
     }
@@ -85,8 +89,8 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
     constexpr int V = D / 32;  // columns per lane
     float acc[V] = {}, L = 0.0f;
     if (M > -INFINITY) {
-        for (int base = 0; base < total; base += 32) {
-            const int idx = base + lane;
+        for (int base = wi; base < total; base += 32 * wpr) {
+            const int idx = base + wpr * lane;
             int64_t at = idx < total ? place(idx) : -1;
             float f = 0.0f;
             if (at >= 0) {
@@ -94,21 +98,21 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
                 f = ml.x > -INFINITY ? ex2_approx(ml.x - M) : 0.0f;
                 L = fmaf(ml.y, f, L);
             }
-            const int cnt = min(32, total - base);
-#pragma unroll 4
+            const float *src = at < 0 || f == 0.0f ? nullptr : (idx < np * per ? w.Op : w.Oo) + at * D;
+            const int cnt = min(32, (total - base + wpr - 1) / wpr);
+#pragma unroll 8
             for (int k = 0; k < cnt; ++k) {
                 const float fk = __shfl_sync(0xffffffffu, f, k);
-                const int64_t ak = __shfl_sync(0xffffffffu, (long long)at, k);
-                if (ak < 0) continue;
-                const float *O = (base + k < np * per ? w.Op : w.Oo) + ak * D + lane * V;
+                const float *O = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
+                if (!O) continue;
                 if constexpr (V == 4) {
-                    const float4 o = *reinterpret_cast<const float4 *>(O);
+                    const float4 o = *reinterpret_cast<const float4 *>(O + lane * V);
                     acc[0] = fmaf(fk, o.x, acc[0]);
                     acc[1] = fmaf(fk, o.y, acc[1]);
                     acc[2] = fmaf(fk, o.z, acc[2]);
                     acc[3] = fmaf(fk, o.w, acc[3]);
                 } else {
-                    const float2 o = *reinterpret_cast<const float2 *>(O);
+                    const float2 o = *reinterpret_cast<const float2 *>(O + lane * V);
                     acc[0] = fmaf(fk, o.x, acc[0]);
                     acc[1] = fmaf(fk, o.y, acc[1]);
                 }
@@ -116,6 +120,29 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
         }
         L = warp_sum(L);
     }
+    if (wpr > 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
+        if (lane == 0) {
+            s_M[warp] = M;
+            s_L[warp] = L;
+        }
+        __syncthreads();
+        if (wi > 0) return;
+        const float M0 = M;
+        for (int k = 1; k < wpr; ++k) M = fmaxf(M, s_M[warp + k]);
+        const float f0 = M0 > -INFINITY ? ex2_approx(M0 - M) : 0.0f;
+        L *= f0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] *= f0;
+        for (int k = 1; k < wpr; ++k) {
+            const float f = s_M[warp + k] > -INFINITY ? ex2_approx(s_M[warp + k] - M) : 0.0f;
+            L = fmaf(s_L[warp + k], f, L);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(s_acc[warp + k][lane * V + i], f, acc[i]);
+        }
+    }
+    if (want >= rows) return;
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     uint32_t *out = reinterpret_cast<uint32_t *>(a.out + row * D + lane * V);
 #pragma unroll
@@ -163,10 +190,13 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, cudaStream_t s) {
     if (e == cudaSuccess && few) e = launch_prefix_few(a, d, w, ctas, !wide, true, wide, s);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.B * a.H * a.Tq;
-    const unsigned grid = (unsigned)((rows + kPfJoinThreads / 32 - 1) / (kPfJoinThreads / 32));
+    int wpr = kPfJoinWarps;
+    while (wpr > 1 && rows * wpr > 16 * kPfCtas) wpr /= 2;  // about 16 warps per SM at most
+    const int per_block = kPfJoinWarps / wpr;
+    const unsigned grid = (unsigned)((rows + per_block - 1) / per_block);
     HSA_PROF("prefix_join", s);
-    return a.D == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wide, few)
-                      : launch_pdl(prefix_join_kernel<64>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wide, few);
+    return a.D == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wide, few, wpr)
+                      : launch_pdl(prefix_join_kernel<64>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wide, few, wpr);
 }
 
 }  // namespace hsa

@@ -22,7 +22,7 @@ constexpr int kPfFewRows = 64;    // segments of up to this many rows go to the 
 constexpr int kPfCtas = 148;      // at most: one per SM; the workspace is sized for it
 constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per head and row group)
 // Costs in half tiles: a tile, and what a segment's start and end take beside its tiles
-constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 1;
+constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 2;
 
 // The division of one kernel's work; every CTA computes the same, CTA 0 stores it for the join.
 //   prefix: per key head and row group, `nsplit` runs of `run` tiles; segment i goes to CTA i % ctas, the row
@@ -80,6 +80,11 @@ __device__ __forceinline__ int pf_weight(int64_t n) { return n > 0 ? kPfTileCost
 // Tile boundary of a place on a stretch: 0 at its start, the number of tiles at its end, never decreasing.
 __device__ __forceinline__ int pf_tile_at(int64_t at) { return (int)(max(at - kPfOwnCost + kPfTileCost - 1, (int64_t)0) / kPfTileCost); }
 
+// a / b for a >= 0, b > 0, in 32 bits where they suffice (a 64-bit division takes several times as long)
+__device__ __forceinline__ int64_t pf_div(int64_t a, int b) {
+    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 struct PfSeg {
     int h, b;            // key head; request (own segments; -1: prefix)
     int r0, nr;          // its rows among the key head's (prefix) or the request's (own)
@@ -131,7 +136,7 @@ struct PfWalk {
         }
         const int hr_n = a.Hkv * d.Rgo;
         while (x < end) {
-            const int xw = (int)(x / hr_n);  // on the axis of the requests' weights alone
+            const int xw = (int)pf_div(x, hr_n);  // on the axis of the requests' weights alone
             int lo = 0, hi = d.blocks;       // the block that holds it (blocks of no weight are passed over)
             while (hi - lo > 1) {
                 const int m = (lo + hi) >> 1;
@@ -144,7 +149,7 @@ struct PfWalk {
             const int w = __shfl_sync(0xffffffffu, weight, l);
             const int64_t rest = x - (int64_t)__shfl_sync(0xffffffffu, before, l) * hr_n;
             s.len = __shfl_sync(0xffffffffu, len, l);
-            const int hr = (int)(rest / w), from = (int)(rest - (int64_t)hr * w);
+            const int hr = (int)pf_div(rest, w), from = (int)(rest - (int64_t)hr * w);
             const int to = (int)min((int64_t)w, from + (end - x));
             x += to - from;
             const int t0 = pf_tile_at(from), t1 = pf_tile_at(to);
@@ -222,12 +227,12 @@ __device__ void pf_schedule(const PrefixArgs &a, const PfDims &d, bool prefix, b
             // a number of runs per lane: 1 .. 16, and what fills 1/4 .. 4 waves; the one that ends the work soonest,
             // both kinds of it counted (fewer runs win a tie)
             const int ns_max = min(max(kPfItems / units, 1), tiles);
-            const int want = lane < 16 ? lane + 1 : (int)((int64_t)(lane - 15) * ctas / 4 / units);
+            const int want = lane < 16 ? lane + 1 : (lane - 15) * ctas / 4 / units;
             const int ns = min(max(want, 1), ns_max);
             const int run = (tiles + ns - 1) / ns, items = units * ((tiles + run - 1) / run);
             const int cost = kPfTileCost * run + kPfPrefixCost;
             const int64_t waves = (int64_t)((items + ctas - 1) / ctas) * cost;
-            const int64_t even = ((int64_t)items * cost + axis + ctas - 1) / ctas;
+            const int64_t even = pf_div((int64_t)items * cost + axis + ctas - 1, ctas);
             long long key = max(waves, even) * 1024 + ns;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
@@ -240,12 +245,12 @@ __device__ void pf_schedule(const PrefixArgs &a, const PfDims &d, bool prefix, b
         p.lo_ctas = p.items % ctas;
         const int64_t pc_hi = p.items / ctas * cost, pc_lo = pc_hi + cost;
         const int hi_ctas = ctas - p.lo_ctas;
-        const int64_t alone = (axis + hi_ctas - 1) / hi_ctas;
+        const int64_t alone = pf_div(axis + hi_ctas - 1, hi_ctas);
         if (pc_hi + alone <= pc_lo) {  // the CTAs with a prefix segment less take all of it
             p.cap_lo = 0;
             p.cap_hi = alone;
         } else {
-            const int64_t share = (axis + p.lo_ctas * pc_lo + hi_ctas * pc_hi + ctas - 1) / ctas;
+            const int64_t share = pf_div(axis + p.lo_ctas * pc_lo + hi_ctas * pc_hi + ctas - 1, ctas);
             p.cap_lo = share - pc_lo;
             p.cap_hi = share - pc_hi;
         }

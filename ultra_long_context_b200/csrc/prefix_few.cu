@@ -5,9 +5,11 @@
 // part of an MMA or of the softmax is spent on padding rows:
 //   S^T = K Q^T    (128 keys x N, fp32 in TMEM; thread = key)       P^T = exp2(S^T scale' - m) (bf16, to shared memory)
 //   O^T += V^T P^T (D x N, fp32 in TMEM; thread = dim)
-// A row's maximum m is that of the first tile and moves only when a later logit exceeds it by more than 2^8 (P stays
-// in a comfortable range up to there, and the final quotient cancels m); then, and in a segment's first tile,
-// the warpgroup reduces the maxima over the keys and rescales O^T in TMEM. Every other tile costs a thread N
+// The reference m of a row need not be its maximum: the final quotient cancels it, and P (bf16) and the fp32 sums keep
+// their relative precision as long as nothing leaves their range. So m is the logit of the first key that the row sees
+// in the segment, and moves only when a later one exceeds it by more than 2^64 (sums of 2^64 over 2^30 keys, times
+// V, stay far below 2^127; what is 2^126 below m is less than 2^-126 of the sum, which is at least 1). Then the
+// warpgroup reduces the maxima over the keys and rescales O^T in TMEM; every other tile costs a thread N
 // exponentials and one barrier with a vote. Row sums stay per thread until the segment ends.
 //
 // Persistent, warp-specialised, one CTA per SM; the CTA's tiles are numbered through all its segments:
@@ -25,6 +27,7 @@ namespace hsa {
 
 constexpr int kFwMmaWarp = 8, kFwTmaWarp = 9, kFwQWarp = 10;
 constexpr int kFwThreads = 32 * (kFwQWarp + 1);
+constexpr float kFwGrow = 64.0f;
 constexpr int kFwRing = 4;    // announced segments
 constexpr int kFwFlags = 8;   // tiles whose page flags are kept (copies run at most KS tiles ahead of S^T)
 
@@ -51,7 +54,8 @@ struct FwSmem {
     static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;
     static constexpr uint32_t MS = RING + kFwRing * sizeof(FwSeg);        // float[2][NR]: m * scale * log2(e), or -inf
     static constexpr uint32_t LIM = MS + 2 * NR * 4;                      // int[2][NR]
-    static constexpr uint32_t FLAG = LIM + 2 * NR * 4;                    // int[kFwFlags]
+    static constexpr uint32_t SUM = LIM + 2 * NR * 4;                     // float[2][4][NR]: row sums of a warp's keys
+    static constexpr uint32_t FLAG = SUM + 8 * NR * 4;                    // int[kFwFlags]
     static constexpr uint32_t MISC = FLAG + 4 * kFwFlags;                 // TMEM base, bad[2], -
     static constexpr uint32_t PLAN = (MISC + 16 + 15) / 16 * 16;
     static constexpr uint32_t BCUM = PLAN + (sizeof(PfPlan) + 15) / 16 * 16;  // int[blocks + 1]
@@ -251,32 +255,42 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         uint32_t k_par = 0, v_par = 0, idle = 0;
         while (true) {
             bool progress = false;
-            if (!have && !end) {
-                const int slot = seg_no % kFwRing;
-                if (pf_done(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kFwRing) & 1u)) {
-                    q = seg_no & 1;
-                    quse = (uint32_t)(seg_no >> 1);
-                    take(g);
-                    have = g.s.nr > 0;
-                    end = !have;
-                    t = 0;
-                    progress = true;
-                }
+            // one probe per lane: the next segment, fillings, P^T and free O^T of both streams, in one round
+            const int slot = seg_no % kFwRing;
+            int b = SM::kSegFull + slot;
+            uint32_t par = (uint32_t)(seg_no / kFwRing);
+            if (lane == 1) b = SM::kKFull + k_slot, par = k_par;
+            if (lane == 2) b = SM::kVFull + v_slot, par = v_par;
+            if (lane == 3) b = SM::kQFull + q, par = quse;
+            if (lane == 4) b = SM::kPFull, par = tiles[0];
+            if (lane == 5) b = SM::kPFull + 1, par = tiles[1];
+            if (lane == 6) b = SM::kOEmpty, par = runs[0];
+            if (lane == 7) b = SM::kOEmpty + 1, par = runs[1];
+            const unsigned hit = __ballot_sync(0xffffffffu, lane < 8 && tc::mbar_test(bar(b), par & 1u));
+            __syncwarp();  // what the probing lanes acquired holds for the issuing one
+            if (!have && !end && (hit & 1u)) {
+                q = seg_no & 1;
+                quse = (uint32_t)(seg_no >> 1);
+                take(g);
+                have = g.s.nr > 0;
+                end = !have;
+                t = 0;
+                progress = true;
             }
             if (end && next_o == next_s) break;
-            if (pf_done(bar(SM::kKFull + k_slot), k_par)) {
+            if (hit & 2u) {
                 ++k_seen;
                 if (++k_slot == KS) k_slot = 0, k_par ^= 1u;
             }
-            if (pf_done(bar(SM::kVFull + v_slot), v_par)) {
+            if (hit & 4u) {
                 ++v_seen;
                 if (++v_slot == VS) v_slot = 0, v_par ^= 1u;
             }
 #pragma unroll
             for (int sid = 0; sid < 2; ++sid) {  // O^T(next_o)
                 if (next_o >= next_s || (next_o & 1) != sid || next_o >= v_seen) continue;
-                if (!pf_done(bar(SM::kPFull + sid), tiles[sid] & 1u)) continue;
-                if (first[sid] && runs[sid] > 1 && !pf_done(bar(SM::kOEmpty + sid), (runs[sid] - 2) & 1u)) continue;
+                if (!(hit & (16u << sid))) continue;
+                if (first[sid] && runs[sid] > 1 && !(hit & (64u << sid))) continue;
                 tc::fence_after();
                 const int vs = next_o % VS;
                 const uint32_t sv = sb + SM::V + vs * SM::OP, sp = sb + SM::P + sid * SM::PB;
@@ -293,10 +307,12 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 ++next_o;
                 progress = true;
             }
+            // Q of the segment, if the probe was of it (a segment taken just now is asked for in the next round)
+            const bool q_in = (hit & 8u) && !progress;
             // S^T(next_s): its buffer is free once P^T of the tile two before is written. The V filling before this
             // tile's in its slot has landed, so that a softmax wait on the slot's parity, which follows S^T, is exact
             if (have && next_s < next_o + 2 && next_s < k_seen && next_s - VS < v_seen &&
-                (t > 0 || pf_done(bar(SM::kQFull + q), quse & 1u))) {
+                (t > 0 || q_in)) {
                 tc::fence_after();
                 tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
                 const int ks = next_s % KS;
@@ -341,7 +357,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         const uint32_t tS = tmem + lane_off + SM::S_COL + sid * 64, tO = tmem + lane_off + SM::O_COL + sid * 64;
         unsigned char *s_p = s + SM::P + sid * SM::PB;
         float *s_red = reinterpret_cast<float *>(s_p), *s_f = s_red + 4 * NR;
-        float *ms = s_ms + sid * NR;
+        float *ms = s_ms + sid * NR, *s_sum = reinterpret_cast<float *>(s + SM::SUM) + sid * 4 * NR;
         int *lims = s_lim + sid * NR;
         const float sl2 = a.scale * 1.4426950408889634f;
         uint32_t tiles = 0;
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             } else if (r < NR) {
                 lims[r] = INT32_MAX;
             }
-            if (r < NR) ms[r] = -INFINITY;
+            fw_bar(bid);
             float l[NR];
 #pragma unroll
             for (int i = 0; i < NR; ++i) l[i] = 0.0f;
@@ -389,7 +405,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 }
                 const bool page_ok = (flags >> (r >> 6)) & 1;
                 float y[NR];
-                // y = logit * log2(e) - m, -inf where the row does not see the key; false where one is above 8
+                // y = logit * log2(e) - m, -inf where the row does not see the key; false where one is too far above m
                 auto logits = [&]() {
                     float top = -INFINITY;
 #pragma unroll
@@ -413,11 +429,29 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
 #pragma unroll
                         for (int i = 0; i < 16; ++i) top = fmaxf(top, y[16 * c + i]);
                     }
-                    return top <= 8.0f;
+                    return top <= kFwGrow;
                 };
-                bool high = t == t0;  // the first tile sets the maxima
-                if (!high && good) high = !logits();
-                if (!good) s_bad[sid] = 1;
+                if (t == t0) {  // the references: the first key, or the 65th where the first page is bad
+                    const int lead = flags & 1 ? 0 : 64;
+                    if (r >> 5 == lead >> 5 && good) {
+#pragma unroll
+                        for (int c = 0; c < NR / 16; ++c) {
+                            if (c >= nc) break;
+                            float x[16];
+                            __syncwarp();
+                            tc::tmem_ld16(tS + 16 * c, x);
+                            if (lane == 0) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    ms[16 * c + i] = page_ok && base + lead < lims[16 * c + i] ? x[i] * sl2 : -INFINITY;
+                            }
+                        }
+                    }
+                    fw_bar(bid);
+                }
+                bool high = false;
+                if (good) high = !logits();
+                else s_bad[sid] = 1;
                 const bool any = fw_bar_or(bid, high);
                 if (s_bad[sid]) {
                     ok = false;
@@ -444,7 +478,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     if (r < 16 * nc) {
                         const float mx = fmaxf(fmaxf(s_red[r], s_red[NR + r]), fmaxf(s_red[2 * NR + r], s_red[3 * NR + r]));
                         const float old = ms[r];
-                        const bool grow = mx - old > 8.0f;  // from -inf, too; not where nothing is visible yet (-inf, NaN)
+                        const bool grow = mx - old > kFwGrow;  // from -inf, too; not where nothing is visible yet (-inf, NaN)
                         s_f[r] = grow ? ex2_approx(old - mx) : 1.0f;
                         if (grow) ms[r] = mx;
                     }
@@ -493,28 +527,13 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 if (!good) s_bad[sid] = 1;
             }
             if (!ok) break;
-            const bool good = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);
-            if (!good) s_bad[sid] = 1;
-            tc::fence_after();
-            const int64_t at = (int64_t)seg.part * (seg.b < 0 ? d.strideP : d.strideO) + (t0 == 0 ? 0 : seg.nr);
-            float *O = (seg.b < 0 ? w.Op : w.Oo) + at * D;
+            // the warp's row sums: each step halves the rows a lane holds
 #pragma unroll
             for (int c = 0; c < NR / 16; ++c) {
                 if (c >= nc) break;
-                float o[16];
-                __syncwarp();
-                tc::tmem_ld16(tO + 16 * c, o);
-                if (r < D) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (16 * c + i < seg.nr) O[(size_t)(16 * c + i) * D + r] = o[i];
-                }
-                // the warp's sums of 16 rows: each step halves the rows a lane holds
                 float v[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = l[16 * c + i];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+                for (int i = 0; i < 16; ++i) v[i] = l[16 * c + i] + __shfl_xor_sync(0xffffffffu, l[16 * c + i], 16);
 #pragma unroll
                 for (int h = 8; h > 0; h >>= 1) {
                     const bool up = lane & h;
@@ -526,15 +545,31 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                         }
                     }
                 }
-                if (lane < 16) s_red[wq * NR + 16 * c + lane] = v[0];
+                if (lane < 16) s_sum[wq * NR + 16 * c + lane] = v[0];
+            }
+            const int64_t at = (int64_t)seg.part * (seg.b < 0 ? d.strideP : d.strideO) + (t0 == 0 ? 0 : seg.nr);
+            float *O = (seg.b < 0 ? w.Op : w.Oo) + at * D;
+            fw_bar(bid);
+            if (r < seg.nr) {
+                const float sum = (s_sum[r] + s_sum[NR + r]) + (s_sum[2 * NR + r] + s_sum[3 * NR + r]);
+                reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at + r] = make_float2(ms[r], sum);
+            }
+            if (!pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u)) s_bad[sid] = 1;  // seen at the next barrier
+            tc::fence_after();
+#pragma unroll
+            for (int c = 0; c < NR / 16; ++c) {
+                if (c >= nc) break;
+                float o[16];
+                __syncwarp();
+                tc::tmem_ld16(tO + 16 * c, o);
+                if (r < D) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (16 * c + i < seg.nr) O[(size_t)(16 * c + i) * D + r] = o[i];
+                }
             }
             tc::fence_before();
             tc::mbar_arrive(bar(SM::kOEmpty + sid));
-            fw_bar(bid);
-            if (r < seg.nr) {
-                const float sum = (s_red[r] + s_red[NR + r]) + (s_red[2 * NR + r] + s_red[3 * NR + r]);
-                reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at + r] = make_float2(ms[r], sum);
-            }
         }
     }
     if (!ok) s_bad[2] = 1;

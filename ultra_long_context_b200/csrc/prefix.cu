@@ -14,6 +14,7 @@ template <int D>
 __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const PrefixArgs a, const PfDims d, const PfWork w,
                                                                      int ctas, bool wide, bool few, int wpr) {
     __shared__ float s_acc[kPfJoinWarps][D], s_M[kPfJoinWarps], s_L[kPfJoinWarps];
+    pdl_launch_dependents();  // what follows may set itself up; it waits for this grid's end before it reads
     pdl_wait();
     const int lane = threadIdx.x & 31;
     if (blockIdx.x == 0 && threadIdx.x < 32) {
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
             const int k = idx / per, st = idx - k * per;
             const int nt = min(p.run, p.tiles - k * p.run);
             if (st >= nt) return -1;
-            return (int64_t)((h * p.nsplit + k) * d.Rgp + rg) * d.strideP + st * nr + rr;
+            return (int64_t)((k * a.Hkv + h) * d.Rgp + rg) * d.strideP + st * nr + rr;
         }
         const int i = i0 + (idx - np * per) / 2, st = (idx - np * per) & 1;
         const int nt = pf_tile_at(min(po.start(i + 1), x0 + wt) - x0) - pf_tile_at(max(po.start(i), x0) - x0);

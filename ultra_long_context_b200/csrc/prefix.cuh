@@ -25,8 +25,9 @@ constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per he
 constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 2;
 
 // The division of one kernel's work; every CTA computes the same, CTA 0 stores it for the join.
-//   prefix: per key head and row group, `nsplit` runs of `run` tiles; segment i goes to CTA i % ctas, the row
-//   groups of one run next to each other (they read the same keys at about the same time, through L2);
+//   prefix: per key head and row group (a unit), `nsplit` runs of `run` tiles; segment i = run i / units of unit
+//   i % units goes to CTA i % ctas, so that the row groups of one run, which read the same keys, do so at about the
+//   same time, through L2;
 //   own: the stretches of all (request, key head, row group), weight = cost of their tiles + kPfOwnCost each, laid
 //   end to end on an axis, and the axis cut into one interval per CTA such that prefix and own work
 //   add up evenly: the first `lo_ctas` CTAs, which have one prefix segment more, get `cap_lo`, the others `cap_hi`.
@@ -121,10 +122,10 @@ struct PfWalk {
     }
     __device__ bool next(PfSeg &s) {
         if (item < p.items) {
-            const int rg = item % d.Rgp, k = item / d.Rgp % p.nsplit;
-            s.h = item / d.Rgp / p.nsplit;
+            const int units = a.Hkv * d.Rgp, k = item / units, u = item - k * units;
+            s.h = d.Rgp == 1 ? u : u / d.Rgp;
             s.b = -1;
-            s.r0 = rg * kPfRows;
+            s.r0 = (u - s.h * d.Rgp) * kPfRows;
             s.nr = min(kPfRows, d.Rp - s.r0);
             s.tile0 = k * p.run;
             s.nt = min(p.run, p.tiles - s.tile0);
@@ -225,25 +226,25 @@ __device__ void pf_schedule(const PrefixArgs &a, const PfDims &d, bool prefix, b
         p.nsplit = 1;
         if (tiles > 0) {
             // a number of runs per lane: 1 .. 16, and what fills 1/4 .. 4 waves; the one that ends the work soonest,
-            // both kinds of it counted (fewer runs win a tie)
+            // both kinds of it counted (fewer runs win a tie). An estimate: in floats, whose quotients are quick
             const int ns_max = min(max(kPfItems / units, 1), tiles);
-            const int want = lane < 16 ? lane + 1 : (lane - 15) * ctas / 4 / units;
-            const int ns = min(max(want, 1), ns_max);
-            const int run = (tiles + ns - 1) / ns, items = units * ((tiles + run - 1) / run);
-            const int cost = kPfTileCost * run + kPfPrefixCost;
-            const int64_t waves = (int64_t)((items + ctas - 1) / ctas) * cost;
-            const int64_t even = pf_div((int64_t)items * cost + axis + ctas - 1, ctas);
-            long long key = max(waves, even) * 1024 + ns;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
-            const int best = (int)(key & 1023);
+            const float quarter = (float)ctas * 0.25f / (float)units;
+            const int ns = min(max(lane < 16 ? lane + 1 : (int)((float)(lane - 15) * quarter), 1), ns_max);
+            const float run = ceilf(__fdividef((float)tiles, (float)ns) - 1e-3f), cost = kPfTileCost * run + kPfPrefixCost;
+            const float items = (float)units * ceilf(__fdividef((float)tiles, run) - 1e-3f);
+            const float waves = ceilf(__fdividef(items, (float)ctas) - 1e-3f) * cost;
+            const float even = __fdividef(items * cost + (float)axis, (float)ctas);
+            // costs are positive, so their bits order as they do; the last five say whose it is
+            const uint32_t key = __reduce_min_sync(0xffffffffu, (__float_as_uint(fmaxf(waves, even)) & ~31u) | (uint32_t)lane);
+            const int best = __shfl_sync(0xffffffffu, ns, (int)(key & 31u));
             p.run = (tiles + best - 1) / best;
             p.nsplit = (tiles + p.run - 1) / p.run;
             p.items = units * p.nsplit;
         }
         const int64_t cost = kPfTileCost * p.run + kPfPrefixCost;
-        p.lo_ctas = p.items % ctas;
-        const int64_t pc_hi = p.items / ctas * cost, pc_lo = pc_hi + cost;
+        const int waves = p.items / ctas;
+        p.lo_ctas = p.items - waves * ctas;
+        const int64_t pc_hi = waves * cost, pc_lo = pc_hi + cost;
         const int hi_ctas = ctas - p.lo_ctas;
         const int64_t alone = pf_div(axis + hi_ctas - 1, hi_ctas);
         if (pc_hi + alone <= pc_lo) {  // the CTAs with a prefix segment less take all of it
@@ -267,6 +268,10 @@ __device__ void pf_publish(const PfDims &d, bool prefix, bool own, const PfPlan 
         for (int k = threadIdx.x; k <= d.blocks; k += NT) w.bcum[k] = bcum[k];
     if (threadIdx.x == 0 && prefix) *w.planP = *plan;
     if (threadIdx.x == 0 && own) *w.planO = *plan;
+}
+
+__device__ __forceinline__ void pf_prefetch_tmap(const CUtensorMap *m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
 // A bounded wait of a whole warp, with one answer for all lanes: the warp is converged behind it, which the

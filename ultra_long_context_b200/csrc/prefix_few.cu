@@ -105,6 +105,10 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == kFwMmaWarp) tc::tmem_alloc(sb + SM::MISC, SM::TMEM_COLS);
+    if (warp == kFwTmaWarp && lane == 0) {
+        pf_prefetch_tmap(&tmK);
+        pf_prefetch_tmap(&tmV);
+    }
     if (tid == 0) {
         s_bad[0] = s_bad[1] = s_bad[2] = 0;
         for (int i = 0; i < KS; ++i) {

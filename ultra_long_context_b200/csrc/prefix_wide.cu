@@ -68,6 +68,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == kPfMmaWarp) tc::tmem_alloc(sb + SM::TMEM, SM::TMEM_COLS);
+    if (warp == kPfTmaWarp && lane == 0) {
+        pf_prefetch_tmap(&tmK);
+        pf_prefetch_tmap(&tmV);
+    }
     if (tid == 0) {
         *s_bad = 0;
         for (int i = 0; i < KS; ++i) {

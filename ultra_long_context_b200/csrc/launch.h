@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace hsa {
 
 struct DecodeArgs {
@@ -172,6 +174,22 @@ cudaError_t launch_chunk_offsets(const int32_t *cu, int B, int32_t *cuN, cudaStr
 // with `fill` (the rows no kernel reads are left alone otherwise).
 cudaError_t launch_varlen_rows(const void *src, void *dst, const int32_t *cu, int B, int Hs, int Tp, int row_bytes,
                                bool pack, bool fill_pad, uint32_t fill, cudaStream_t s);
+
+// The current device's number of SMs, and a kernel's dynamic shared memory limit raised to `bytes`, asked of the
+// driver once per device (and kernel): a serving step's small launches are bound by the host.
+int sm_count();
+template <auto Kern>
+cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<int> granted[64];  // of this kernel, per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && granted[dev].load(std::memory_order_relaxed) >= (int)bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && known) granted[dev].store((int)bytes, std::memory_order_relaxed);
+    return e;
+}
 
 // Paged cache (page.cu). Pages of kChunk tokens; arguments as in include/hsa.h.
 struct PagePlanArgs {

@@ -20,6 +20,18 @@
 
 namespace hsa {
 
+int sm_count() {
+    static std::atomic<int> counts[64];
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess) return sms;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && (sms = counts[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    sms = 148;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && known)
+        counts[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
+
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanMaxCtas = 8;  // a portable cluster
@@ -189,7 +201,7 @@ size_t page_plan_smem(int B) { return (size_t)B * (sizeof(int64_t) + 3 * sizeof(
 
 cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t s) {
     const size_t smem = page_plan_smem(a.B);
-    cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<page_plan_kernel>(smem);
     if (e != cudaSuccess) return e;
     int ctas = 1;
     while (ctas < kPlanMaxCtas && (int64_t)ctas * 4 * kPlanThreads < (int64_t)a.max_tokens + a.B) ctas *= 2;
@@ -235,8 +247,7 @@ cudaError_t launch_page_append(const uint16_t *K, int64_t k_stride, const uint16
     if (n <= 0) return cudaSuccess;
     const int vpr = D / 8, vpt = Hkv * vpr;
     const int64_t vecs = (int64_t)n * vpt;
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int sms = sm_count();
     const int64_t want = (vecs + kAppendThreads - 1) / kAppendThreads;
     const unsigned grid = (unsigned)(want < (int64_t)sms * 8 ? want : (int64_t)sms * 8);
     HSA_PROF("page_append", s);

@@ -181,9 +181,7 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, cudaStream_t s) {
     const PfDims d(a.B, a.H, a.Hkv, a.Tq, a.max_prefix_pages);
     PfWork w{};
     pf_layout(a.workspace, d, a.D, &w);
-    int dev = 0, sms = kPfCtas;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int ctas = sms < kPfCtas ? sms : kPfCtas;
+    const int sms = sm_count(), ctas = sms < kPfCtas ? sms : kPfCtas;
     // rows of the prefix's segments (Rp) and of the requests' own (Ro <= Rp): few or many
     const bool wide = d.Rp > kPfFewRows, few = d.Ro <= kPfFewRows;
     cudaError_t e = cudaSuccess;

@@ -596,7 +596,7 @@ static cudaError_t launch_few(const PrefixArgs &a, const PfDims &d, const PfWork
     if (!make_tmap_bf16(&tk, a.Kp, rows, D, kChunk) || !make_tmap_bf16(&tv, a.Vp, rows, D, kChunk))
         return cudaErrorInvalidValue;
     const size_t smem = FwSmem<D, NR>::dyn(d.blocks);
-    cudaError_t e = cudaFuncSetAttribute(prefix_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<prefix_few_kernel<D, NR>>(smem);
     if (e != cudaSuccess) return e;
     HSA_PROF("prefix_few", s);
     return launch_pdl(prefix_few_kernel<D, NR>, dim3(ctas), dim3(kFwThreads), smem, s, a, d, w, prefix, own, follows, tk, tv);

@@ -456,7 +456,7 @@ static cudaError_t launch_wide(const PrefixArgs &a, const PfDims &d, const PfWor
     if (!make_tmap_bf16(&tk, a.Kp, rows, D, kChunk) || !make_tmap_bf16(&tv, a.Vp, rows, D, kChunk))
         return cudaErrorInvalidValue;
     const size_t smem = PfSmem<D>::dyn(d.blocks);
-    cudaError_t e = cudaFuncSetAttribute(prefix_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<prefix_wide_kernel<D>>(smem);
     if (e != cudaSuccess) return e;
     HSA_PROF("prefix_wide", s);
     return launch_pdl(prefix_wide_kernel<D>, dim3(ctas), dim3(kPfThreads), smem, s, a, d, w, prefix, own, tk, tv);

@@ -399,9 +399,35 @@ def hsa_backward_varlen(Q, K, V, L, out, dout, sel_idx, sel_w, cu_seqlens, max_s
     return (dQ, dK, dV, dL) if Qs is None else (dQ, dK, dV, dL, dQs)
 
 
-def _on(dev, stream):
-    """The call's device and stream made current, so that what it allocates belongs to that stream."""
-    return torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)
+# ---- paged cache ----
+# A serving step calls these once per layer, on batches whose kernels take a few microseconds: the marshalling
+# below is kept to what a call needs (plain integers for pointers, no context manager where the device is current).
+_BF16, _F32, _I32, _I64T = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(dev, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _elsewhere(dev, stream):
+    """The context that the call has to be made in, so that what it allocates belongs to its device and stream;
+    None if that is the present one."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return None
+
+
+def _fits(t, name, dtype, shape, dev):
+    """As _need, quick where nothing is wrong."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+        _need(t, name, dtype, shape, dev)
 
 
 def hsa_page_plan(cache_len, new_len, block_table, free_pages, pool, max_tokens, cu_new=None, slots=None,
@@ -414,28 +440,39 @@ def hsa_page_plan(cache_len, new_len, block_table, free_pages, pool, max_tokens,
     cache_len itself. Returns (cu_new [B + 1] int32, slots [max_tokens] int64, total_len [B] int64); the
     number of refused requests is in pool[2] (pool_out[2])."""
     dev = cache_len.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return hsa_page_plan(cache_len, new_len, block_table, free_pages, pool, max_tokens, cu_new, slots, total_len,
+                                 pool_out)
     B, width = block_table.shape
-    pool_out = pool if pool_out is None else pool_out
-    with _on(dev, stream):
-        if cu_new is None:
-            cu_new = torch.empty((B + 1,), dtype=torch.int32, device=dev)
-        if slots is None:
-            slots = torch.empty((max_tokens,), dtype=torch.int64, device=dev)
-        if total_len is None:
-            total_len = torch.empty((B,), dtype=torch.int64, device=dev)
-        _need(cache_len, "cache_len", torch.int64, (B,), dev)
-        _need(new_len, "new_len", torch.int32, (B,), dev)
-        _need(block_table, "block_table", torch.int32, (B, width), dev)
-        _need(free_pages, "free_pages", torch.int32, (free_pages.numel(),), dev)
-        _need(pool, "pool", torch.int64, (3,), dev)
-        _need(pool_out, "pool_out", torch.int64, (3,), dev)
-        _need(cu_new, "cu_new", torch.int32, (B + 1,), dev)
-        _need(slots, "slots", torch.int64, (max_tokens,), dev)
-        _need(total_len, "total_len", torch.int64, (B,), dev)
-        st = lib().hsa_page_plan(_ptr(cache_len), _ptr(new_len), B, _ptr(block_table), width, _ptr(free_pages),
-                                 free_pages.numel(), _ptr(pool), _ptr(pool_out), _ptr(total_len), _ptr(cu_new),
-                                 _ptr(slots) if max_tokens else None, max_tokens, _stream(dev, stream))
-    _check("hsa_page_plan", st)
+    num_free = free_pages.numel()
+    if pool_out is None:
+        pool_out = pool
+    _fits(cache_len, "cache_len", _I64T, (B,), dev)
+    _fits(new_len, "new_len", _I32, (B,), dev)
+    _fits(block_table, "block_table", _I32, (B, width), dev)
+    _fits(free_pages, "free_pages", _I32, (num_free,), dev)
+    _fits(pool, "pool", _I64T, (3,), dev)
+    if pool_out is not pool:
+        _fits(pool_out, "pool_out", _I64T, (3,), dev)
+    if cu_new is None:
+        cu_new = torch.empty(B + 1, dtype=_I32, device=dev)
+    else:
+        _fits(cu_new, "cu_new", _I32, (B + 1,), dev)
+    if slots is None:
+        slots = torch.empty(max_tokens, dtype=_I64T, device=dev)
+    else:
+        _fits(slots, "slots", _I64T, (max_tokens,), dev)
+    if total_len is None:
+        total_len = torch.empty_like(cache_len)
+    else:
+        _fits(total_len, "total_len", _I64T, (B,), dev)
+    st = lib().hsa_page_plan(cache_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(), width,
+                             free_pages.data_ptr(), num_free, pool.data_ptr(), pool_out.data_ptr(), total_len.data_ptr(),
+                             cu_new.data_ptr(), slots.data_ptr(), max_tokens, _stream_of(dev, None))
+    if st:
+        _check("hsa_page_plan", st)
     return cu_new, slots, total_len
 
 
@@ -443,14 +480,15 @@ def _rows(t, name, dev):
     """[n, Hkv, D] bf16 rows whose heads are contiguous; returns the distance between tokens in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
     n, heads, D = t.shape
-    if n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+    step, head, one = t.stride()
+    if n and (one != 1 or (heads > 1 and head != D)):
         raise ValueError(f"{name} must hold each token's heads contiguously")
-    return t.stride(0) if n > 1 else heads * D
+    return step if n > 1 else heads * D
 
 
 def hsa_page_append(K, V, slots, Kp, Vp, stream=None):
@@ -458,23 +496,27 @@ def hsa_page_append(K, V, slots, Kp, Vp, stream=None):
     contiguous (slices of a fused projection are taken as they are); slots [n] int64 (a row whose slot is
     outside the pool is skipped); Kp, Vp [num_pages, Hkv, 64, D] bf16, updated in place and returned."""
     dev = Kp.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return hsa_page_append(K, V, slots, Kp, Vp)
     n, Hkv, D = K.shape
     pages = Kp.shape[0]
     ks, vs = _rows(K, "K", dev), _rows(V, "V", dev)
-    if tuple(V.shape) != (n, Hkv, D):
+    if V.shape != K.shape:
         raise ValueError(f"V must have shape {(n, Hkv, D)}, got {tuple(V.shape)}")
-    _need(slots, "slots", torch.int64, (n,), dev)
-    _need(Kp, "Kp", torch.bfloat16, (pages, Hkv, 64, D), dev)
-    _need(Vp, "Vp", torch.bfloat16, (pages, Hkv, 64, D), dev)
-    with _on(dev, stream):
-        st = lib().hsa_page_append(_ptr(K), ks, _ptr(V), vs, _ptr(slots), n, Hkv, D, 64, _ptr(Kp), _ptr(Vp), pages,
-                                   _stream(dev, stream))
-    _check("hsa_page_append", st)
+    _fits(slots, "slots", _I64T, (n,), dev)
+    _fits(Kp, "Kp", _BF16, (pages, Hkv, 64, D), dev)
+    _fits(Vp, "Vp", _BF16, (pages, Hkv, 64, D), dev)
+    st = lib().hsa_page_append(K.data_ptr(), ks, V.data_ptr(), vs, slots.data_ptr(), n, Hkv, D, 64, Kp.data_ptr(),
+                               Vp.data_ptr(), pages, _stream_of(dev, None))
+    if st:
+        _check("hsa_page_append", st)
     return Kp, Vp
 
 
 def hsa_prefix_decode_workspace_size(B, H, Hkv, D, max_prefix_pages, max_pages, Tq=1):
-    return int(lib().hsa_prefix_decode_workspace_size(B, H, Hkv, Tq, D, max_prefix_pages, max_pages))
+    return lib().hsa_prefix_decode_workspace_size(B, H, Hkv, Tq, D, max_prefix_pages, max_pages)
 
 
 def hsa_prefix_decode(q, Kp, Vp, prefix_table, prefix_len, block_table, own_len, scale=0.0, out=None, lse=None,
@@ -486,30 +528,41 @@ def hsa_prefix_decode(q, Kp, Vp, prefix_table, prefix_len, block_table, own_len,
     [B, max_pages] int32 and own_len [B] int64: each request's own (negative: an empty row of a padded batch,
     out = 0 and lse = -inf). Returns (out shaped like q, lse fp32 without the last dimension)."""
     dev = q.device
-    multi = q.dim() == 4
-    B, H, D = q.shape[0], q.shape[1], q.shape[-1]
-    Tq = q.shape[2] if multi else 1
-    pages, Hkv = Kp.shape[0], Kp.shape[1]
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return hsa_prefix_decode(q, Kp, Vp, prefix_table, prefix_len, block_table, own_len, scale, out, lse, workspace)
+    shape = q.shape
+    B, H, D = shape[0], shape[1], shape[-1]
+    Tq = shape[2] if len(shape) == 4 else 1
+    pages, Hkv = Kp.shape[:2]
     npre, width = prefix_table.numel(), block_table.shape[1]
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-        _need(q, "q", torch.bfloat16, q.shape, dev)
-        _need(Kp, "Kp", torch.bfloat16, (pages, Hkv, 64, D), dev)
-        _need(Vp, "Vp", torch.bfloat16, (pages, Hkv, 64, D), dev)
-        _need(prefix_table, "prefix_table", torch.int32, (npre,), dev)
-        _need(prefix_len, "prefix_len", torch.int64, (1,), dev)
-        _need(block_table, "block_table", torch.int32, (B, width), dev)
-        _need(own_len, "own_len", torch.int64, (B,), dev)
-        _need(out, "out", torch.bfloat16, q.shape, dev)
-        _need(lse, "lse", torch.float32, q.shape[:-1], dev)
-        wp, wn = _aligned(_workspace(hsa_prefix_decode_workspace_size(B, H, Hkv, D, npre, width, Tq), dev, workspace))
-        st = lib().hsa_prefix_decode(_ptr(q), _ptr(Kp), _ptr(Vp), pages, _ptr(prefix_table) if npre else None, npre,
-                                     _ptr(prefix_len), _ptr(block_table) if width else None, width, _ptr(own_len), B, H,
-                                     Hkv, Tq, D, 64, float(scale), _ptr(out), _ptr(lse), wp, wn, _stream(dev, stream))
-    _check("hsa_prefix_decode", st)
+    _fits(q, "q", _BF16, (B, H, D) if len(shape) == 3 else (B, H, Tq, D), dev)
+    _fits(Kp, "Kp", _BF16, (pages, Hkv, 64, D), dev)
+    _fits(Vp, "Vp", _BF16, (pages, Hkv, 64, D), dev)
+    _fits(prefix_table, "prefix_table", _I32, (npre,), dev)
+    _fits(prefix_len, "prefix_len", _I64T, (1,), dev)
+    _fits(block_table, "block_table", _I32, (B, width), dev)
+    _fits(own_len, "own_len", _I64T, (B,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _fits(out, "out", _BF16, shape, dev)
+    if lse is None:
+        lse = torch.empty(shape[:-1], dtype=_F32, device=dev)
+    else:
+        _fits(lse, "lse", _F32, shape[:-1], dev)
+    if workspace is None:
+        need = hsa_prefix_decode_workspace_size(B, H, Hkv, D, npre, width, Tq)
+        workspace = torch.empty(need + 256, dtype=torch.uint8, device=dev)  # + 256: an aligned window always fits
+    ws = workspace.data_ptr()
+    pad = -ws % 256
+    st = lib().hsa_prefix_decode(q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), pages, prefix_table.data_ptr(), npre,
+                                 prefix_len.data_ptr(), block_table.data_ptr(), width, own_len.data_ptr(), B, H, Hkv, Tq,
+                                 D, 64, scale, out.data_ptr(), lse.data_ptr(), ws + pad,
+                                 max(0, workspace.numel() * workspace.element_size() - pad), _stream_of(dev, None))
+    if st:
+        _check("hsa_prefix_decode", st)
     return out, lse
 
 

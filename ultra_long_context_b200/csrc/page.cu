@@ -41,33 +41,50 @@ constexpr int kPlanMaxWarps = 32;
 constexpr int kPlanMaxCtas = 8;   // a portable cluster
 constexpr int kPlanTokens = 4;    // packed tokens a thread looks up at once, so that their loads overlap
 
-// Exclusive block scan of one value per thread (warp shuffles, then the warps' sums).
-template <typename T>
-__device__ __forceinline__ T plan_scan(T v, T *s_warp, T *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    T x = v;
+// What a request asks for: packed rows, pages given back, new pages. (Page sums stay below B * max_pages < 2^31.)
+struct PlanSum {
+    int64_t rows;
+    int back, need;
+    __device__ void add(const PlanSum &o) {
+        rows += o.rows;
+        back += o.back;
+        need += o.need;
+    }
+    __device__ PlanSum from_below(int o) const {
+        return {__shfl_up_sync(0xffffffffu, rows, o), __shfl_up_sync(0xffffffffu, back, o), __shfl_up_sync(0xffffffffu, need, o)};
+    }
+    __device__ PlanSum of_lane(int l) const {
+        return {__shfl_sync(0xffffffffu, rows, l), __shfl_sync(0xffffffffu, back, l), __shfl_sync(0xffffffffu, need, l)};
+    }
+};
+
+__device__ __forceinline__ PlanSum plan_warp_scan(PlanSum x) {  // inclusive
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const PlanSum y = x.from_below(o);
+        if (lane >= o) x.add(y);
     }
+    return x;
+}
+
+// Exclusive block scan (warp shuffles, then the warps' sums). s_warp is free again after the next barrier.
+__device__ __forceinline__ PlanSum plan_scan(const PlanSum &v, PlanSum *s_warp, PlanSum *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const PlanSum x = plan_warp_scan(v);
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
-    T w = lane < warps ? s_warp[lane] : 0;  // every warp sums the warps before it
-    const T mine = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-    }
-    *total = __shfl_sync(0xffffffffu, w, 31);
-    return __shfl_sync(0xffffffffu, w - mine, warp) + x - v;
+    const PlanSum w = plan_warp_scan(lane < warps ? s_warp[lane] : PlanSum{0, 0, 0});  // every warp sums all warps
+    *total = w.of_lane(31);
+    const PlanSum b = w.of_lane(warp > 0 ? warp - 1 : 0);
+    return {x.rows - v.rows + (warp > 0 ? b.rows : 0), x.back - v.back + (warp > 0 ? b.back : 0),
+            x.need - v.need + (warp > 0 ? b.need : 0)};
 }
 
 // Pages of 64 for n >= 0.
 __device__ __forceinline__ int plan_pages(int64_t n) { return (int)((uint64_t)(n + kChunk - 1) / kChunk); }
 
-__global__ void __launch_bounds__(32 * kPlanMaxWarps) page_plan_kernel(PagePlanArgs a) {
+__global__ void __launch_bounds__(32 * kPlanMaxWarps) page_plan_kernel(PagePlanArgs a, int run) {
     namespace cg = cooperative_groups;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     int64_t *s_len = reinterpret_cast<int64_t *>(smem_raw);            // [B] cache_len
@@ -75,8 +92,8 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps) page_plan_kernel(PagePlanA
     int32_t *s_cu = s_new + a.B;                                       // [B + 1] packed rows
     int32_t *s_at = s_cu + a.B + 1;                                    // [B] first page's place in the ring's order
     int32_t *s_gone = s_at + a.B;                                      // [B] finished requests
-    __shared__ int64_t s_rows[kPlanMaxWarps];
-    __shared__ int s_back[kPlanMaxWarps], s_need[kPlanMaxWarps], s_refused, s_got, s_ngone;
+    __shared__ PlanSum s_warp[2][kPlanMaxWarps];
+    __shared__ int s_refused, s_got, s_ngone;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, block = blockDim.x;
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks(), nthr = ctas * block;
@@ -90,69 +107,62 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps) page_plan_kernel(PagePlanA
     __syncthreads();
     const int per = (a.B + block - 1) / block;
     const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
-    // packed rows, and the pages that finished requests give back (page sums stay below B * max_pages < 2^31)
-    int64_t rows = 0, total_rows;
-    int back = 0, total_back;
-    for (int b = lo; b < hi; ++b) {
+    PlanSum sum{0, 0, 0}, total;
+    // rows_before: packed rows of the requests before it
+    auto asks = [&](int b, int64_t rows_before) {
         const int n = s_new[b];
         const int64_t c = s_len[b];
-        rows += max(n, 0);
-        back += n < 0 && c >= 0 && c <= cap ? plan_pages(c) : 0;
-    }
-    rows = plan_scan(rows, s_rows, &total_rows);
-    back = plan_scan(back, s_back, &total_back);
-    int need = 0, total_need;
-    int64_t r = rows;
-    for (int b = lo; b < hi; ++b) {
-        const int n = s_new[b];
-        const int64_t c = s_len[b];
-        s_cu[b] = (int)min(r, (int64_t)INT32_MAX);
-        r += max(n, 0);
-        if (n < 0 && c >= 0 && c <= cap) {
-            s_at[b] = back;
-            back += plan_pages(c);
-            // this block's share of them, in any order: each has its own places in the ring
-            if (b % ctas == rank) s_gone[atomicAdd(&s_ngone, 1)] = b;
-        } else if (n > 0 && c >= 0 && c <= cap && c + n <= cap && r <= a.max_tokens) {
-            need += plan_pages(c + n) - plan_pages(c);
+        PlanSum q{max(n, 0), 0, 0};
+        if (c >= 0 && c <= cap) {
+            if (n < 0) q.back = plan_pages(c);
+            if (n > 0 && c + n <= cap && rows_before + n <= a.max_tokens) q.need = plan_pages(c + n) - plan_pages(c);
         }
+        return q;
+    };
+    for (int b = lo; b < hi; ++b) sum.add(asks(b, 0));
+    PlanSum before = plan_scan(sum, s_warp[0], &total);
+    if (total.rows > a.max_tokens) {  // some have no room in the slot map and get no pages: sum the needs again
+        PlanSum again{0, 0, 0}, total2;
+        int64_t r = before.rows;
+        for (int b = lo; b < hi; ++b) {
+            again.need += asks(b, r).need;
+            r += max(s_new[b], 0);
+        }
+        before.need = plan_scan(again, s_warp[1], &total2).need;
     }
-    if (tid == 0) s_cu[a.B] = (int)min(total_rows, (int64_t)INT32_MAX);
-    need = plan_scan(need, s_need, &total_need);
     const int64_t avail = min(max(returned - taken, (int64_t)0), (int64_t)a.num_free);
     int got = 0, refused = 0;
-    r = rows;
     for (int b = lo; b < hi; ++b) {
         const int n = s_new[b];
         const int64_t c = s_len[b];
-        const bool known = c >= 0 && c <= cap;
-        r += max(n, 0);
-        if (n <= 0) {
-            refused += !known;
-            if (!known) s_new[b] = 0;
-            continue;
+        const PlanSum q = asks(b, before.rows);
+        s_cu[b] = (int)min(before.rows, (int64_t)INT32_MAX);
+        s_at[b] = n < 0 ? before.back : before.need;
+        before.add(q);
+        bool ok = c >= 0 && c <= cap;
+        if (n < 0 && ok && b % ctas == rank) s_gone[atomicAdd(&s_ngone, 1)] = b;  // this block's share, in any order
+        if (n > 0) {
+            ok = ok && c + n <= cap && before.rows <= a.max_tokens && (q.need == 0 || before.need <= avail);
+            if (ok && q.need > 0) got = before.need;  // those that get pages are the first that ask for any
         }
-        bool ok = known && c + n <= cap && r <= a.max_tokens;
-        if (ok) {
-            const int k = plan_pages(c + n) - plan_pages(c);
-            s_at[b] = need;
-            need += k;
-            ok = k == 0 || need <= avail;
-            if (ok && k > 0) got = need;  // those that get pages are the first that ask for any
+        if (!ok) {
+            ++refused;
+            s_new[b] = 0;
         }
-        refused += !ok;
-        if (!ok) s_new[b] = 0;
     }
+    if (tid == 0) s_cu[a.B] = (int)min(total.rows, (int64_t)INT32_MAX);
     got = __reduce_max_sync(0xffffffffu, got);
     refused = __reduce_add_sync(0xffffffffu, refused);
     if (lane == 0 && got) atomicMax(&s_got, got);
     if (lane == 0 && refused) atomicAdd(&s_refused, refused);
-    cluster.sync();  // every block has read cache_len and pool, which the outputs may overwrite
+    // every block has read cache_len and pool, which the outputs may overwrite
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
 
     const int gtid = rank * block + tid;
     if (gtid == 0) {
         a.pool_out[0] = taken + s_got;
-        a.pool_out[1] = returned + total_back;
+        a.pool_out[1] = returned + total.back;
         a.pool_out[2] = s_refused;
     }
     for (int b = gtid; b <= a.B; b += nthr) {
@@ -160,62 +170,57 @@ __global__ void __launch_bounds__(32 * kPlanMaxWarps) page_plan_kernel(PagePlanA
         if (b < a.B) a.total_len[b] = s_new[b] < 0 ? 0 : s_len[b] + s_new[b];
     }
     const int ring0 = ring_index(taken, a.num_free), ring1 = ring_index(returned, a.num_free);
-    const int live = (int)min(total_rows, (int64_t)a.max_tokens);
-    const int top = a.B > 1 ? 1 << (31 - __clz(a.B - 1)) : 0;
-    for (int64_t t0 = gtid; t0 < a.max_tokens; t0 += (int64_t)kPlanTokens * nthr) {
-        int req[kPlanTokens], id[kPlanTokens];
-        int64_t pos[kPlanTokens];
-        int32_t *entry[kPlanTokens];
-        // the last request whose rows begin at or before the token: requests without rows begin where the next does
-#pragma unroll
-        for (int u = 0; u < kPlanTokens; ++u) req[u] = 0;
-        for (int step = top; step > 0; step >>= 1) {
-#pragma unroll
-            for (int u = 0; u < kPlanTokens; ++u) {
-                const int m = req[u] + step;
-                if (m < a.B && s_cu[m] <= t0 + (int64_t)u * nthr) req[u] = m;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kPlanTokens; ++u) {
-            const int64_t t = t0 + (int64_t)u * nthr;
-            const int b = req[u];
-            id[u] = -1;
-            entry[u] = nullptr;
-            if (t >= live || s_new[b] <= 0) continue;
-            const int64_t c = s_len[b];
-            pos[u] = c + (t - s_cu[b]);
-            const int64_t pg = pos[u] / kChunk;
-            const int held = plan_pages(c);
-            int32_t *slot = a.block_table + (int64_t)b * a.max_pages + pg;
-            if (pg < held) {
-                id[u] = *slot;
-            } else {
-                const int64_t k = (int64_t)ring0 + s_at[b] + (pg - held);
-                id[u] = a.free_pages[k >= a.num_free ? k - a.num_free : k];
-                if (pos[u] % kChunk == 0) entry[u] = slot;
-            }
-            pos[u] %= kChunk;
-        }
-#pragma unroll
-        for (int u = 0; u < kPlanTokens; ++u) {
-            const int64_t t = t0 + (int64_t)u * nthr;
-            if (t >= a.max_tokens) continue;
-            const bool placed = t < live && s_new[req[u]] > 0;
-            a.slots[t] = placed ? (int64_t)id[u] * kChunk + pos[u] : -1;
-            if (entry[u]) *entry[u] = id[u];
-        }
-    }
-    // finished requests' pages, a warp to a request
-    for (int i = tid >> 5; i < s_ngone; i += block >> 5) {
+    // finished requests' pages: eight warps (or all there are) to a request
+    const int team = min(block, 256);
+    for (int i = tid / team; i < s_ngone; i += block / team) {
         const int b = s_gone[i], held = plan_pages(s_len[b]);
         const int32_t *row = a.block_table + (int64_t)b * a.max_pages;
-        const int first = ring_index((int64_t)ring1 + s_at[b], a.num_free);
-#pragma unroll 4
-        for (int j = lane; j < held; j += 32) {
+        const int64_t first = ring_index((int64_t)ring1 + s_at[b], a.num_free);
+        for (int j = tid % team; j < held; j += team) {
             // more pages than the ring holds cannot come back; if they do all the same, it goes round
-            const int64_t k = (int64_t)first + j;
+            const int64_t k = first + j;
             a.free_pages[k < a.num_free ? k : k % a.num_free] = row[j];
+        }
+    }
+    // packed tokens: `run` consecutive ones to a thread, kPlanTokens at a time
+    const int live = (int)min(total.rows, (int64_t)a.max_tokens);
+    const int top = a.B > 1 ? 1 << (31 - __clz(a.B - 1)) : 0;
+    for (int64_t t0 = (int64_t)gtid * run; t0 < a.max_tokens; t0 += (int64_t)nthr * run) {
+        // the last request whose rows begin at or before the token: requests without rows begin where the next does
+        int b = 0;
+        for (int step = top; step > 0; step >>= 1)
+            if (b + step < a.B && s_cu[b + step] <= t0) b += step;
+        const int64_t t_end = min(t0 + run, (int64_t)a.max_tokens);
+        for (int64_t t1 = t0; t1 < t_end; t1 += kPlanTokens) {
+            int id[kPlanTokens], off[kPlanTokens];
+            int32_t *entry[kPlanTokens];
+#pragma unroll
+            for (int u = 0; u < kPlanTokens; ++u) {
+                const int64_t t = t1 + u;
+                id[u] = -1;
+                off[u] = 0;
+                entry[u] = nullptr;
+                if (t >= t_end || t >= live) continue;
+                while (b + 1 < a.B && s_cu[b + 1] <= t) ++b;
+                if (s_new[b] <= 0) continue;
+                const int64_t c = s_len[b], pos = c + (t - s_cu[b]), pg = pos / kChunk;
+                const int held = plan_pages(c);
+                int32_t *slot = a.block_table + (int64_t)b * a.max_pages + pg;
+                off[u] = (int)(pos % kChunk);
+                if (pg < held) {
+                    id[u] = *slot;
+                } else {
+                    const int64_t k = (int64_t)ring0 + s_at[b] + (pg - held);
+                    id[u] = a.free_pages[k >= a.num_free ? k - a.num_free : k];
+                    if (off[u] == 0) entry[u] = slot;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kPlanTokens; ++u) {
+                if (t1 + u >= t_end) continue;
+                a.slots[t1 + u] = id[u] < 0 ? -1 : (int64_t)id[u] * kChunk + off[u];
+                if (entry[u]) *entry[u] = id[u];
+            }
         }
     }
 }
@@ -231,6 +236,9 @@ cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t s) {
     int threads = 128, ctas = 1;
     while (threads < 1024 && threads < work) threads *= 2;
     while (ctas < kPlanMaxCtas && (int64_t)ctas * threads < work) ctas *= 2;
+    // tokens to a thread: one while there are threads enough, then as many as there are to each, up to 16
+    const int64_t each = (a.max_tokens + (int64_t)ctas * threads - 1) / ((int64_t)ctas * threads);
+    const int run = (int)(each < 1 ? 1 : each > 16 ? 16 : each);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(threads);
@@ -242,7 +250,7 @@ cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     HSA_PROF("page_plan", s);
-    return cudaLaunchKernelEx(&cfg, page_plan_kernel, a);
+    return cudaLaunchKernelEx(&cfg, page_plan_kernel, a, run);
 }
 
 constexpr int kAppendThreads = 256;

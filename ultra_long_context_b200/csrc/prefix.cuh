@@ -95,6 +95,15 @@ struct PfSeg {
     const int32_t *table;
 };
 
+// What the copying warp, which walks the segments, announces of one to the other warps, through a ring in shared
+// memory; nr = 0 ends the walk.
+constexpr int kPfRing = 4;
+struct PfNote {
+    PfSeg s;
+    int n0;  // number of its first tile among the CTA's
+    int i0;  // wide: number of its first item (a tile for one of the two streams) among the CTA's
+};
+
 // Walks a CTA's segments; by a whole warp, its lanes holding the lengths of a block of 32 requests.
 struct PfWalk {
     const PrefixArgs &a;

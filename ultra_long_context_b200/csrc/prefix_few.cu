@@ -28,14 +28,7 @@ namespace hsa {
 constexpr int kFwMmaWarp = 8, kFwTmaWarp = 9, kFwQWarp = 10;
 constexpr int kFwThreads = 32 * (kFwQWarp + 1);
 constexpr float kFwGrow = 64.0f;
-constexpr int kFwRing = 4;    // announced segments
 constexpr int kFwFlags = 8;   // tiles whose page flags are kept (copies run at most KS tiles ahead of S^T)
-
-// What the other warps know of a segment.
-struct FwSeg {
-    PfSeg s;
-    int n0;  // number of its first tile
-};
 
 template <int D, int NR>  // NR: rows per segment at most
 struct FwSmem {
@@ -49,10 +42,10 @@ struct FwSmem {
     static constexpr uint32_t BAR = Q + 2 * QB;
     static constexpr int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = 2 * KS + VS, kQFull = 2 * KS + 2 * VS,
                          kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kInfo = kSFull + 2, kPFull = kInfo + 2,
-                         kODone = kPFull + 2, kOEmpty = kODone + 2, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kFwRing,
-                         NBAR = kSegEmpty + kFwRing;
+                         kODone = kPFull + 2, kOEmpty = kODone + 2, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kPfRing,
+                         NBAR = kSegEmpty + kPfRing;
     static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;
-    static constexpr uint32_t MS = RING + kFwRing * sizeof(FwSeg);        // float[2][NR]: m * scale * log2(e), or -inf
+    static constexpr uint32_t MS = RING + kPfRing * sizeof(PfNote);        // float[2][NR]: m * scale * log2(e), or -inf
     static constexpr uint32_t LIM = MS + 2 * NR * 4;                      // int[2][NR]
     static constexpr uint32_t SUM = LIM + 2 * NR * 4;                     // float[2][4][NR]: row sums of a warp's keys
     static constexpr uint32_t FLAG = SUM + 8 * NR * 4;                    // int[kFwFlags]
@@ -94,7 +87,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;  // 1 KB aligned (swizzle atoms)
     unsigned char *s = smem_raw + (sb - raw);
-    FwSeg *s_ring = reinterpret_cast<FwSeg *>(s + SM::RING);
+    PfNote *s_ring = reinterpret_cast<PfNote *>(s + SM::RING);
     float *s_ms = reinterpret_cast<float *>(s + SM::MS);
     int *s_lim = reinterpret_cast<int *>(s + SM::LIM);
     int *s_flag = reinterpret_cast<int *>(s + SM::FLAG);
@@ -128,7 +121,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             tc::mbar_init(bar(SM::kODone + i), 1);
             tc::mbar_init(bar(SM::kOEmpty + i), 128);
         }
-        for (int i = 0; i < kFwRing; ++i) {
+        for (int i = 0; i < kPfRing; ++i) {
             tc::mbar_init(bar(SM::kSegFull + i), 1);
             tc::mbar_init(bar(SM::kSegEmpty + i), 10);  // the warps but this ring's writer
         }
@@ -145,9 +138,9 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
 
     // the next announced segment; nr = 0 ends the walk
     int seg_no = 0;
-    auto take = [&](FwSeg &g) {
-        const int slot = seg_no % kFwRing;
-        if (!pf_wait(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kFwRing) & 1u)) return false;
+    auto take = [&](PfNote &g) {
+        const int slot = seg_no % kPfRing;
+        if (!pf_wait(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kPfRing) & 1u)) return false;
         g = s_ring[slot];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(SM::kSegEmpty + slot));
@@ -162,12 +155,12 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         int n = 0;
         bool more = true;
         while (ok && more) {
-            FwSeg g;
+            PfNote g;
             more = walk.next(g.s);
             if (!more) g.s.nr = 0;
             g.n0 = n;
-            const int slot = seg_no % kFwRing;
-            ok = pf_wait(bar(SM::kSegEmpty + slot), ((uint32_t)(seg_no / kFwRing) & 1u) ^ 1u);
+            const int slot = seg_no % kPfRing;
+            ok = pf_wait(bar(SM::kSegEmpty + slot), ((uint32_t)(seg_no / kPfRing) & 1u) ^ 1u);
             if (!ok) break;
             if (lane == 0) {
                 s_ring[slot] = g;
@@ -228,7 +221,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         // ================= Q rows =================
         constexpr int CPR = D / 8, RPW = 32 / CPR;  // 16-byte chunks per row, rows per warp-wide copy
         const int rsub = lane / CPR, ch = lane % CPR;
-        FwSeg g;
+        PfNote g;
         while (true) {
             const int q = seg_no & 1;
             const uint32_t use = (uint32_t)(seg_no >> 1);
@@ -248,7 +241,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         cp_async_wait<0>();  // nothing in flight when the CTA exits
     } else if (warp == kFwMmaWarp) {
         // ================= MMA issuer: the whole warp runs the loop, one elected lane issues =================
-        FwSeg g;
+        PfNote g;
         bool have = false, end = false;   // is there a segment at next_s; is there none any more
         int t = 0, q = 0;                 // of next_s: tile of the segment; Q buffer
         uint32_t quse = 0;
@@ -260,9 +253,9 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         while (true) {
             bool progress = false;
             // one probe per lane: the next segment, fillings, P^T and free O^T of both streams, in one round
-            const int slot = seg_no % kFwRing;
+            const int slot = seg_no % kPfRing;
             int b = SM::kSegFull + slot;
-            uint32_t par = (uint32_t)(seg_no / kFwRing);
+            uint32_t par = (uint32_t)(seg_no / kPfRing);
             if (lane == 1) b = SM::kKFull + k_slot, par = k_par;
             if (lane == 2) b = SM::kVFull + v_slot, par = v_par;
             if (lane == 3) b = SM::kQFull + q, par = quse;
@@ -365,7 +358,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         int *lims = s_lim + sid * NR;
         const float sl2 = a.scale * 1.4426950408889634f;
         uint32_t tiles = 0;
-        FwSeg g;
+        PfNote g;
         // A warp whose wait ran out says so and still comes to the barriers, and the warpgroup leaves together
         while (true) {
             if (!take(g)) s_bad[sid] = 1;

@@ -1,19 +1,19 @@
 // prefix_wide.cu -- segments of more than 64 query rows of the shared-prefix decode: the prefix of large batches,
 // a matrix product with (requests x query heads x tokens) rows, bound by the tensor cores and the exponentials.
 //
-// S = Q K^T (128 rows x 128 keys, fp32 in TMEM; thread = row), P = exp2(S scale' - m) as bf16 over S in TMEM, which
-// is the A operand of O += P V (128 x D, fp32 in TMEM). The accumulator is rescaled only when a row's maximum
-// grows by more than 2^8 (then P would leave a comfortable range; up to that the old maximum serves as well, since
-// the final quotient cancels it).
+// S = Q K^T (128 rows x 128 keys, fp32 in TMEM), P = exp2(S scale' - m) as bf16 over S in TMEM, which is the A operand
+// of O += P V (128 x D, fp32 in TMEM). The reference m of a row need not be its maximum (see prefix_few.cu): it is the
+// logit of the first key that the row sees in the segment, so no maximum is taken at all; a tile whose row sum exceeds
+// 2^70 moves it (rarely): the pair of warps then reduces the maximum, rescales O in TMEM and does the tile again.
 //
 // Persistent, warp-specialised kernel, one CTA per SM:
-//   warps 0-3, 4-7  two softmax warpgroups = two STREAMS, one thread per row. A segment of more than
-//               128 rows gives each stream 128 of them and both read every tile; a smaller one gives both
-//               streams the same rows and alternates the tiles between them (each keeps a partial of its own),
-//               so that one stream's products run under the other's softmax either way;
-//   warp 8      MMA issuer: S and O of both streams, whichever is ready;
-//   warp 9      K and V tiles by TMA, page by page (64 rows of one head are contiguous);
-//   warps 10-11 Q rows by cp.async.
+//   warps 0-7, 8-15 softmax of two STREAMS: two threads per row, one for each page of the tile (a thread's 64
+//               logits stay in registers). The work is a sequence of items that go to the streams in turn: a
+//               segment of more than 128 rows has two items per tile, one for each 128 rows; a smaller one has one
+//               (and each stream keeps a partial of its own). So one stream's products run under the other's softmax;
+//   warp 16     MMA issuer, in a fixed order: S(i + 1), then O(i);
+//   warp 17     K and V tiles by TMA, page by page (64 rows of one head are contiguous);
+//   warps 18-19 Q rows by cp.async, padded with zero rows.
 #include <cuda.h>
 
 #include "prefix.cuh"
@@ -21,22 +21,30 @@
 
 namespace hsa {
 
-constexpr int kPfMmaWarp = 8, kPfTmaWarp = 9, kPfQWarp = 10, kPfQWarps = 2;
+constexpr int kPfStreamWarps = 8;
+constexpr int kPfMmaWarp = 2 * kPfStreamWarps, kPfTmaWarp = kPfMmaWarp + 1, kPfQWarp = kPfMmaWarp + 2, kPfQWarps = 2;
 constexpr int kPfThreads = 32 * (kPfQWarp + kPfQWarps);
+constexpr int kPfFlags = 8;               // tiles whose page flags are kept
+constexpr float kPfGrow = 64.0f, kPfSumMax = 0x1p70f;  // a sum of 64 terms of at most 2^64
 
 template <int D>
 struct PfSmem {
     static constexpr int KH = D / 64;                       // 128-byte column blocks of D
     static constexpr uint32_t OP = KH * 16384;              // one operand tile [128][D]
     static constexpr int KS = D == 128 ? 2 : 4, VS = D == 128 ? 2 : 4;
+    static_assert(KS + 2 <= kPfFlags, "page flags");
     static constexpr uint32_t Q = 0, K = 2 * OP, V = K + KS * OP;
     static constexpr uint32_t BAR = V + VS * OP;
     // mbarriers
     static constexpr int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = 2 * KS + VS, kQFull = 2 * KS + 2 * VS,
-                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 2, kODone = kPFull + 2,
-                         kOEmpty = kODone + 2, NBAR = kOEmpty + 2;
-    static constexpr uint32_t FLAG = BAR + 8 * NBAR;        // int[VS]: which of a V slot's two pages are good
-    static constexpr uint32_t TMEM = FLAG + 4 * VS;
+                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kInfo = kSFull + 2, kPFull = kInfo + 2,
+                         kODone = kPFull + 2, kOEmpty = kODone + 2, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kPfRing,
+                         NBAR = kSegEmpty + kPfRing;
+    static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;  // PfNote[kPfRing]
+    static constexpr uint32_t ROW = RING + kPfRing * sizeof(PfNote);   // float[2 streams][2 halves][128]: exchanged by a row's threads
+    static constexpr uint32_t FLAG = ROW + 2 * 2 * 128 * 4;  // int[kPfFlags]: which of a tile's two pages are good
+    static constexpr uint32_t BADP = FLAG + 4 * kPfFlags;    // int[8]: a wait of the pair of warps ran out
+    static constexpr uint32_t TMEM = BADP + 32;
     static constexpr uint32_t BAD = TMEM + 4;
     static constexpr uint32_t PLAN = (BAD + 4 + 15) / 16 * 16;
     static constexpr uint32_t BCUM = PLAN + (sizeof(PfPlan) + 15) / 16 * 16;  // int[blocks + 1]
@@ -45,9 +53,23 @@ struct PfSmem {
 };
 static_assert(PfSmem<128>::dyn(256) <= 227 * 1024 && PfSmem<64>::dyn(256) <= 227 * 1024, "shared memory budget");
 
-// Do both streams read every tile of the segment (each for rows of its own)? The tiles of stream s otherwise.
+// Do both streams read every tile of the segment, each for rows of its own?
 __device__ __forceinline__ bool pf_both(const PfSeg &s) { return s.nr > kPfTile; }
-__device__ __forceinline__ int pf_count(const PfSeg &s, int sid) { return pf_both(s) ? s.nt : (s.nt + 1 - sid) >> 1; }
+
+// Named barriers of the two warps (64 threads) that share 32 rows.
+__device__ __forceinline__ void pf_pair_bar(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pf_pair_or(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id)
+        : "memory");
+    return r != 0u;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const PrefixArgs a, const PfDims d, const PfWork w,
@@ -60,8 +82,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;  // 1 KB aligned (swizzle atoms)
     unsigned char *s = smem_raw + (sb - raw);
-    volatile int *s_flag = reinterpret_cast<volatile int *>(s + SM::FLAG);
-    int *s_bad = reinterpret_cast<int *>(s + SM::BAD);
+    PfNote *s_ring = reinterpret_cast<PfNote *>(s + SM::RING);
+    int *s_flag = reinterpret_cast<int *>(s + SM::FLAG);
+    volatile int *s_badp = reinterpret_cast<volatile int *>(s + SM::BADP), *s_bad = reinterpret_cast<volatile int *>(s + SM::BAD);
     PfPlan *s_plan = reinterpret_cast<PfPlan *>(s + SM::PLAN);
     int32_t *s_bcum = reinterpret_cast<int32_t *>(s + SM::BCUM);
     auto bar = [&](int i) { return sb + SM::BAR + 8u * (uint32_t)i; };
@@ -74,21 +97,27 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     }
     if (tid == 0) {
         *s_bad = 0;
+        for (int i = 0; i < 8; ++i) s_badp[i] = 0;
         for (int i = 0; i < KS; ++i) {
             tc::mbar_init(bar(SM::kKFull + i), 1);
-            tc::mbar_init(bar(SM::kKEmpty + i), 2);  // each stream's S, or one stream's twice
+            tc::mbar_init(bar(SM::kKEmpty + i), 1);
         }
         for (int i = 0; i < VS; ++i) {
             tc::mbar_init(bar(SM::kVFull + i), 1);
-            tc::mbar_init(bar(SM::kVEmpty + i), 2);
+            tc::mbar_init(bar(SM::kVEmpty + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(SM::kQFull + i), 32 * kPfQWarps);
-            tc::mbar_init(bar(SM::kQEmpty + i), 2);
+            tc::mbar_init(bar(SM::kQEmpty + i), 1);
             tc::mbar_init(bar(SM::kSFull + i), 1);
-            tc::mbar_init(bar(SM::kPFull + i), kPfTile);
+            tc::mbar_init(bar(SM::kInfo + i), 1);
+            tc::mbar_init(bar(SM::kPFull + i), 32 * kPfStreamWarps);
             tc::mbar_init(bar(SM::kODone + i), 1);
-            tc::mbar_init(bar(SM::kOEmpty + i), kPfTile);
+            tc::mbar_init(bar(SM::kOEmpty + i), 32 * kPfStreamWarps);
+        }
+        for (int i = 0; i < kPfRing; ++i) {
+            tc::mbar_init(bar(SM::kSegFull + i), 1);
+            tc::mbar_init(bar(SM::kSegEmpty + i), 2 * kPfStreamWarps + kPfQWarps + 1);  // the warps but this ring's writer
         }
         tc::fence_mbar_init();
     }
@@ -101,14 +130,41 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     pf_schedule<kPfThreads>(a, d, take_prefix, take_own, s_plan, s_bcum);
     pf_publish<kPfThreads>(d, take_prefix, take_own, s_plan, s_bcum, w);
     bool ok = true;
-    PfWalk walk(a, *s_plan, s_bcum, d);
-    PfSeg seg;
+
+    int seg_no = 0;  // the next announced segment
+    auto take = [&](PfNote &g) {
+        const int slot = seg_no % kPfRing;
+        if (!pf_wait(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kPfRing) & 1u)) return false;
+        g = s_ring[slot];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(SM::kSegEmpty + slot));
+        ++seg_no;
+        return true;
+    };
 
     if (warp == kPfTmaWarp) {
-        // ================= K and V tiles =================
+        // ================= the walk, K and V tiles =================
+        PfWalk walk(a, *s_plan, s_bcum, d);
         const int pages_all = a.num_pages;
-        int n = 0;
-        while (ok && walk.next(seg)) {
+        int n = 0, items = 0;
+        bool more = true;
+        while (ok && more) {
+            PfNote g;
+            more = walk.next(g.s);
+            if (!more) g.s.nr = 0;
+            g.n0 = n;
+            g.i0 = items;
+            if (more) items += pf_both(g.s) ? 2 * g.s.nt : g.s.nt;
+            const int slot = seg_no % kPfRing;
+            ok = pf_wait(bar(SM::kSegEmpty + slot), ((uint32_t)(seg_no / kPfRing) & 1u) ^ 1u);
+            if (!ok) break;
+            if (lane == 0) {
+                s_ring[slot] = g;
+                tc::mbar_arrive(bar(SM::kSegFull + slot));
+            }
+            ++seg_no;
+            if (!more) break;
+            const PfSeg &seg = g.s;
             const int npages = (seg.len + kChunk - 1) / kChunk;  // of the sequence; its table holds them
             auto fetch = [&](int from) {  // this lane's page id of the batch that starts at page `from`
                 const int i = from + lane;
@@ -130,6 +186,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                     ok = pf_wait_lane(bar(SM::kKEmpty + ks), ((uint32_t)(n / KS) & 1u) ^ 1u);
                     if (ok) {
                         const uint32_t dst = sb + SM::K + ks * SM::OP;
+                        s_flag[n % kPfFlags] = (g0 ? 1 : 0) | (g1 ? 2 : 0);
                         tc::mbar_arrive_expect_tx(bar(SM::kKFull + ks), SM::OP);
 #pragma unroll
                         for (int h = 0; h < SM::KH; ++h) {
@@ -141,7 +198,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                     }
                     if (ok) {
                         const uint32_t dst = sb + SM::V + vs * SM::OP;
-                        s_flag[vs] = (g0 ? 1 : 0) | (g1 ? 2 : 0);
                         tc::mbar_arrive_expect_tx(bar(SM::kVFull + vs), SM::OP);
 #pragma unroll
                         for (int h = 0; h < SM::KH; ++h) {
@@ -163,7 +219,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         const int qw = warp - kPfQWarp, rsub = lane / CPR, ch = lane % CPR;
         uint32_t uses[2] = {0, 0};
         int turn = 0;
-        while (ok && walk.next(seg)) {
+        PfNote g;
+        while (true) {
+            ok = take(g);
+            if (!ok || g.s.nr == 0) break;
+            const PfSeg &seg = g.s;
             const bool both = pf_both(seg);
             for (int k = 0; k < (both ? 2 : 1) && ok; ++k) {
                 const int q = both ? k : turn;
@@ -172,11 +232,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                 ++uses[q];
                 const int rows = min(kPfTile, seg.nr - k * kPfTile);
                 const uint32_t dst = sb + SM::Q + q * SM::OP;
-                for (int r = qw * RPW + rsub; r < rows; r += kPfQWarps * RPW)  // the other rows are nobody's
+                // (the other rows are nobody's; zeros keep their logits small)
+                for (int r = qw * RPW + rsub; r < kPfTile; r += kPfQWarps * RPW) {
+                    const bool in = r < rows;
                     cp_async16_u32(dst + (ch >> 3) * 16384 + tc::sw128(r, ch & 7),
-                                   a.q + pf_q_row(seg, d, a.Hkv, k * kPfTile + r) * D + ch * 8, 16);
+                                   in ? a.q + pf_q_row(seg, d, a.Hkv, k * kPfTile + r) * D + ch * 8 : a.q, in ? 16 : 0);
+                }
                 pf_cp_async_arrive(bar(SM::kQFull + q));  // fires when this thread's copies have landed
             }
+            if (!ok) break;
             if (!both) turn ^= 1;
         }
         cp_async_commit();
@@ -185,223 +249,209 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         // ================= MMA issuer: the whole warp runs the loop, one elected lane issues =================
         constexpr uint32_t idesc_s = tc::idesc_bf16(kPfTile, kPfTile, 0, 0);
         constexpr uint32_t idesc_o = tc::idesc_bf16(kPfTile, D, 0, 1);
-        struct Stream {
-            PfSeg seg;
-            int item;
-            int64_t x;
-            bool live, want_pv;
-            int j, cnt, n0, q, turn;
-            uint32_t uses0, uses1, qphase, tiles, segs;
-        } st[2];
-        auto advance = [&](Stream &c, int sid) {  // to the next segment with tiles of this stream
-            walk.item = c.item;
-            walk.x = c.x;
-            c.live = false;
-            while (walk.next(c.seg)) {
-                const bool both = pf_both(c.seg);
-                if (both) {
-                    c.q = sid;
-                    c.qphase = sid ? c.uses1 : c.uses0;
-                    ++c.uses0;
-                    ++c.uses1;
-                } else {
-                    c.q = c.turn;
-                    c.qphase = c.turn ? c.uses1 : c.uses0;
-                    if (c.turn) ++c.uses1;
-                    else ++c.uses0;
-                    c.turn ^= 1;
-                }
-                c.j = 0;
-                c.cnt = pf_count(c.seg, sid);
-                if (c.cnt > 0) {
-                    c.live = true;
-                    break;
-                }
-                c.n0 += c.seg.nt;
+        // Every filling of every slot is waited for in order. Nothing waits for an O that is not issued yet: S(i + 1) needs
+        // O(i - 1), and its K, in the copies' order, slots that O(i - 1) and earlier ones release; a segment that is not
+        // announced yet is waited for only when no O is due (its announcement comes after the copies of the one before).
+        PfNote g{};
+        int nt = 0, items = 0, u = 0, q0 = 0, turn = 0;  // of the segment at item i_s: u is the item's number in it
+        bool both = false, end = false;
+        uint32_t uses0 = 0, uses1 = 0;                   // fillings of the Q buffers before this segment's
+        int i_s = 0, i_o = 0;                            // next items
+        uint32_t issued[2] = {0, 0}, runs[2] = {0, 0};   // O products of a stream; its runs (one per segment) begun
+        int tile[2] = {0, 0};                            // of the stream's item at O: its tile's number,
+        bool first[2] = {false, false}, last[2] = {false, false};  // does it begin a run; is it the tile's last item
+        auto issue_s = [&](const int sid) {
+            const int t = both ? u >> 1 : u, n = g.n0 + t, ks = n % KS, q = both ? u & 1 : q0;
+            const bool starts = both ? u < 2 : u == 0;  // the first to read its Q buffer
+            ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS) & 1u);
+            if (ok && starts) ok = pf_wait(bar(SM::kQFull + q), (q ? uses1 : uses0) & 1u);
+            // S and P share columns: P of the stream's item before must have been read
+            if (ok && issued[sid] > 0) ok = pf_wait(bar(SM::kODone + sid), (issued[sid] - 1) & 1u);
+            if (!ok) return;
+            if (lane == 0) tc::mbar_arrive(bar(SM::kInfo + sid));  // hands on the page flags that came with K
+            tc::fence_after();
+            tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
+            const uint32_t sq = sb + SM::Q + q * SM::OP, sk = sb + SM::K + ks * SM::OP;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
+                tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * kPfTile, tc::desc_kmajor(sq + off), tc::desc_kmajor(sk + off),
+                                  idesc_s, k > 0 ? 1u : 0u);
             }
-            c.item = walk.item;
-            c.x = walk.x;
+            tc::commit_w(bar(SM::kSFull + sid));
+            tile[sid] = n;
+            first[sid] = u < 2;
+            last[sid] = !both || (u & 1);
+            if (first[sid]) ++runs[sid];
+            if (last[sid]) tc::commit_w(bar(SM::kKEmpty + ks));
+            if (u >= items - (both ? 2 : 1)) tc::commit_w(bar(SM::kQEmpty + q));
+            ++u;
+            ++i_s;
         };
+        auto issue_o = [&](const int sid) {
+            const int n = tile[sid], vs = n % VS;
+            ok = pf_wait(bar(SM::kPFull + sid), issued[sid] & 1u) && pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
+            if (ok && first[sid] && runs[sid] > 1) ok = pf_wait(bar(SM::kOEmpty + sid), (runs[sid] - 2) & 1u);
+            if (!ok) return;
+            tc::fence_after();
+            const uint32_t sv = sb + SM::V + vs * SM::OP;
 #pragma unroll
-        for (int sid = 0; sid < 2; ++sid) {
-            st[sid].item = walk.item;
-            st[sid].x = walk.x;
-            st[sid].want_pv = false;
-            st[sid].n0 = st[sid].turn = 0;
-            st[sid].uses0 = st[sid].uses1 = st[sid].tiles = st[sid].segs = 0;
-        }
-        advance(st[0], 0);
-        advance(st[1], 1);
-        // one answer for the whole warp, so that it stays converged
-        auto done = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_test(bar(i), parity)) != 0; };
-        // A slot's fillings are used by either stream, and a stream that skips some cannot tell a filling from the
-        // one two before it by its parity. So the warp observes every filling of every slot in order (none can be
-        // replaced before a stream has used it), and the streams ask the counts.
-        int k_seen = 0, v_seen = 0, k_slot = 0, v_slot = 0;
-        uint32_t q_seen0 = 0, q_seen1 = 0, k_par = 0, v_par = 0;
-        uint32_t idle = 0;
-        while (st[0].live || st[1].live) {
-            bool progress = false;
-            if (done(SM::kKFull + k_slot, k_par)) {
-                ++k_seen;
-                if (++k_slot == KS) k_slot = 0, k_par ^= 1u;
-            }
-            if (done(SM::kVFull + v_slot, v_par)) {
-                ++v_seen;
-                if (++v_slot == VS) v_slot = 0, v_par ^= 1u;
-            }
-            if (done(SM::kQFull, q_seen0 & 1u)) ++q_seen0;
-            if (done(SM::kQFull + 1, q_seen1 & 1u)) ++q_seen1;
-#pragma unroll
-            for (int sid = 0; sid < 2; ++sid) {
-                Stream &c = st[sid];
-                if (!c.live) continue;
-                const bool both = pf_both(c.seg);
-                const int n = c.n0 + (both ? c.j : 2 * c.j + sid);
-                const int ks = n % KS, vs = n % VS;
-                if (!c.want_pv) {
-                    // the V filling before this tile's in its slot has landed, too: the softmax's wait on the slot's
-                    // parity, which follows S, is then exact
-                    if (n >= k_seen || n - VS >= v_seen) continue;
-                    if (c.j == 0 && c.qphase >= (c.q ? q_seen1 : q_seen0)) continue;
-                    // S and P share columns: P of the stream's tile before must have been read
-                    if (c.tiles > 0 && !done(SM::kODone + sid, (c.tiles - 1) & 1u)) continue;
-                    tc::fence_after();
-                    tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
-                    const uint32_t sq = sb + SM::Q + c.q * SM::OP, sk = sb + SM::K + ks * SM::OP;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
-                        tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * kPfTile, tc::desc_kmajor(sq + off),
-                                          tc::desc_kmajor(sk + off), idesc_s, k > 0 ? 1u : 0u);
-                    }
-                    tc::commit_w(bar(SM::kSFull + sid));
-                    tc::commit_w(bar(SM::kKEmpty + ks));
-                    if (!both) tc::commit_w(bar(SM::kKEmpty + ks));
-                    if (c.j == c.cnt - 1) {
-                        tc::commit_w(bar(SM::kQEmpty + c.q));
-                        if (both || pf_count(c.seg, sid ^ 1) == 0) tc::commit_w(bar(SM::kQEmpty + c.q));
-                    }
-                    c.want_pv = true;
-                } else {
-                    if (!done(SM::kPFull + sid, c.tiles & 1u)) continue;
-                    if (n >= v_seen) continue;
-                    if (c.j == 0 && c.segs > 0 && !done(SM::kOEmpty + sid, (c.segs - 1) & 1u)) continue;
-                    tc::fence_after();
-                    const uint32_t sv = sb + SM::V + vs * SM::OP;
-#pragma unroll
-                    for (int k = 0; k < kPfTile / 16; ++k)
-                        tc::mma_bf16_ts_w(tmem + SM::O_COL + sid * D, tmem + SM::S_COL + sid * kPfTile + k * 8,
-                                          tc::desc_mnmajor(sv + k * 2048, 16384), idesc_o, c.j > 0 || k > 0 ? 1u : 0u);
-                    tc::commit_w(bar(SM::kODone + sid));
-                    tc::commit_w(bar(SM::kVEmpty + vs));
-                    if (!both) tc::commit_w(bar(SM::kVEmpty + vs));
-                    c.want_pv = false;
-                    ++c.tiles;
-                    if (++c.j == c.cnt) {
-                        ++c.segs;
-                        c.n0 += c.seg.nt;
-                        advance(c, sid);
+            for (int k = 0; k < kPfTile / 16; ++k)  // a page's P stands where its S began
+                tc::mma_bf16_ts_w(tmem + SM::O_COL + sid * D, tmem + SM::S_COL + sid * kPfTile + (k >> 2) * 64 + (k & 3) * 8,
+                                  tc::desc_mnmajor(sv + k * 2048, 16384), idesc_o, !first[sid] || k > 0 ? 1u : 0u);
+            tc::commit_w(bar(SM::kODone + sid));
+            if (last[sid]) tc::commit_w(bar(SM::kVEmpty + vs));
+            ++issued[sid];
+            ++i_o;
+        };
+        while (ok) {
+            if (u == items && !end && i_s < i_o + 2) {
+                const int slot = seg_no % kPfRing;
+                if (i_o == i_s || pf_done(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kPfRing) & 1u)) {
+                    // the last segment's Q buffers have been counted as used
+                    ok = take(g);
+                    if (!ok) break;
+                    uses0 += items > 0 && (both || q0 == 0);
+                    uses1 += items > 0 && (both || q0 == 1);
+                    end = g.s.nr == 0;
+                    both = pf_both(g.s);
+                    nt = g.s.nt;
+                    items = end ? 0 : both ? 2 * nt : nt;
+                    u = 0;
+                    if (!end && !both) {
+                        q0 = turn;
+                        turn ^= 1;
                     }
                 }
-                progress = true;
             }
-            if (progress) {
-                idle = 0;
-            } else if (++idle > (1u << 26)) {
-                ok = false;
+            if (u < items && i_s < i_o + 2) {
+                if (i_s & 1) issue_s(1);
+                else issue_s(0);
+                if (!ok) break;
+                if (i_s == i_o + 1) continue;  // the very first, or the only one at hand: one more S before its O
+            }
+            if (i_o < i_s) {
+                if (i_o & 1) issue_o(1);
+                else issue_o(0);
+            } else if (end) {
                 break;
             }
         }
         __syncwarp();
     } else {
-        // ================= softmax: stream sid, thread = row =================
-        const int sid = warp >> 2, r = (warp & 3) * 32 + lane;
-        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        // ================= softmax: stream sid, two threads per row (half = page of the tile) =================
+        // A warp whose wait ran out says so and still comes to the pair's next barrier, and the pair leaves together
+        const int sid = warp / kPfStreamWarps, half = (warp >> 2) & 1, quad = warp & 3, r = quad * 32 + lane;
+        const int pid = 1 + sid * 4 + quad;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         const uint32_t tS = tmem + lane_off + SM::S_COL + sid * kPfTile;
-        const uint32_t tO = tmem + lane_off + SM::O_COL + sid * D;
+        const uint32_t tO = tmem + lane_off + SM::O_COL + sid * D + half * (D / 2);
+        float *s_row = reinterpret_cast<float *>(s + SM::ROW) + sid * 256 + r;  // [0]: half 0, [128]: half 1
         const float sl2 = a.scale * 1.4426950408889634f;
         uint32_t tiles = 0;
-        int n0 = 0;
-        for (; ok && walk.next(seg); n0 += seg.nt) {
-            const int cnt = pf_count(seg, sid);
-            if (cnt == 0) continue;
+        PfNote g;
+        while (ok) {
+            if (!take(g)) s_badp[pid - 1] = 1;
+            pf_pair_bar(pid);
+            if (s_badp[pid - 1]) ok = false;
+            if (!ok || g.s.nr == 0) break;
+            const PfSeg &seg = g.s;
             const bool both = pf_both(seg);
-            const int rr = both ? sid * kPfTile + r : r;
+            const int turn = (sid ^ g.i0) & 1;  // which of the segment's items go to this stream: the even or the odd ones
+            if (!both && turn >= seg.nt) continue;
+            const int rr = both ? turn * kPfTile + r : r, t0 = both ? 0 : turn, dt = both ? 1 : 2;
             const bool mine = rr < seg.nr;
-            const bool active = rr - lane < seg.nr;  // does this warp hold any row?
-            // rows that are nobody's compute something that is never read
+            const bool active = rr - lane < seg.nr;  // do this pair's warps hold any row?
             const int lim = mine ? pf_limit(a, seg, d, rr) : INT32_MAX;
-            float m = -INFINITY, l = 0.0f;
-            for (int j = 0; j < cnt; ++j, ++tiles) {
-                const int t = both ? j : 2 * j + sid, n = n0 + t, vs = n % VS;
+            float ms = 0.0f, l = 0.0f;
+            for (int t = t0; t < seg.nt; t += dt, ++tiles) {
+                const int n = g.n0 + t, vs = n % VS;
                 const int base = (seg.tile0 + t) * kPfTile;
-                // v_full also publishes the tile's page flags; its slot is not filled again before this
-                // stream's P V has read it, and S says that the filling before this one is over
-                ok = pf_wait(bar(SM::kSFull + sid), tiles & 1u) && pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
-                if (!ok) break;
+                bool good = pf_wait(bar(SM::kInfo + sid), tiles & 1u) && pf_wait(bar(SM::kSFull + sid), tiles & 1u);
                 tc::fence_after();
-                const int flags = s_flag[vs];
+                const int flags = s_flag[n % kPfFlags];
+                if (!good) s_badp[pid - 1] = 1;
                 if (active) {
-                    __syncwarp();
-                    float x[2][64];
-                    tc::tmem_ld64(tS, x[0]);
-                    tc::tmem_ld64(tS + 64, x[1]);
-                    if (__any_sync(0xffffffffu, flags != 3 || base + kPfTile > lim)) {
+                    const int vis = (flags >> half) & 1 ? lim - base - 64 * half : 0;  // keys of this half that the row sees
+                    const bool edge = __any_sync(0xffffffffu, vis < 64);
+                    uint32_t pk[32];
+                    float sum;
+                    // P of this half as bf16 pairs, and its sum
+                    auto probs = [&](const float (&x)[64]) {
+                        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        if (edge) {
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const int vis = (flags >> p) & 1 ? lim - base - 64 * p : 0;
+                            for (int i = 0; i < 32; ++i) {
+                                const float p0 = 2 * i < vis ? ex2_approx(fmaf(x[2 * i], sl2, -ms)) : 0.0f;
+                                const float p1 = 2 * i + 1 < vis ? ex2_approx(fmaf(x[2 * i + 1], sl2, -ms)) : 0.0f;
+                                s4[i & 3] += p0 + p1;
+                                pk[i] = pack_bf16x2(p0, p1);
+                            }
+                        } else {
 #pragma unroll
-                            for (int i = 0; i < 64; ++i) x[p][i] = i < vis ? x[p][i] : -INFINITY;
+                            for (int i = 0; i < 32; ++i) {
+                                const float p0 = ex2_approx(fmaf(x[2 * i], sl2, -ms));
+                                const float p1 = ex2_approx(fmaf(x[2 * i + 1], sl2, -ms));
+                                s4[i & 3] += p0 + p1;
+                                pk[i] = pack_bf16x2(p0, p1);
+                            }
                         }
+                        sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    };
+                    bool high;
+                    {
+                        float x[64];
+                        __syncwarp();
+                        tc::tmem_ld64(tS + 64 * half, x);
+                        if (t == t0) {  // the row's reference: its first key, or the second page's where the first is bad
+                            if (half == (flags & 1 ? 0 : 1)) s_row[0] = vis > 0 ? x[0] * sl2 : -INFINITY;
+                            pf_pair_bar(pid);
+                            ms = s_row[0];
+                        }
+                        probs(x);
+                        high = sum > kPfSumMax;
                     }
-                    float m8[8];  // row maximum as a tree
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        m8[i] = fmaxf(x[0][i], x[1][i]);
-#pragma unroll
-                        for (int k = 8; k < 64; k += 8) m8[i] = fmaxf(m8[i], fmaxf(x[0][i + k], x[1][i + k]));
+                    const bool any = pf_pair_or(pid, high);
+                    if (s_badp[pid - 1]) {
+                        ok = false;
+                        break;
                     }
-                    const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                           fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-                    const bool grow = (mx - m) * sl2 > 8.0f;  // from -inf, too; false while nothing is visible
-                    if (j == 0) {
-                        m = mx;
-                    } else if (__any_sync(0xffffffffu, grow)) {
-                        ok = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);
-                        if (!ok) break;
-                        tc::fence_after();
-                        const float f = grow ? ex2_approx((m - mx) * sl2) : 1.0f;
-                        if (grow) m = mx;
+                    if (any) {
+                        float x[64], mx = -INFINITY;
+                        tc::tmem_ld64(tS + 64 * half, x);
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) mx = fmaxf(mx, i < vis ? x[i] * sl2 : -INFINITY);
+                        s_row[128 * half] = mx;
+                        if (tiles > 0) good = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);  // O is at rest
+                        if (!good) s_badp[pid - 1] = 1;
+                        pf_pair_bar(pid);
+                        mx = fmaxf(s_row[0], s_row[128]);
+                        const bool grow = mx - ms > kPfGrow;  // from -inf, too; not where nothing is visible yet
+                        const float f = grow ? ex2_approx(ms - mx) : 1.0f;
+                        if (grow) ms = mx;
                         l *= f;
+                        if (t > t0) {
+                            tc::fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tc::tmem_ld32(tO + c, o);
+                            for (int c = 0; c < D / 2; c += 32) {
+                                float o[32];
+                                tc::tmem_ld32(tO + c, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= f;
-                            tc::tmem_st32f(tO + c, o);
+                                for (int i = 0; i < 32; ++i) o[i] *= f;
+                                tc::tmem_st32f(tO + c, o);
+                            }
                         }
+                        probs(x);
                     }
-                    const float ms = m > -INFINITY ? m * sl2 : 0.0f;
-                    float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t pk[32];  // P row as bf16 pairs, over S
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float p0 = ex2_approx(fmaf(x[p][2 * i], sl2, -ms));
-                            const float p1 = ex2_approx(fmaf(x[p][2 * i + 1], sl2, -ms));
-                            l4[i & 3] += p0 + p1;
-                            pk[i] = pack_bf16x2(p0, p1);
-                        }
-                        tc::tmem_st32(tS + 32 * p, pk);
-                    }
-                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    tc::tmem_st32(tS + 64 * half, pk);
+                    l += sum;
+                } else if (!good) {
+                    break;
                 }
                 // keys behind the sequence's end weigh nothing, but 0 x NaN is NaN: their V rows become zero
                 if (base + kPfTile > seg.len) {
-                    if (r >= seg.len - base) {
+                    if (!pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u)) s_badp[pid - 1] = 1;
+                    if (half == 0 && r >= seg.len - base) {
 #pragma unroll
                         for (int h = 0; h < SM::KH; ++h) {
                             uint4 *row = reinterpret_cast<uint4 *>(s + SM::V + vs * SM::OP + h * 16384 + r * 128);
@@ -415,14 +465,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                 tc::mbar_arrive(bar(SM::kPFull + sid));
             }
             if (!ok) break;
-            ok = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);
-            if (!ok) break;
-            tc::fence_after();
+            // (warps without a row wait as well: they must not come to the next segment's end before this one's)
+            const bool rest = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);
+            if (!rest) s_badp[pid - 1] = 1;
+            if (!active && !rest) continue;
             if (active) {
-                const int64_t at = (int64_t)seg.part * (seg.b < 0 ? d.strideP : d.strideO) + (both ? rr : sid * seg.nr + rr);
-                float *O = (seg.b < 0 ? w.Op : w.Oo) + at * D;
+                s_row[128 * half] = l;
+                pf_pair_bar(pid);
+                if (s_badp[pid - 1]) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const int64_t at = (int64_t)seg.part * (seg.b < 0 ? d.strideP : d.strideO) + (both ? rr : turn * seg.nr + rr);
+                float *O = (seg.b < 0 ? w.Op : w.Oo) + at * D + half * (D / 2);
+                if (mine && half == 0)
+                    reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at] = make_float2(ms, s_row[0] + s_row[128]);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = 0; c < D / 2; c += 32) {
                     float o[32];
                     __syncwarp();  // the lanes without a row skip the stores
                     tc::tmem_ld32(tO + c, o);
@@ -432,13 +492,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                             reinterpret_cast<float4 *>(O + c)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
-                if (mine) reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at] = make_float2(m * sl2, l);
+                pf_pair_bar(pid);  // s_row is written again by the next segment
             }
             tc::fence_before();
             tc::mbar_arrive(bar(SM::kOEmpty + sid));
         }
     }
-    if (!ok) *s_bad = 1;
+    if (!ok) *s_bad = 1;  // (any thread's)
     tc::fence_before();
     __syncthreads();
     if (tid == 0) w.status[blockIdx.x] = *s_bad;

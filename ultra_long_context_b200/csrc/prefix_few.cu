@@ -230,10 +230,11 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             ok = pf_wait(bar(SM::kQEmpty + q), (use & 1u) ^ 1u);
             if (!ok) break;
             const uint32_t dst = sb + SM::Q + q * SM::QB;
-            for (int r = rsub; r < (g.s.nr + 15) / 16 * 16; r += RPW) {
+            PfQRows at(g.s, d, rsub);
+            for (int r = rsub; r < (g.s.nr + 15) / 16 * 16; r += RPW, at.advance(g.s, d, RPW)) {
                 const bool in = r < g.s.nr;
                 cp_async16_u32(dst + (ch >> 3) * (NR * 128) + tc::sw128(r, ch & 7),
-                               in ? a.q + pf_q_row(g.s, d, a.Hkv, r) * D + ch * 8 : a.q, in ? 16 : 0);
+                               in ? a.q + at.row(g.s, d, a.Hkv) * D + ch * 8 : a.q, in ? 16 : 0);
             }
             pf_cp_async_arrive(bar(SM::kQFull + q));  // fires when this thread's copies have landed
         }

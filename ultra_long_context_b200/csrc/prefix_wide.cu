@@ -56,6 +56,20 @@ static_assert(PfSmem<128>::dyn(256) <= 227 * 1024 && PfSmem<64>::dyn(256) <= 227
 // Do both streams read every tile of the segment, each for rows of its own?
 __device__ __forceinline__ bool pf_both(const PfSeg &s) { return s.nr > kPfTile; }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return reinterpret_cast<float2 &>(r);
+}
+
 // Named barriers of the two warps (64 threads) that share 32 rows.
 __device__ __forceinline__ void pf_pair_bar(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool pf_pair_or(int id, bool v) {
@@ -233,10 +247,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                 const int rows = min(kPfTile, seg.nr - k * kPfTile);
                 const uint32_t dst = sb + SM::Q + q * SM::OP;
                 // (the other rows are nobody's; zeros keep their logits small)
-                for (int r = qw * RPW + rsub; r < kPfTile; r += kPfQWarps * RPW) {
+                PfQRows at(seg, d, k * kPfTile + qw * RPW + rsub);
+                for (int r = qw * RPW + rsub; r < kPfTile; r += kPfQWarps * RPW, at.advance(seg, d, kPfQWarps * RPW)) {
                     const bool in = r < rows;
                     cp_async16_u32(dst + (ch >> 3) * 16384 + tc::sw128(r, ch & 7),
-                                   in ? a.q + pf_q_row(seg, d, a.Hkv, k * kPfTile + r) * D + ch * 8 : a.q, in ? 16 : 0);
+                                   in ? a.q + at.row(seg, d, a.Hkv) * D + ch * 8 : a.q, in ? 16 : 0);
                 }
                 pf_cp_async_arrive(bar(SM::kQFull + q));  // fires when this thread's copies have landed
             }
@@ -265,12 +280,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             const bool starts = both ? u < 2 : u == 0;  // the first to read its Q buffer
             ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS) & 1u);
             if (ok && starts) ok = pf_wait(bar(SM::kQFull + q), (q ? uses1 : uses0) & 1u);
+            if (ok && lane == 0) tc::mbar_arrive(bar(SM::kInfo + sid));  // hands on the page flags that came with K
             // S and P share columns: P of the stream's item before must have been read
             if (ok && issued[sid] > 0) ok = pf_wait(bar(SM::kODone + sid), (issued[sid] - 1) & 1u);
             if (!ok) return;
-            if (lane == 0) tc::mbar_arrive(bar(SM::kInfo + sid));  // hands on the page flags that came with K
             tc::fence_after();
-            tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
+            if (starts) tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
             const uint32_t sq = sb + SM::Q + q * SM::OP, sk = sb + SM::K + ks * SM::OP;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -290,8 +305,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         };
         auto issue_o = [&](const int sid) {
             const int n = tile[sid], vs = n % VS;
-            ok = pf_wait(bar(SM::kPFull + sid), issued[sid] & 1u) && pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
+            // (what is there long before comes first, so that only the wait for P is followed by the products)
+            ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
             if (ok && first[sid] && runs[sid] > 1) ok = pf_wait(bar(SM::kOEmpty + sid), (runs[sid] - 2) & 1u);
+            if (ok) ok = pf_wait(bar(SM::kPFull + sid), issued[sid] & 1u);
             if (!ok) return;
             tc::fence_after();
             const uint32_t sv = sb + SM::V + vs * SM::OP;
@@ -367,36 +384,38 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             for (int t = t0; t < seg.nt; t += dt, ++tiles) {
                 const int n = g.n0 + t, vs = n % VS;
                 const int base = (seg.tile0 + t) * kPfTile;
-                bool good = pf_wait(bar(SM::kInfo + sid), tiles & 1u) && pf_wait(bar(SM::kSFull + sid), tiles & 1u);
-                tc::fence_after();
+                bool good = pf_wait(bar(SM::kInfo + sid), tiles & 1u);
                 const int flags = s_flag[n % kPfFlags];
+                const int vis = (flags >> half) & 1 ? lim - base - 64 * half : 0;  // keys of this half that the row sees
+                const bool edge = __any_sync(0xffffffffu, vis < 64);
+                good = good && pf_wait(bar(SM::kSFull + sid), tiles & 1u);
+                tc::fence_after();
                 if (!good) s_badp[pid - 1] = 1;
                 if (active) {
-                    const int vis = (flags >> half) & 1 ? lim - base - 64 * half : 0;  // keys of this half that the row sees
-                    const bool edge = __any_sync(0xffffffffu, vis < 64);
                     uint32_t pk[32];
                     float sum;
                     // P of this half as bf16 pairs, and its sum
                     auto probs = [&](const float (&x)[64]) {
-                        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        float2 s2[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                        const float2 scale2 = {sl2, sl2}, off2 = {-ms, -ms};
                         if (edge) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                const float p0 = 2 * i < vis ? ex2_approx(fmaf(x[2 * i], sl2, -ms)) : 0.0f;
-                                const float p1 = 2 * i + 1 < vis ? ex2_approx(fmaf(x[2 * i + 1], sl2, -ms)) : 0.0f;
-                                s4[i & 3] += p0 + p1;
-                                pk[i] = pack_bf16x2(p0, p1);
+                                const float2 y = fma2({x[2 * i], x[2 * i + 1]}, scale2, off2);
+                                const float2 p = {2 * i < vis ? ex2_approx(y.x) : 0.0f, 2 * i + 1 < vis ? ex2_approx(y.y) : 0.0f};
+                                s2[i & 1] = add2(s2[i & 1], p);
+                                pk[i] = pack_bf16x2(p.x, p.y);
                             }
                         } else {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                const float p0 = ex2_approx(fmaf(x[2 * i], sl2, -ms));
-                                const float p1 = ex2_approx(fmaf(x[2 * i + 1], sl2, -ms));
-                                s4[i & 3] += p0 + p1;
-                                pk[i] = pack_bf16x2(p0, p1);
+                                const float2 y = fma2({x[2 * i], x[2 * i + 1]}, scale2, off2);
+                                const float2 p = {ex2_approx(y.x), ex2_approx(y.y)};
+                                s2[i & 1] = add2(s2[i & 1], p);
+                                pk[i] = pack_bf16x2(p.x, p.y);
                             }
                         }
-                        sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                        sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
                     };
                     bool high;
                     {

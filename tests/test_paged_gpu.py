@@ -168,8 +168,10 @@ def decode_case(seed, B, H, Hkv, Tq, D, prefix, own, scale=0.0, poison=True, sha
     return q, pool[0].contiguous(), pool[1].contiguous(), ids[:npre].copy(), prefix, table, own, scale
 
 
-def check_decode(q, Kp, Vp, pre, prefix, table, own, scale, squeeze=False, **kw):
+def check_decode(q, Kp, Vp, pre, prefix, table, own, scale, squeeze=False, room=0, **kw):
+    """room: pages that the prefix's table has beyond the prefix (the kernels are chosen by the table's size)."""
     D = q.shape[-1]
+    pre = np.concatenate([pre, np.full(room, -1, np.int32)])
     args = [torch.tensor(x, device=DEV) for x in (pre, [prefix], table, own)]
     out, lse = hsa.hsa_prefix_decode(q.squeeze(2) if squeeze else q, Kp, Vp, args[0], args[1], args[2], args[3], scale=scale, **kw)
     torch.cuda.synchronize()
@@ -217,6 +219,55 @@ DECODES = [
 @pytest.mark.parametrize("case", DECODES)
 def test_prefix_decode_equals_the_plain_form(case):
     check_decode(*decode_case(21, **case))
+
+
+WIDE = 4000   # with a table this long, batches of more than 64 rows per key head take the kernel for wide products
+
+
+@pytest.mark.parametrize("case", [c for c in DECODES if c["B"] * c["H"] * c["Tq"] // c["Hkv"] > 64] + [
+    dict(B=65, H=1, Hkv=1, Tq=1, D=64, prefix=129, own=[2] * 65),
+    dict(B=129, H=2, Hkv=2, Tq=1, D=128, prefix=1, own=[i % 3 - 1 for i in range(129)]),
+    dict(B=100, H=4, Hkv=1, Tq=1, D=128, prefix=64, own=[i % 70 for i in range(100)]),
+    dict(B=86, H=3, Hkv=1, Tq=3, D=64, prefix=1000, own=[i % 5 for i in range(86)]),
+    dict(B=257, H=2, Hkv=1, Tq=1, D=128, prefix=3333, own=[i for i in range(257)]),
+    dict(B=16, H=16, Hkv=1, Tq=1, D=128, prefix=0, own=[3] * 16),
+])
+def test_prefix_decode_of_wide_batches_equals_the_plain_form(case):
+    check_decode(*decode_case(41, **case), room=WIDE)
+
+
+@pytest.mark.parametrize("sharp,scale", [(8.0, 0.0), (1.0, 2.0), (0.02, 0.0)])
+def test_wide_prefix_decode_of_peaked_and_flat_rows(sharp, scale):
+    check_decode(*decode_case(42, B=40, H=8, Hkv=2, Tq=1, D=128, prefix=2500, own=[i for i in range(40)], sharp=sharp, scale=scale), room=WIDE)
+
+
+def test_wide_prefix_decode_maxima_that_keep_growing():
+    """Rows of which some move their reference in every tile while others of the same tile do not."""
+    for D, flip in ((64, False), (128, True), (128, False)):
+        q, Kp, Vp, pre, prefix, table, own, scale = decode_case(43, B=90, H=2, Hkv=2, Tq=1, D=D, prefix=1500, own=[1] * 90, poison=False)
+        size = torch.linspace(0.0, 40.0, len(pre), device=DEV)
+        if flip:
+            size = size.flip(0)
+        Kp[torch.tensor(pre.astype(np.int64), device=DEV)] = (q[::2].float().mean(0)[:, 0][None, :, None] * 8 * size[:, None, None, None]).to(BF16)
+        check_decode(q, Kp, Vp, pre, prefix, table, own, scale, room=WIDE)
+
+
+def test_wide_prefix_decode_leaves_out_bad_pages():
+    q, Kp, Vp, pre, prefix, table, own, scale = decode_case(44, B=70, H=4, Hkv=2, Tq=1, D=128, prefix=1900, own=[5] * 70)
+    pre[[0, 1, 5, 14, 29]] = [-1, Kp.shape[0], Kp.shape[0], 2**31 - 1, -9]
+    check_decode(q, Kp, Vp, pre, prefix, table, own, scale, room=WIDE)
+    pre[:] = -1
+    check_decode(q, Kp, Vp, pre, prefix, table, own, scale, room=WIDE)
+
+
+def test_wide_and_few_row_kernels_back_to_back():
+    """Many calls without a pause, the two kernels of each overlapping; the same answer every time."""
+    q, Kp, Vp, pre, prefix, table, own, scale = decode_case(45, B=48, H=16, Hkv=2, Tq=1, D=128, prefix=9000, own=[1 + 61 * i % 700 for i in range(48)])
+    args = [torch.tensor(x, device=DEV) for x in (np.concatenate([pre, np.full(WIDE, -1, np.int32)]), [prefix], table, own)]
+    got = [hsa.hsa_prefix_decode(q, Kp, Vp, *args) for _ in range(60)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, got[0][0]) and torch.equal(l, got[0][1]) for o, l in got)
+    check_decode(q, Kp, Vp, pre, prefix, table, own, scale, room=WIDE)
 
 
 @pytest.mark.parametrize("sharp,scale", [(8.0, 0.0), (1.0, 2.0), (0.02, 0.0)])

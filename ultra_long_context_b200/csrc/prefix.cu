@@ -12,14 +12,14 @@ constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const PrefixArgs a, const PfDims d, const PfWork w,
-                                                                     int ctas, bool wide, bool few, int wpr) {
+                                                                     int ctas, int wpr) {
     __shared__ float s_acc[kPfJoinWarps][D], s_M[kPfJoinWarps], s_L[kPfJoinWarps];
     pdl_launch_dependents();  // what follows may set itself up; it waits for this grid's end before it reads
     pdl_wait();
     const int lane = threadIdx.x & 31;
     if (blockIdx.x == 0 && threadIdx.x < 32) {
         int bad = 0;
-        for (int i = lane; i < ctas; i += 32) bad |= (wide ? w.status[i] : 0) | (few ? w.status[kPfCtas + i] : 0);
+        for (int i = lane; i < ctas; i += 32) bad |= (d.wide ? w.status[i] : 0) | w.status[kPfCtas + i];
         bad = __any_sync(0xffffffffu, bad != 0);
         if (lane == 0) *w.err = bad;
     }
@@ -46,19 +46,19 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
     int64_t x0 = 0;
     if (live) {
         const int rp = b * d.Ro + ro;
-        rg = rp / kPfRows;
-        rr = rp % kPfRows;
-        nr = min(kPfRows, d.Rp - rg * kPfRows);
+        rg = rp / d.gp;
+        rr = rp - rg * d.gp;
+        nr = min(d.gp, d.Rp - rg * d.gp);
         per = nr > kPfTile ? 1 : 2;
         np = p.items > 0 ? p.nsplit : 0;
         if (wt > 0) {
-            const int hr = h * d.Rgo + ro / kPfRows;
+            const int hr = h * d.Rgo + ro / kPfFewRows;
             x0 = cum * hr_n + (int64_t)hr * wt;
             i0 = po.cta_of(x0);
             no = po.cta_of(x0 + wt - 1) - i0 + 1;
             obase = b * hr_n + hr;
-            orr = ro % kPfRows;
-            onr = min(kPfRows, d.Ro - ro / kPfRows * kPfRows);
+            orr = ro % kPfFewRows;
+            onr = min(kPfFewRows, d.Ro - ro / kPfFewRows * kPfFewRows);
         }
     }
     const int total = np * per + 2 * no;
@@ -72,10 +72,6 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
         }
         const int i = i0 + (idx - np * per) / 2, st = (idx - np * per) & 1;
         const int nt = pf_tile_at(min(po.start(i + 1), x0 + wt) - x0) - pf_tile_at(max(po.start(i), x0) - x0);
-        if (onr > kPfTile) {
-            if (nt <= 0 || st > 0) return -1;
-            return (int64_t)(obase + i) * d.strideO + orr;
-        }
         if (st >= nt) return -1;
         return (int64_t)(obase + i) * d.strideO + st * onr + orr;
     };
@@ -174,19 +170,17 @@ static size_t pf_layout(void *ws, const PfDims &d, int D, PfWork *w) {
 size_t prefix_workspace(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages, int max_pages) {
     (void)max_pages;
     PfWork w{};
-    return pf_layout(nullptr, PfDims(B, H, Hkv, Tq, max_prefix_pages), D, &w);
+    return pf_layout(nullptr, PfDims(B, H, Hkv, Tq, D, max_prefix_pages), D, &w);
 }
 
 cudaError_t launch_prefix_decode(const PrefixArgs &a, cudaStream_t s) {
-    const PfDims d(a.B, a.H, a.Hkv, a.Tq, a.max_prefix_pages);
+    const PfDims d(a.B, a.H, a.Hkv, a.Tq, a.D, a.max_prefix_pages);
     PfWork w{};
     pf_layout(a.workspace, d, a.D, &w);
     const int sms = sm_count(), ctas = sms < kPfCtas ? sms : kPfCtas;
-    // rows of the prefix's segments (Rp) and of the requests' own (Ro <= Rp): few or many
-    const bool wide = d.Rp > kPfFewRows, few = d.Ro <= kPfFewRows;
     cudaError_t e = cudaSuccess;
-    if (wide) e = launch_prefix_wide(a, d, w, ctas, true, !few, s);
-    if (e == cudaSuccess && few) e = launch_prefix_few(a, d, w, ctas, !wide, true, wide, s);
+    if (d.wide) e = launch_prefix_wide(a, d, w, ctas, s);
+    if (e == cudaSuccess) e = launch_prefix_few(a, d, w, ctas, s);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.B * a.H * a.Tq;
     int wpr = kPfJoinWarps;
@@ -194,8 +188,8 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, cudaStream_t s) {
     const int per_block = kPfJoinWarps / wpr;
     const unsigned grid = (unsigned)((rows + per_block - 1) / per_block);
     HSA_PROF("prefix_join", s);
-    return a.D == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wide, few, wpr)
-                      : launch_pdl(prefix_join_kernel<64>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wide, few, wpr);
+    return a.D == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wpr)
+                      : launch_pdl(prefix_join_kernel<64>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wpr);
 }
 
 }  // namespace hsa

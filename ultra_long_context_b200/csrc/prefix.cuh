@@ -3,10 +3,10 @@
 //
 // For a query row q and its visible keys, out = sum_k exp(s_k - m) v_k / sum_k exp(s_k - m) with
 // s = scale q.k. The keys are cut into tiles of 128 (two pages). A SEGMENT is a run of tiles of one page list
-// (the prefix's, or a request's own) for one key head and up to 256 query rows: all rows of the batch that read
-// the key head, for the prefix; the request's own rows, for its own pages. Over a segment a row keeps its running
-// maximum m, sum l = sum exp(s - m) and output O = sum exp(s - m) v, and the segments' (m, l, O) of a row are
-// joined at the end. So every prefix page is read once for up to 256 rows, and both kinds of work are the same.
+// (the prefix's, or a request's own) for one key head and up to 64 or 256 query rows: rows of the whole batch that
+// read the key head, for the prefix; the request's own rows, for its own pages. Over a segment a row keeps a reference m
+// (see prefix_few.cu), its sum l = sum exp(s - m) and output O = sum exp(s - m) v, and the segments' (m, l, O) of a row
+// are joined at the end. So a prefix page is read once for as many rows, and both kinds of work are the same.
 #pragma once
 
 #include <cuda.h>
@@ -17,8 +17,8 @@
 namespace hsa {
 
 constexpr int kPfTile = 128;      // keys per tile = 2 pages
-constexpr int kPfRows = 256;      // rows per segment at most
-constexpr int kPfFewRows = 64;    // segments of up to this many rows go to the few-rows kernel
+constexpr int kPfFewRows = 64;    // rows per segment at most: in the few-rows kernel,
+constexpr int kPfWideRows = 256;  // in the wide kernel
 constexpr int kPfCtas = 148;      // at most: one per SM; the workspace is sized for it
 constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per head and row group)
 // Costs in half tiles: a tile, and what a segment's start and end take beside its tiles
@@ -45,18 +45,31 @@ struct PfPlan {
 
 // Sizes that follow from the call's arguments alone.
 struct PfDims {
-    int Rp, Rgp;           // prefix rows per key head, in groups of kPfRows
-    int Ro, Rgo;           // own rows per request and key head
-    int strideP, strideO;  // rows of one segment's partials (two streams of few rows keep one each)
+    bool wide;             // the prefix goes to the wide kernel (the requests' own pages to the few-rows kernel always)
+    int Rp, gp, Rgp;       // prefix rows per key head, in Rgp groups of gp
+    int Ro, Rgo;           // own rows per request and key head, in groups of kPfFewRows
+    int strideP, strideO;  // rows of one segment's partials (two streams that share rows keep one each)
     int max_items, max_slots, blocks;  // blocks: of 32 requests
-    PfDims(int B, int H, int Hkv, int Tq, int max_prefix_pages) {
+    // Which kernel ends the prefix sooner? A tile of 128 keys takes the few-rows kernel 1.15 us (D = 128; half that with
+    // D = 64: its bytes) for 64 rows, the wide one 2.3 us for 256, and that is a launch of its own, 12 us before the
+    // first product ends. Both are measured; the tiles are those of the table, since the length is not known here.
+    static bool pf_wide(int Rp, int Hkv, int D, int tiles) {
+        const double per_sm = (double)Hkv * tiles / kPfCtas;
+        const double few = per_sm * ((Rp + kPfFewRows - 1) / kPfFewRows) * (D == 128 ? 1.15 : 0.6);
+        const double wide = 12.0 + per_sm * ((Rp + kPfWideRows - 1) / kPfWideRows) * 2.3;
+        return Rp > kPfFewRows && wide < few;
+    }
+    PfDims(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages) {
         Ro = H / Hkv * Tq;
         Rp = B * Ro;
-        Rgp = (Rp + kPfRows - 1) / kPfRows;
-        Rgo = (Ro + kPfRows - 1) / kPfRows;
-        strideP = Rp <= kPfTile ? 2 * Rp : kPfRows;
-        strideO = Ro <= kPfTile ? 2 * Ro : kPfRows;
-        const int units = Hkv * Rgp, tiles = (max_prefix_pages + 1) / 2;
+        const int tiles = (max_prefix_pages + 1) / 2;
+        wide = pf_wide(Rp, Hkv, D, tiles);
+        gp = wide ? kPfWideRows : kPfFewRows;
+        Rgp = (Rp + gp - 1) / gp;
+        Rgo = (Ro + kPfFewRows - 1) / kPfFewRows;
+        strideP = wide ? kPfWideRows : 2 * (Rp < kPfFewRows ? Rp : kPfFewRows);
+        strideO = 2 * (Ro < kPfFewRows ? Ro : kPfFewRows);
+        const int units = Hkv * Rgp;
         int ns = kPfItems / units;
         ns = ns < 1 ? 1 : ns;
         ns = ns < tiles ? ns : tiles;
@@ -134,8 +147,8 @@ struct PfWalk {
             const int units = a.Hkv * d.Rgp, k = item / units, u = item - k * units;
             s.h = d.Rgp == 1 ? u : u / d.Rgp;
             s.b = -1;
-            s.r0 = (u - s.h * d.Rgp) * kPfRows;
-            s.nr = min(kPfRows, d.Rp - s.r0);
+            s.r0 = (u - s.h * d.Rgp) * d.gp;
+            s.nr = min(d.gp, d.Rp - s.r0);
             s.tile0 = k * p.run;
             s.nt = min(p.run, p.tiles - s.tile0);
             s.len = p.P;
@@ -166,8 +179,8 @@ struct PfWalk {
             if (t1 <= t0) continue;
             s.b = 32 * lo + l;
             s.h = hr / d.Rgo;
-            s.r0 = hr % d.Rgo * kPfRows;
-            s.nr = min(kPfRows, d.Ro - s.r0);
+            s.r0 = hr % d.Rgo * kPfFewRows;
+            s.nr = min(kPfFewRows, d.Ro - s.r0);
             s.tile0 = t0;
             s.nt = t1 - t0;
             s.part = s.b * hr_n + hr + (int)blockIdx.x;
@@ -180,19 +193,20 @@ struct PfWalk {
 
 // The rows of a segment in q / out, walked upwards (a division per row made the copy of 256 rows take 20 us).
 struct PfQRows {
-    int request, rem;  // of the row at hand
-    __device__ PfQRows(const PfSeg &s, const PfDims &d, int rr) {
-        const int r = s.r0 + rr;
-        request = s.b < 0 ? r / d.Ro : s.b;
+    int row, rem, wrap, jump;  // the row at hand; its place among its request's; where the next request's begin, and how far
+    __device__ PfQRows(const PfSeg &s, const PfDims &d, int Hkv, int rr) {  // rows stay below 2^31 / D
+        const int r = s.r0 + rr, request = s.b < 0 ? r / d.Ro : s.b;
         rem = s.b < 0 ? r - request * d.Ro : r;
+        row = (request * Hkv + s.h) * d.Ro + rem;
+        wrap = s.b < 0 ? d.Ro : INT32_MAX;
+        jump = (Hkv - 1) * d.Ro;
     }
-    __device__ int64_t row(const PfSeg &s, const PfDims &d, int Hkv) const { return (int64_t)(request * Hkv + s.h) * d.Ro + rem; }
-    __device__ void advance(const PfSeg &s, const PfDims &d, int by) {
+    __device__ void advance(int by) {
+        row += by;
         rem += by;
-        if (s.b >= 0) return;
-        while (rem >= d.Ro) {
-            rem -= d.Ro;
-            ++request;
+        while (rem >= wrap) {
+            rem -= wrap;
+            row += jump;
         }
     }
 };
@@ -312,11 +326,9 @@ __device__ __forceinline__ void pf_cp_async_arrive(uint32_t mbar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(mbar) : "memory");
 }
 
-// The kernels (prefix_few.cu, prefix_wide.cu). prefix / own: the kinds of segments a launch takes; follows: it is
-// launched as the dependent of the other kernel, whose results it does not need.
-cudaError_t launch_prefix_few(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
-                              bool follows, cudaStream_t s);
-cudaError_t launch_prefix_wide(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
-                               cudaStream_t s);
+// The kernels (prefix_few.cu, prefix_wide.cu). With d.wide the few-rows kernel is launched as the dependent of the wide
+// one, whose results it does not need.
+cudaError_t launch_prefix_few(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, cudaStream_t s);
+cudaError_t launch_prefix_wide(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, cudaStream_t s);
 
 }  // namespace hsa

@@ -77,8 +77,6 @@ __device__ __forceinline__ void fw_bar(int id) { asm volatile("bar.sync %0, 128;
 
 template <int D, int NR>
 __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixArgs a, const PfDims d, const PfWork w,
-                                                                   const bool take_prefix, const bool take_own,
-                                                                   const bool follows,
                                                                    const __grid_constant__ CUtensorMap tmK,
                                                                    const __grid_constant__ CUtensorMap tmV) {
     using SM = FwSmem<D, NR>;
@@ -131,9 +129,9 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *reinterpret_cast<uint32_t *>(s + SM::MISC);
-    if (!follows) pdl_wait();  // what precedes the call in its stream is visible from here on
-    pf_schedule<kFwThreads>(a, d, take_prefix, take_own, s_plan, s_bcum);
-    pf_publish<kFwThreads>(d, take_prefix, take_own, s_plan, s_bcum, w);
+    if (!d.wide) pdl_wait();  // what precedes the call in its stream is visible from here on
+    pf_schedule<kFwThreads>(a, d, !d.wide, true, s_plan, s_bcum);
+    pf_publish<kFwThreads>(d, !d.wide, true, s_plan, s_bcum, w);
     bool ok = true;
 
     // the next announced segment; nr = 0 ends the walk
@@ -230,11 +228,11 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             ok = pf_wait(bar(SM::kQEmpty + q), (use & 1u) ^ 1u);
             if (!ok) break;
             const uint32_t dst = sb + SM::Q + q * SM::QB;
-            PfQRows at(g.s, d, rsub);
-            for (int r = rsub; r < (g.s.nr + 15) / 16 * 16; r += RPW, at.advance(g.s, d, RPW)) {
+            PfQRows at(g.s, d, a.Hkv, rsub);
+            for (int r = rsub; r < (g.s.nr + 15) / 16 * 16; r += RPW, at.advance(RPW)) {
                 const bool in = r < g.s.nr;
                 cp_async16_u32(dst + (ch >> 3) * (NR * 128) + tc::sw128(r, ch & 7),
-                               in ? a.q + at.row(g.s, d, a.Hkv) * D + ch * 8 : a.q, in ? 16 : 0);
+                               in ? a.q + (int64_t)at.row * D + ch * 8 : a.q, in ? 16 : 0);
             }
             pf_cp_async_arrive(bar(SM::kQFull + q));  // fires when this thread's copies have landed
         }
@@ -242,13 +240,16 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         cp_async_wait<0>();  // nothing in flight when the CTA exits
     } else if (warp == kFwMmaWarp) {
         // ================= MMA issuer: the whole warp runs the loop, one elected lane issues =================
-        PfNote g;
         bool have = false, end = false;   // is there a segment at next_s; is there none any more
-        int t = 0, q = 0;                 // of next_s: tile of the segment; Q buffer
-        uint32_t quse = 0;
+        int t = 0, nt = 0, q = 0;         // of next_s: tile of the segment, its tiles, Q buffer
+        uint32_t quse = 0, id_s = 0;
         int next_s = 0, next_o = 0;       // tiles
-        uint32_t idesc[2] = {0, 0}, tiles[2] = {0, 0}, runs[2] = {0, 0};
-        bool first[2] = {false, false};   // does tile next_o (of the parity) begin a run of its stream in its segment?
+        // of the even and odd tiles: the instruction of the tile at O^T, whether it begins a run in its segment, O^T
+        // products so far, runs begun
+        struct Stream {
+            uint32_t id = 0, tiles = 0, runs = 0;
+            bool first = false;
+        } st0, st1;
         int k_seen = 0, v_seen = 0, k_slot = 0, v_slot = 0;  // fillings of the slots observed, in order
         uint32_t k_par = 0, v_par = 0, idle = 0;
         while (true) {
@@ -260,19 +261,26 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             if (lane == 1) b = SM::kKFull + k_slot, par = k_par;
             if (lane == 2) b = SM::kVFull + v_slot, par = v_par;
             if (lane == 3) b = SM::kQFull + q, par = quse;
-            if (lane == 4) b = SM::kPFull, par = tiles[0];
-            if (lane == 5) b = SM::kPFull + 1, par = tiles[1];
-            if (lane == 6) b = SM::kOEmpty, par = runs[0];
-            if (lane == 7) b = SM::kOEmpty + 1, par = runs[1];
+            if (lane == 4) b = SM::kPFull, par = st0.tiles;
+            if (lane == 5) b = SM::kPFull + 1, par = st1.tiles;
+            if (lane == 6) b = SM::kOEmpty, par = st0.runs;
+            if (lane == 7) b = SM::kOEmpty + 1, par = st1.runs;
             const unsigned hit = __ballot_sync(0xffffffffu, lane < 8 && tc::mbar_test(bar(b), par & 1u));
             __syncwarp();  // what the probing lanes acquired holds for the issuing one
+            bool q_in = hit & 8u;  // Q of the segment (one taken just now is asked for in the next round)
             if (!have && !end && (hit & 1u)) {
                 q = seg_no & 1;
                 quse = (uint32_t)(seg_no >> 1);
-                take(g);
-                have = g.s.nr > 0;
+                const int nr = s_ring[slot].s.nr;
+                nt = s_ring[slot].s.nt;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar(SM::kSegEmpty + slot));
+                ++seg_no;
+                have = nr > 0;
                 end = !have;
+                id_s = tc::idesc_bf16(128, (nr + 15) / 16 * 16, 0, 0);
                 t = 0;
+                q_in = false;
                 progress = true;
             }
             if (end && next_o == next_s) break;
@@ -284,61 +292,58 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 ++v_seen;
                 if (++v_slot == VS) v_slot = 0, v_par ^= 1u;
             }
-#pragma unroll
-            for (int sid = 0; sid < 2; ++sid) {  // O^T(next_o)
-                if (next_o >= next_s || (next_o & 1) != sid || next_o >= v_seen) continue;
-                if (!(hit & (16u << sid))) continue;
-                if (first[sid] && runs[sid] > 1 && !(hit & (64u << sid))) continue;
+            auto o_step = [&](Stream &c, const int sid) {  // O^T(next_o)
+                if (!(hit & (16u << sid)) || (c.first && c.runs > 1 && !(hit & (64u << sid)))) return;
                 tc::fence_after();
                 const int vs = next_o % VS;
-                const uint32_t sv = sb + SM::V + vs * SM::OP, sp = sb + SM::P + sid * SM::PB;
-                const uint32_t id = idesc[sid] | (1u << 15) | (1u << 16);  // A and B MN-major
                 // the second 64 rows of A: dims 64 .. 127, or, with D = 64, whatever follows the tile (lanes that are not read)
+                const uint64_t dv = tc::desc_mnmajor(sb + SM::V + vs * SM::OP, 16384);
+                const uint64_t dp = tc::desc_mnmajor(sb + SM::P + sid * SM::PB, 16384);
+                const uint32_t id = c.id | (1u << 15) | (1u << 16);  // A and B MN-major
 #pragma unroll
-                for (int k = 0; k < kPfTile / 16; ++k)
-                    tc::mma_bf16_ss_w(tmem + SM::O_COL + sid * 64, tc::desc_mnmajor(sv + k * 2048, 16384),
-                                      tc::desc_mnmajor(sp + k * 2048, 16384), id, first[sid] && k == 0 ? 0u : 1u);
+                for (int k = 0; k < kPfTile / 16; ++k)  // (a descriptor's low bits are its address / 16)
+                    tc::mma_bf16_ss_w(tmem + SM::O_COL + sid * 64, dv + (uint64_t)k * (2048 >> 4), dp + (uint64_t)k * (2048 >> 4), id,
+                                      c.first && k == 0 ? 0u : 1u);
                 tc::commit_w(bar(SM::kODone + sid));
                 tc::commit_w(bar(SM::kVEmpty + vs));
-                first[sid] = false;
-                ++tiles[sid];
+                c.first = false;
+                ++c.tiles;
                 ++next_o;
                 progress = true;
+            };
+            if (next_o < next_s && next_o < v_seen) {
+                if (next_o & 1) o_step(st1, 1);
+                else o_step(st0, 0);
             }
-            // Q of the segment, if the probe was of it (a segment taken just now is asked for in the next round)
-            const bool q_in = (hit & 8u) && !progress;
             // S^T(next_s): its buffer is free once P^T of the tile two before is written. The V filling before this
             // tile's in its slot has landed, so that a softmax wait on the slot's parity, which follows S^T, is exact
-            if (have && next_s < next_o + 2 && next_s < k_seen && next_s - VS < v_seen &&
-                (t > 0 || q_in)) {
+            auto s_step = [&](Stream &c, const int sid) {
                 tc::fence_after();
-                tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
+                if (t == 0) tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
                 const int ks = next_s % KS;
-                const uint32_t sk = sb + SM::K + ks * SM::OP, sq = sb + SM::Q + q * SM::QB;
-                const uint32_t id = tc::idesc_bf16(128, (g.s.nr + 15) / 16 * 16, 0, 0);
+                const uint64_t dk = tc::desc_kmajor(sb + SM::K + ks * SM::OP), dq = tc::desc_kmajor(sb + SM::Q + q * SM::QB);
+                if (lane == 0) tc::mbar_arrive(bar(SM::kInfo + sid));  // hands on the page flags that came with K
 #pragma unroll
-                for (int sid = 0; sid < 2; ++sid) {
-                    if ((next_s & 1) != sid) continue;
-                    if (lane == 0) tc::mbar_arrive(bar(SM::kInfo + sid));  // hands on the page flags that came with K
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * 64,
-                                          tc::desc_kmajor(sk + (k >> 2) * 16384 + (k & 3) * 32),
-                                          tc::desc_kmajor(sq + (k >> 2) * (NR * 128) + (k & 3) * 32), id, k > 0 ? 1u : 0u);
-                    tc::commit_w(bar(SM::kSFull + sid));
-                    idesc[sid] = id;
-                    if (t < 2) {
-                        first[sid] = true;
-                        ++runs[sid];
-                    }
-                }
+                for (int k = 0; k < D / 16; ++k)
+                    tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * 64, dk + ((uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                                      dq + ((uint64_t)((k >> 2) * (NR * 128) + (k & 3) * 32) >> 4), id_s, k > 0 ? 1u : 0u);
+                tc::commit_w(bar(SM::kSFull + sid));
                 tc::commit_w(bar(SM::kKEmpty + ks));
-                if (++t == g.s.nt) {
+                c.id = id_s;
+                if (t < 2) {
+                    c.first = true;
+                    ++c.runs;
+                }
+                if (++t == nt) {
                     tc::commit_w(bar(SM::kQEmpty + q));
                     have = false;
                 }
                 ++next_s;
                 progress = true;
+            };
+            if (have && next_s < next_o + 2 && next_s < k_seen && next_s - VS < v_seen && (t > 0 || q_in)) {
+                if (next_s & 1) s_step(st1, 1);
+                else s_step(st0, 0);
             }
             if (progress) {
                 idle = 0;
@@ -402,33 +407,27 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     __syncwarp();
                 }
                 const bool page_ok = (flags >> (r >> 6)) & 1;
-                float y[NR];
-                // y = logit * log2(e) - m, -inf where the row does not see the key; false where one is too far above m
-                auto logits = [&]() {
-                    float top = -INFINITY;
+                // of 16 rows: y = logit * log2(e) - m, -inf where the row does not see the key
+                auto logits = [&](float (&y)[16], const int c) {
+                    tc::tmem_ld16(tS + 16 * c, y);
 #pragma unroll
-                    for (int c = 0; c < NR / 16; ++c) {
-                        if (c >= nc) break;
-                        float x[16];
-                        tc::tmem_ld16(tS + 16 * c, x);
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 m4 = *reinterpret_cast<const float4 *>(ms + 16 * c + i);
-                            y[16 * c + i] = fmaf(x[i], sl2, -m4.x);
-                            y[16 * c + i + 1] = fmaf(x[i + 1], sl2, -m4.y);
-                            y[16 * c + i + 2] = fmaf(x[i + 2], sl2, -m4.z);
-                            y[16 * c + i + 3] = fmaf(x[i + 3], sl2, -m4.w);
-                        }
-                        if (edge) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (!(page_ok && base + r < lims[16 * c + i])) y[16 * c + i] = -INFINITY;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) top = fmaxf(top, y[16 * c + i]);
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 m4 = *reinterpret_cast<const float4 *>(ms + 16 * c + i);
+                        y[i] = fmaf(y[i], sl2, -m4.x);
+                        y[i + 1] = fmaf(y[i + 1], sl2, -m4.y);
+                        y[i + 2] = fmaf(y[i + 2], sl2, -m4.z);
+                        y[i + 3] = fmaf(y[i + 3], sl2, -m4.w);
                     }
-                    return top <= kFwGrow;
+                    if (edge) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (!(page_ok && base + r < lims[16 * c + i])) y[i] = -INFINITY;
+                    }
                 };
+                // with up to 32 rows the logits stay in registers from the vote to the exponentials; those of 64 rows
+                // beside their sums would not, and are read from TMEM again
+                constexpr bool KEEP = NR <= 32;
+                float y[KEEP ? NR / 16 : 1][16];
                 if (t == t0) {  // the references: the first key, or the 65th where the first page is bad
                     const int lead = flags & 1 ? 0 : 64;
                     if (r >> 5 == lead >> 5 && good) {
@@ -447,10 +446,20 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     }
                     fw_bar(bid);
                 }
-                bool high = false;
-                if (good) high = !logits();
-                else s_bad[sid] = 1;
-                const bool any = fw_bar_or(bid, high);
+                float top = -INFINITY;
+                if (good) {
+#pragma unroll
+                    for (int c = 0; c < NR / 16; ++c) {
+                        if (c >= nc) break;
+                        float(&yc)[16] = y[KEEP ? c : 0];
+                        logits(yc, c);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) top = fmaxf(top, yc[i]);
+                    }
+                } else {
+                    s_bad[sid] = 1;
+                }
+                const bool any = fw_bar_or(bid, top > kFwGrow);
                 if (s_bad[sid]) {
                     ok = false;
                     break;
@@ -499,19 +508,27 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                             tc::tmem_st16(tO + 16 * c, u);
                         }
                     }
-                    logits();
+                    if constexpr (KEEP) {
+#pragma unroll
+                        for (int c = 0; c < NR / 16; ++c) {
+                            if (c >= nc) break;
+                            logits(y[c], c);
+                        }
+                    }
                     fw_bar(bid);  // the scratch has been read: P^T may go there
                 }
 #pragma unroll
                 for (int c = 0; c < NR / 16; ++c) {
                     if (c >= nc) break;
+                    float(&yc)[16] = y[KEEP ? c : 0];
+                    if constexpr (!KEEP) logits(yc, c);
 #pragma unroll
                     for (int hv = 0; hv < 2; ++hv) {
                         uint32_t pk[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int e = 16 * c + 8 * hv + 2 * i;
-                            const float p0 = ex2_approx(y[e]), p1 = ex2_approx(y[e + 1]);
+                            const float p0 = ex2_approx(yc[8 * hv + 2 * i]), p1 = ex2_approx(yc[8 * hv + 2 * i + 1]);
                             l[e] += p0;
                             l[e + 1] += p1;
                             pk[i] = pack_bf16x2(p0, p1);
@@ -573,7 +590,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     if (!ok) s_bad[2] = 1;
     tc::fence_before();
     __syncthreads();
-    if (follows) pdl_wait();  // the kernel before, whose partials the join reads, too
+    if (d.wide) pdl_wait();  // the kernel before, whose partials the join reads, too
     pdl_launch_dependents();
     if (tid == 0) w.status[kPfCtas + blockIdx.x] = s_bad[0] | s_bad[1] | s_bad[2];
     if (warp == kFwMmaWarp) {
@@ -583,8 +600,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
 }
 
 template <int D, int NR>
-static cudaError_t launch_few(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
-                              bool follows, cudaStream_t s) {
+static cudaError_t launch_few(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, cudaStream_t s) {
     CUtensorMap tk, tv;
     const uint64_t rows = (uint64_t)a.num_pages * a.Hkv * kChunk;
     if (!make_tmap_bf16(&tk, a.Kp, rows, D, kChunk) || !make_tmap_bf16(&tv, a.Vp, rows, D, kChunk))
@@ -593,19 +609,18 @@ static cudaError_t launch_few(const PrefixArgs &a, const PfDims &d, const PfWork
     cudaError_t e = allow_smem<prefix_few_kernel<D, NR>>(smem);
     if (e != cudaSuccess) return e;
     HSA_PROF("prefix_few", s);
-    return launch_pdl(prefix_few_kernel<D, NR>, dim3(ctas), dim3(kFwThreads), smem, s, a, d, w, prefix, own, follows, tk, tv);
+    return launch_pdl(prefix_few_kernel<D, NR>, dim3(ctas), dim3(kFwThreads), smem, s, a, d, w, tk, tv);
 }
 
-cudaError_t launch_prefix_few(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
-                              bool follows, cudaStream_t s) {
-    const int rows = prefix ? d.Rp : d.Ro;  // Rp >= Ro
+cudaError_t launch_prefix_few(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, cudaStream_t s) {
+    const int rows = d.wide ? d.Ro : d.Rp;  // of the largest segment, or more; Rp >= Ro
     if (a.D == 128)
-        return rows <= 16   ? launch_few<128, 16>(a, d, w, ctas, prefix, own, follows, s)
-               : rows <= 32 ? launch_few<128, 32>(a, d, w, ctas, prefix, own, follows, s)
-                            : launch_few<128, 64>(a, d, w, ctas, prefix, own, follows, s);
-    return rows <= 16   ? launch_few<64, 16>(a, d, w, ctas, prefix, own, follows, s)
-           : rows <= 32 ? launch_few<64, 32>(a, d, w, ctas, prefix, own, follows, s)
-                        : launch_few<64, 64>(a, d, w, ctas, prefix, own, follows, s);
+        return rows <= 16   ? launch_few<128, 16>(a, d, w, ctas, s)
+               : rows <= 32 ? launch_few<128, 32>(a, d, w, ctas, s)
+                            : launch_few<128, 64>(a, d, w, ctas, s);
+    return rows <= 16   ? launch_few<64, 16>(a, d, w, ctas, s)
+           : rows <= 32 ? launch_few<64, 32>(a, d, w, ctas, s)
+                        : launch_few<64, 64>(a, d, w, ctas, s);
 }
 
 }  // namespace hsa

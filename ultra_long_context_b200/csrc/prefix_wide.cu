@@ -87,7 +87,6 @@ __device__ __forceinline__ bool pf_pair_or(int id, bool v) {
 
 template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const PrefixArgs a, const PfDims d, const PfWork w,
-                                                                    const bool take_prefix, const bool take_own,
                                                                       const __grid_constant__ CUtensorMap tmK,
                                                                       const __grid_constant__ CUtensorMap tmV) {
     using SM = PfSmem<D>;
@@ -141,8 +140,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     const uint32_t tmem = *reinterpret_cast<uint32_t *>(s + SM::TMEM);
     pdl_wait();  // what precedes the call in its stream is visible from here on
     pdl_launch_dependents();  // the few-rows kernel may come in as SMs fall free; the join waits for this grid's end
-    pf_schedule<kPfThreads>(a, d, take_prefix, take_own, s_plan, s_bcum);
-    pf_publish<kPfThreads>(d, take_prefix, take_own, s_plan, s_bcum, w);
+    pf_schedule<kPfThreads>(a, d, true, false, s_plan, s_bcum);
+    pf_publish<kPfThreads>(d, true, false, s_plan, s_bcum, w);
     bool ok = true;
 
     int seg_no = 0;  // the next announced segment
@@ -247,11 +246,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                 const int rows = min(kPfTile, seg.nr - k * kPfTile);
                 const uint32_t dst = sb + SM::Q + q * SM::OP;
                 // (the other rows are nobody's; zeros keep their logits small)
-                PfQRows at(seg, d, k * kPfTile + qw * RPW + rsub);
-                for (int r = qw * RPW + rsub; r < kPfTile; r += kPfQWarps * RPW, at.advance(seg, d, kPfQWarps * RPW)) {
+                PfQRows at(seg, d, a.Hkv, k * kPfTile + qw * RPW + rsub);
+                for (int r = qw * RPW + rsub; r < kPfTile; r += kPfQWarps * RPW, at.advance(kPfQWarps * RPW)) {
                     const bool in = r < rows;
                     cp_async16_u32(dst + (ch >> 3) * 16384 + tc::sw128(r, ch & 7),
-                                   in ? a.q + at.row(seg, d, a.Hkv) * D + ch * 8 : a.q, in ? 16 : 0);
+                                   in ? a.q + (int64_t)at.row * D + ch * 8 : a.q, in ? 16 : 0);
                 }
                 pf_cp_async_arrive(bar(SM::kQFull + q));  // fires when this thread's copies have landed
             }
@@ -286,12 +285,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             if (!ok) return;
             tc::fence_after();
             if (starts) tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
-            const uint32_t sq = sb + SM::Q + q * SM::OP, sk = sb + SM::K + ks * SM::OP;
+            const uint64_t dq = tc::desc_kmajor(sb + SM::Q + q * SM::OP), dk = tc::desc_kmajor(sb + SM::K + ks * SM::OP);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
-                tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * kPfTile, tc::desc_kmajor(sq + off), tc::desc_kmajor(sk + off),
-                                  idesc_s, k > 0 ? 1u : 0u);
+            for (int k = 0; k < D / 16; ++k) {  // (a descriptor's low bits are its address / 16)
+                const uint64_t off = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * kPfTile, dq + off, dk + off, idesc_s, k > 0 ? 1u : 0u);
             }
             tc::commit_w(bar(SM::kSFull + sid));
             tile[sid] = n;
@@ -311,11 +309,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             if (ok) ok = pf_wait(bar(SM::kPFull + sid), issued[sid] & 1u);
             if (!ok) return;
             tc::fence_after();
-            const uint32_t sv = sb + SM::V + vs * SM::OP;
+            const uint64_t dv = tc::desc_mnmajor(sb + SM::V + vs * SM::OP, 16384);
 #pragma unroll
             for (int k = 0; k < kPfTile / 16; ++k)  // a page's P stands where its S began
                 tc::mma_bf16_ts_w(tmem + SM::O_COL + sid * D, tmem + SM::S_COL + sid * kPfTile + (k >> 2) * 64 + (k & 3) * 8,
-                                  tc::desc_mnmajor(sv + k * 2048, 16384), idesc_o, !first[sid] || k > 0 ? 1u : 0u);
+                                  dv + (uint64_t)k * (2048 >> 4), idesc_o, !first[sid] || k > 0 ? 1u : 0u);
             tc::commit_w(bar(SM::kODone + sid));
             if (last[sid]) tc::commit_w(bar(SM::kVEmpty + vs));
             ++issued[sid];
@@ -392,54 +390,55 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                 tc::fence_after();
                 if (!good) s_badp[pid - 1] = 1;
                 if (active) {
-                    uint32_t pk[32];
-                    float sum;
-                    // P of this half as bf16 pairs, and its sum
-                    auto probs = [&](const float (&x)[64]) {
-                        float2 s2[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                    uint32_t pk[32];  // P of this half as bf16 pairs
+                    // 32 keys at a time: the logits of 64 beside their P would not fit a thread's 96 registers
+                    auto probs = [&](const float (&x)[32], const int c) {
                         const float2 scale2 = {sl2, sl2}, off2 = {-ms, -ms};
+                        float2 s2[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
                         if (edge) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
+                            for (int i = 0; i < 16; ++i) {
                                 const float2 y = fma2({x[2 * i], x[2 * i + 1]}, scale2, off2);
-                                const float2 p = {2 * i < vis ? ex2_approx(y.x) : 0.0f, 2 * i + 1 < vis ? ex2_approx(y.y) : 0.0f};
+                                const int k = 32 * c + 2 * i;
+                                const float2 p = {k < vis ? ex2_approx(y.x) : 0.0f, k + 1 < vis ? ex2_approx(y.y) : 0.0f};
                                 s2[i & 1] = add2(s2[i & 1], p);
-                                pk[i] = pack_bf16x2(p.x, p.y);
+                                pk[16 * c + i] = pack_bf16x2(p.x, p.y);
                             }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
+                            for (int i = 0; i < 16; ++i) {
                                 const float2 y = fma2({x[2 * i], x[2 * i + 1]}, scale2, off2);
                                 const float2 p = {ex2_approx(y.x), ex2_approx(y.y)};
                                 s2[i & 1] = add2(s2[i & 1], p);
-                                pk[i] = pack_bf16x2(p.x, p.y);
+                                pk[16 * c + i] = pack_bf16x2(p.x, p.y);
                             }
                         }
-                        sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+                        return (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
                     };
-                    bool high;
-                    {
-                        float x[64];
-                        __syncwarp();
-                        tc::tmem_ld64(tS + 64 * half, x);
-                        if (t == t0) {  // the row's reference: its first key, or the second page's where the first is bad
-                            if (half == (flags & 1 ? 0 : 1)) s_row[0] = vis > 0 ? x[0] * sl2 : -INFINITY;
-                            pf_pair_bar(pid);
-                            ms = s_row[0];
-                        }
-                        probs(x);
-                        high = sum > kPfSumMax;
+                    float x[32];
+                    __syncwarp();
+                    tc::tmem_ld32(tS + 64 * half, x);
+                    if (t == t0) {  // the row's reference: its first key, or the second page's where the first is bad
+                        if (half == (flags & 1 ? 0 : 1)) s_row[0] = vis > 0 ? x[0] * sl2 : -INFINITY;
+                        pf_pair_bar(pid);
+                        ms = s_row[0];
                     }
-                    const bool any = pf_pair_or(pid, high);
+                    float sum = probs(x, 0);
+                    tc::tmem_ld32(tS + 64 * half + 32, x);
+                    sum += probs(x, 1);
+                    const bool any = pf_pair_or(pid, sum > kPfSumMax);
                     if (s_badp[pid - 1]) {
                         ok = false;
                         break;
                     }
                     if (any) {
-                        float x[64], mx = -INFINITY;
-                        tc::tmem_ld64(tS + 64 * half, x);
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            tc::tmem_ld32(tS + 64 * half + 32 * c, x);
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) mx = fmaxf(mx, i < vis ? x[i] * sl2 : -INFINITY);
+                            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, 32 * c + i < vis ? x[i] * sl2 : -INFINITY);
+                        }
                         s_row[128 * half] = mx;
                         if (tiles > 0) good = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);  // O is at rest
                         if (!good) s_badp[pid - 1] = 1;
@@ -453,14 +452,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                             tc::fence_after();
 #pragma unroll 1
                             for (int c = 0; c < D / 2; c += 32) {
-                                float o[32];
-                                tc::tmem_ld32(tO + c, o);
+                                tc::tmem_ld32(tO + c, x);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= f;
-                                tc::tmem_st32f(tO + c, o);
+                                for (int i = 0; i < 32; ++i) x[i] *= f;
+                                tc::tmem_st32f(tO + c, x);
                             }
                         }
-                        probs(x);
+                        tc::tmem_ld32(tS + 64 * half, x);
+                        sum = probs(x, 0);
+                        tc::tmem_ld32(tS + 64 * half + 32, x);
+                        sum += probs(x, 1);
                     }
                     tc::tmem_st32(tS + 64 * half, pk);
                     l += sum;
@@ -496,10 +497,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                     break;
                 }
                 tc::fence_after();
-                const int64_t at = (int64_t)seg.part * (seg.b < 0 ? d.strideP : d.strideO) + (both ? rr : turn * seg.nr + rr);
-                float *O = (seg.b < 0 ? w.Op : w.Oo) + at * D + half * (D / 2);
+                const int64_t at = (int64_t)seg.part * d.strideP + (both ? rr : turn * seg.nr + rr);
+                float *O = w.Op + at * D + half * (D / 2);
                 if (mine && half == 0)
-                    reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at] = make_float2(ms, s_row[0] + s_row[128]);
+                    reinterpret_cast<float2 *>(w.mlp)[at] = make_float2(ms, s_row[0] + s_row[128]);
 #pragma unroll 1
                 for (int c = 0; c < D / 2; c += 32) {
                     float o[32];
@@ -528,8 +529,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
 }
 
 template <int D>
-static cudaError_t launch_wide(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
-                               cudaStream_t s) {
+static cudaError_t launch_wide(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, cudaStream_t s) {
     CUtensorMap tk, tv;
     const uint64_t rows = (uint64_t)a.num_pages * a.Hkv * kChunk;
     if (!make_tmap_bf16(&tk, a.Kp, rows, D, kChunk) || !make_tmap_bf16(&tv, a.Vp, rows, D, kChunk))
@@ -538,12 +538,11 @@ static cudaError_t launch_wide(const PrefixArgs &a, const PfDims &d, const PfWor
     cudaError_t e = allow_smem<prefix_wide_kernel<D>>(smem);
     if (e != cudaSuccess) return e;
     HSA_PROF("prefix_wide", s);
-    return launch_pdl(prefix_wide_kernel<D>, dim3(ctas), dim3(kPfThreads), smem, s, a, d, w, prefix, own, tk, tv);
+    return launch_pdl(prefix_wide_kernel<D>, dim3(ctas), dim3(kPfThreads), smem, s, a, d, w, tk, tv);
 }
 
-cudaError_t launch_prefix_wide(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, bool prefix, bool own,
-                               cudaStream_t s) {
-    return a.D == 128 ? launch_wide<128>(a, d, w, ctas, prefix, own, s) : launch_wide<64>(a, d, w, ctas, prefix, own, s);
+cudaError_t launch_prefix_wide(const PrefixArgs &a, const PfDims &d, const PfWork &w, int ctas, cudaStream_t s) {
+    return a.D == 128 ? launch_wide<128>(a, d, w, ctas, s) : launch_wide<64>(a, d, w, ctas, s);
 }
 
 }  // namespace hsa

@@ -108,6 +108,20 @@ struct PfSeg {
     const int32_t *table;
 };
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return reinterpret_cast<float2 &>(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return reinterpret_cast<float2 &>(r);
+}
+
 // What the copying warp, which walks the segments, announces of one to the other warps, through a ring in shared
 // memory; nr = 0 ends the walk.
 constexpr int kPfRing = 4;
@@ -193,9 +207,10 @@ struct PfWalk {
 
 // The rows of a segment in q / out, walked upwards (a division per row made the copy of 256 rows take 20 us).
 struct PfQRows {
-    int row, rem, wrap, jump;  // the row at hand; its place among its request's; where the next request's begin, and how far
+    int request, row, rem, wrap, jump;  // of the row at hand; its place among its request's; where the next's begin, and how far
     __device__ PfQRows(const PfSeg &s, const PfDims &d, int Hkv, int rr) {  // rows stay below 2^31 / D
-        const int r = s.r0 + rr, request = s.b < 0 ? r / d.Ro : s.b;
+        const int r = s.r0 + rr;
+        request = s.b < 0 ? r / d.Ro : s.b;
         rem = s.b < 0 ? r - request * d.Ro : r;
         row = (request * Hkv + s.h) * d.Ro + rem;
         wrap = s.b < 0 ? d.Ro : INT32_MAX;
@@ -207,6 +222,7 @@ struct PfQRows {
         while (rem >= wrap) {
             rem -= wrap;
             row += jump;
+            ++request;
         }
     }
 };

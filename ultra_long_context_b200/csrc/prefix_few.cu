@@ -14,10 +14,12 @@
 //
 // Persistent, warp-specialised, one CTA per SM; the CTA's tiles are numbered through all its segments:
 //   warps 0-3, 4-7  softmax of the tiles n of even / odd number, each with an S^T, P^T, O^T (and m, l) of its own;
-//   warp 8      MMA issuer: S^T(n) as soon as its operands and S^T's buffer are there, O^T(n) as soon as P^T(n) is;
-//   warp 9      walks the segments, announces them to the other warps and copies K and V tiles by TMA, page by
+//   warp 8      issues S^T(n), in order, when its operands are there and S^T(n - 2) has been read;
+//   warp 9      issues O^T(n), in order, when P^T(n) and V are there. (Two warps that sleep in their waits; one that polled
+//               for both took its scheduler's issue slots from two softmax warps, 64 rows 3.1 -> TODO thousand cycles);
+//   warp 10     walks the segments, announces them to the other warps and copies K and V tiles by TMA, page by
 //               page (64 rows of one head are contiguous);
-//   warp 10     Q rows by cp.async, padded with zero rows to N.
+//   warp 11     Q rows by cp.async, padded with zero rows to N.
 #include <cuda.h>
 
 #include "prefix.cuh"
@@ -25,9 +27,9 @@
 
 namespace hsa {
 
-constexpr int kFwMmaWarp = 8, kFwTmaWarp = 9, kFwQWarp = 10;
+constexpr int kFwSWarp = 8, kFwOWarp = 9, kFwTmaWarp = 10, kFwQWarp = 11;
 constexpr int kFwThreads = 32 * (kFwQWarp + 1);
-constexpr float kFwGrow = 64.0f;
+constexpr float kFwGrow = 64.0f, kFwSumMax = 0x1p70f;  // a sum of 64 terms of at most 2^64
 constexpr int kFwFlags = 8;   // tiles whose page flags are kept (copies run at most KS tiles ahead of S^T)
 
 template <int D, int NR>  // NR: rows per segment at most
@@ -45,7 +47,7 @@ struct FwSmem {
                          kODone = kPFull + 2, kOEmpty = kODone + 2, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kPfRing,
                          NBAR = kSegEmpty + kPfRing;
     static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;
-    static constexpr uint32_t MS = RING + kPfRing * sizeof(PfNote);        // float[2][NR]: m * scale * log2(e), or -inf
+    static constexpr uint32_t MS = RING + kPfRing * sizeof(PfNote);        // float[2][NR]: -m * scale * log2(e), inf while a row sees nothing
     static constexpr uint32_t LIM = MS + 2 * NR * 4;                      // int[2][NR]
     static constexpr uint32_t SUM = LIM + 2 * NR * 4;                     // float[2][4][NR]: row sums of a warp's keys
     static constexpr uint32_t FLAG = SUM + 8 * NR * 4;                    // int[kFwFlags]
@@ -75,6 +77,13 @@ __device__ __forceinline__ bool fw_bar_or(int id, bool v) {
 }
 __device__ __forceinline__ void fw_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
+template <int NR>
+__device__ __forceinline__ void fw_ld(uint32_t taddr, float (&v)[NR]) {  // NR consecutive columns of this thread's TMEM lane
+    if constexpr (NR == 16) tc::tmem_ld16(taddr, v);
+    else if constexpr (NR == 32) tc::tmem_ld32(taddr, v);
+    else tc::tmem_ld64(taddr, v);
+}
+
 template <int D, int NR>
 __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixArgs a, const PfDims d, const PfWork w,
                                                                    const __grid_constant__ CUtensorMap tmK,
@@ -95,7 +104,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     auto bar = [&](int i) { return sb + SM::BAR + 8u * (uint32_t)i; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (warp == kFwMmaWarp) tc::tmem_alloc(sb + SM::MISC, SM::TMEM_COLS);
+    if (warp == kFwSWarp) tc::tmem_alloc(sb + SM::MISC, SM::TMEM_COLS);
     if (warp == kFwTmaWarp && lane == 0) {
         pf_prefetch_tmap(&tmK);
         pf_prefetch_tmap(&tmV);
@@ -121,7 +130,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         }
         for (int i = 0; i < kPfRing; ++i) {
             tc::mbar_init(bar(SM::kSegFull + i), 1);
-            tc::mbar_init(bar(SM::kSegEmpty + i), 10);  // the warps but this ring's writer
+            tc::mbar_init(bar(SM::kSegEmpty + i), kFwThreads / 32 - 1);  // the warps but this ring's writer
         }
         tc::fence_mbar_init();
     }
@@ -230,7 +239,8 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             const uint32_t dst = sb + SM::Q + q * SM::QB;
             PfQRows at(g.s, d, a.Hkv, rsub);
             for (int r = rsub; r < (g.s.nr + 15) / 16 * 16; r += RPW, at.advance(RPW)) {
-                const bool in = r < g.s.nr;
+                // (zeros, too, for the empty rows of a padded batch: whatever stands there must not look like a large logit)
+                const bool in = r < g.s.nr && a.own_len[at.request] >= 0;
                 cp_async16_u32(dst + (ch >> 3) * (NR * 128) + tc::sw128(r, ch & 7),
                                in ? a.q + (int64_t)at.row * D + ch * 8 : a.q, in ? 16 : 0);
             }
@@ -238,119 +248,71 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         }
         cp_async_commit();
         cp_async_wait<0>();  // nothing in flight when the CTA exits
-    } else if (warp == kFwMmaWarp) {
-        // ================= MMA issuer: the whole warp runs the loop, one elected lane issues =================
-        bool have = false, end = false;   // is there a segment at next_s; is there none any more
-        int t = 0, nt = 0, q = 0;         // of next_s: tile of the segment, its tiles, Q buffer
-        uint32_t quse = 0, id_s = 0;
-        int next_s = 0, next_o = 0;       // tiles
-        // of the even and odd tiles: the instruction of the tile at O^T, whether it begins a run in its segment, O^T
-        // products so far, runs begun
-        struct Stream {
-            uint32_t id = 0, tiles = 0, runs = 0;
-            bool first = false;
-        } st0, st1;
-        int k_seen = 0, v_seen = 0, k_slot = 0, v_slot = 0;  // fillings of the slots observed, in order
-        uint32_t k_par = 0, v_par = 0, idle = 0;
+    } else if (warp == kFwSWarp) {
+        // ================= S^T products: the whole warp runs the loop, one elected lane issues =================
+        PfNote g;
+        int n = 0;
         while (true) {
-            bool progress = false;
-            // one probe per lane: the next segment, fillings, P^T and free O^T of both streams, in one round
-            const int slot = seg_no % kPfRing;
-            int b = SM::kSegFull + slot;
-            uint32_t par = (uint32_t)(seg_no / kPfRing);
-            if (lane == 1) b = SM::kKFull + k_slot, par = k_par;
-            if (lane == 2) b = SM::kVFull + v_slot, par = v_par;
-            if (lane == 3) b = SM::kQFull + q, par = quse;
-            if (lane == 4) b = SM::kPFull, par = st0.tiles;
-            if (lane == 5) b = SM::kPFull + 1, par = st1.tiles;
-            if (lane == 6) b = SM::kOEmpty, par = st0.runs;
-            if (lane == 7) b = SM::kOEmpty + 1, par = st1.runs;
-            const unsigned hit = __ballot_sync(0xffffffffu, lane < 8 && tc::mbar_test(bar(b), par & 1u));
-            __syncwarp();  // what the probing lanes acquired holds for the issuing one
-            bool q_in = hit & 8u;  // Q of the segment (one taken just now is asked for in the next round)
-            if (!have && !end && (hit & 1u)) {
-                q = seg_no & 1;
-                quse = (uint32_t)(seg_no >> 1);
-                const int nr = s_ring[slot].s.nr;
-                nt = s_ring[slot].s.nt;
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar(SM::kSegEmpty + slot));
-                ++seg_no;
-                have = nr > 0;
-                end = !have;
-                id_s = tc::idesc_bf16(128, (nr + 15) / 16 * 16, 0, 0);
-                t = 0;
-                q_in = false;
-                progress = true;
-            }
-            if (end && next_o == next_s) break;
-            if (hit & 2u) {
-                ++k_seen;
-                if (++k_slot == KS) k_slot = 0, k_par ^= 1u;
-            }
-            if (hit & 4u) {
-                ++v_seen;
-                if (++v_slot == VS) v_slot = 0, v_par ^= 1u;
-            }
-            auto o_step = [&](Stream &c, const int sid) {  // O^T(next_o)
-                if (!(hit & (16u << sid)) || (c.first && c.runs > 1 && !(hit & (64u << sid)))) return;
-                tc::fence_after();
-                const int vs = next_o % VS;
-                // the second 64 rows of A: dims 64 .. 127, or, with D = 64, whatever follows the tile (lanes that are not read)
-                const uint64_t dv = tc::desc_mnmajor(sb + SM::V + vs * SM::OP, 16384);
-                const uint64_t dp = tc::desc_mnmajor(sb + SM::P + sid * SM::PB, 16384);
-                const uint32_t id = c.id | (1u << 15) | (1u << 16);  // A and B MN-major
-#pragma unroll
-                for (int k = 0; k < kPfTile / 16; ++k)  // (a descriptor's low bits are its address / 16)
-                    tc::mma_bf16_ss_w(tmem + SM::O_COL + sid * 64, dv + (uint64_t)k * (2048 >> 4), dp + (uint64_t)k * (2048 >> 4), id,
-                                      c.first && k == 0 ? 0u : 1u);
-                tc::commit_w(bar(SM::kODone + sid));
-                tc::commit_w(bar(SM::kVEmpty + vs));
-                c.first = false;
-                ++c.tiles;
-                ++next_o;
-                progress = true;
-            };
-            if (next_o < next_s && next_o < v_seen) {
-                if (next_o & 1) o_step(st1, 1);
-                else o_step(st0, 0);
-            }
-            // S^T(next_s): its buffer is free once P^T of the tile two before is written. The V filling before this
-            // tile's in its slot has landed, so that a softmax wait on the slot's parity, which follows S^T, is exact
-            auto s_step = [&](Stream &c, const int sid) {
+            const int q = seg_no & 1;
+            const uint32_t use = (uint32_t)(seg_no >> 1);
+            ok = take(g);
+            if (!ok || g.s.nr == 0) break;
+            const uint32_t id = tc::idesc_bf16(128, (g.s.nr + 15) / 16 * 16, 0, 0);
+            const uint64_t dq = tc::desc_kmajor(sb + SM::Q + q * SM::QB);
+            for (int t = 0; t < g.s.nt; ++t, ++n) {
+                const int sid = n & 1, ks = n % KS;
+                ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS) & 1u) && (t > 0 || pf_wait(bar(SM::kQFull + q), use & 1u));
+                // P^T of the tile two before is written: its S^T has been read
+                if (ok && n >= 2) ok = pf_wait(bar(SM::kPFull + sid), (uint32_t)((n - 2) >> 1) & 1u);
+                if (!ok) break;
                 tc::fence_after();
                 if (t == 0) tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
-                const int ks = next_s % KS;
-                const uint64_t dk = tc::desc_kmajor(sb + SM::K + ks * SM::OP), dq = tc::desc_kmajor(sb + SM::Q + q * SM::QB);
                 if (lane == 0) tc::mbar_arrive(bar(SM::kInfo + sid));  // hands on the page flags that came with K
+                const uint64_t dk = tc::desc_kmajor(sb + SM::K + ks * SM::OP);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
+                for (int k = 0; k < D / 16; ++k)  // (a descriptor's low bits are its address / 16)
                     tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * 64, dk + ((uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4),
-                                      dq + ((uint64_t)((k >> 2) * (NR * 128) + (k & 3) * 32) >> 4), id_s, k > 0 ? 1u : 0u);
+                                      dq + ((uint64_t)((k >> 2) * (NR * 128) + (k & 3) * 32) >> 4), id, k > 0 ? 1u : 0u);
                 tc::commit_w(bar(SM::kSFull + sid));
                 tc::commit_w(bar(SM::kKEmpty + ks));
-                c.id = id_s;
-                if (t < 2) {
-                    c.first = true;
-                    ++c.runs;
-                }
-                if (++t == nt) {
-                    tc::commit_w(bar(SM::kQEmpty + q));
-                    have = false;
-                }
-                ++next_s;
-                progress = true;
-            };
-            if (have && next_s < next_o + 2 && next_s < k_seen && next_s - VS < v_seen && (t > 0 || q_in)) {
-                if (next_s & 1) s_step(st1, 1);
-                else s_step(st0, 0);
+                if (t == g.s.nt - 1) tc::commit_w(bar(SM::kQEmpty + q));
             }
-            if (progress) {
-                idle = 0;
-            } else if (++idle > (1u << 25)) {
-                ok = false;
-                break;
+            if (!ok) break;
+        }
+        __syncwarp();
+    } else if (warp == kFwOWarp) {
+        // ================= O^T products =================
+        PfNote g;
+        int n = 0;
+        uint32_t runs0 = 0, runs1 = 0;  // runs (of a segment's tiles in a stream) begun
+        while (true) {
+            ok = take(g);
+            if (!ok || g.s.nr == 0) break;
+            // A and B MN-major. The second 64 rows of A: dims 64 .. 127, or, with D = 64, whatever follows the tile (lanes
+            // that are not read)
+            const uint32_t id = tc::idesc_bf16(128, (g.s.nr + 15) / 16 * 16, 1, 1);
+            for (int t = 0; t < g.s.nt; ++t, ++n) {
+                const int sid = n & 1, vs = n % VS;
+                ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
+                if (t < 2) {  // the run before has been read out of O^T
+                    const uint32_t runs = sid ? runs1 : runs0;
+                    if (ok && runs > 0) ok = pf_wait(bar(SM::kOEmpty + sid), (runs - 1) & 1u);
+                    if (sid) ++runs1;
+                    else ++runs0;
+                }
+                if (ok) ok = pf_wait(bar(SM::kPFull + sid), (uint32_t)(n >> 1) & 1u);
+                if (!ok) break;
+                tc::fence_after();
+                const uint64_t dv = tc::desc_mnmajor(sb + SM::V + vs * SM::OP, 16384);
+                const uint64_t dp = tc::desc_mnmajor(sb + SM::P + sid * SM::PB, 16384);
+#pragma unroll
+                for (int k = 0; k < kPfTile / 16; ++k)
+                    tc::mma_bf16_ss_w(tmem + SM::O_COL + sid * 64, dv + (uint64_t)k * (2048 >> 4), dp + (uint64_t)k * (2048 >> 4), id,
+                                      t >= 2 || k > 0 ? 1u : 0u);
+                tc::commit_w(bar(SM::kODone + sid));
+                tc::commit_w(bar(SM::kVEmpty + vs));
             }
+            if (!ok) break;
         }
         __syncwarp();
     } else {
@@ -360,7 +322,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         const uint32_t tS = tmem + lane_off + SM::S_COL + sid * 64, tO = tmem + lane_off + SM::O_COL + sid * 64;
         unsigned char *s_p = s + SM::P + sid * SM::PB;
         float *s_red = reinterpret_cast<float *>(s_p), *s_f = s_red + 4 * NR;
-        float *ms = s_ms + sid * NR, *s_sum = reinterpret_cast<float *>(s + SM::SUM) + sid * 4 * NR;
+        float *nms = s_ms + sid * NR, *s_sum = reinterpret_cast<float *>(s + SM::SUM) + sid * 4 * NR;
         int *lims = s_lim + sid * NR;
         const float sl2 = a.scale * 1.4426950408889634f;
         uint32_t tiles = 0;
@@ -378,10 +340,9 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             const int t0 = (sid ^ g.n0) & 1;
             if (t0 >= seg.nt) continue;
             const int min_lim = pf_min_limit(a, seg), nc = (seg.nr + 15) / 16;
-            if (r < seg.nr) {
-                lims[r] = pf_limit(a, seg, d, r);
-            } else if (r < NR) {
-                lims[r] = INT32_MAX;
+            if (r < NR) {  // rows that are nobody's: -1 (they see nothing, where it is asked: in tiles with an edge)
+                const int lim = r < seg.nr ? pf_limit(a, seg, d, r) : -1;
+                lims[r] = lim == INT32_MAX ? -1 : lim;
             }
             fw_bar(bid);
             float l[NR];
@@ -389,10 +350,14 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             for (int i = 0; i < NR; ++i) l[i] = 0.0f;
             for (int t = t0; t < seg.nt; t += 2, ++tiles) {
                 const int n = g.n0 + t, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
-                bool good = pf_wait(bar(SM::kInfo + sid), tiles & 1u) && pf_wait(bar(SM::kSFull + sid), tiles & 1u);
-                tc::fence_after();
+                bool good = pf_wait(bar(SM::kInfo + sid), tiles & 1u);
                 const int flags = s_flag[n % kFwFlags];
                 const bool edge = flags != 3 || base + kPfTile > min_lim;
+                // the O^T product before has read P^T, and O^T is at rest (and so every V filling before this tile's in its slot
+                // is over, which makes the wait for it by its parity exact)
+                if (good && tiles > 0) good = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);
+                good = good && pf_wait(bar(SM::kSFull + sid), tiles & 1u);
+                tc::fence_after();
                 if (edge && good) {
                     good = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
                     // a key behind the sequence's end weighs nothing, but 0 x NaN is NaN: its V row becomes zero
@@ -407,27 +372,41 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     __syncwarp();
                 }
                 const bool page_ok = (flags >> (r >> 6)) & 1;
-                // of 16 rows: y = logit * log2(e) - m, -inf where the row does not see the key
-                auto logits = [&](float (&y)[16], const int c) {
-                    tc::tmem_ld16(tS + 16 * c, y);
+                float p[NR];
+                // P^T of this key to shared memory, kept in p for the row sums; false if a term leaves the range
+                auto probs = [&]() {
+                    float2 sum = {0.0f, 0.0f};
+                    fw_ld<NR>(tS, p);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 m4 = *reinterpret_cast<const float4 *>(ms + 16 * c + i);
-                        y[i] = fmaf(y[i], sl2, -m4.x);
-                        y[i + 1] = fmaf(y[i + 1], sl2, -m4.y);
-                        y[i + 2] = fmaf(y[i + 2], sl2, -m4.z);
-                        y[i + 3] = fmaf(y[i + 3], sl2, -m4.w);
-                    }
-                    if (edge) {
+                    for (int c = 0; c < NR / 8; ++c) {
+                        if (c >= 2 * nc) break;
+                        uint32_t pk[4];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (!(page_ok && base + r < lims[16 * c + i])) y[i] = -INFINITY;
+                        for (int i = 0; i < 8; i += 4) {
+                            const int e = 8 * c + i;
+                            const float4 off = *reinterpret_cast<const float4 *>(nms + e);
+                            float2 a0 = fma2({p[e], p[e + 1]}, {sl2, sl2}, {off.x, off.y});
+                            float2 a1 = fma2({p[e + 2], p[e + 3]}, {sl2, sl2}, {off.z, off.w});
+                            a0 = {ex2_approx(a0.x), ex2_approx(a0.y)};
+                            a1 = {ex2_approx(a1.x), ex2_approx(a1.y)};
+                            if (edge) {
+                                const int key = base + r;
+                                const int4 lim = *reinterpret_cast<const int4 *>(lims + e);
+                                a0 = {page_ok && key < lim.x ? a0.x : 0.0f, page_ok && key < lim.y ? a0.y : 0.0f};
+                                a1 = {page_ok && key < lim.z ? a1.x : 0.0f, page_ok && key < lim.w ? a1.y : 0.0f};
+                            }
+                            sum = add2(sum, add2(a0, a1));
+                            p[e] = a0.x;
+                            p[e + 1] = a0.y;
+                            p[e + 2] = a1.x;
+                            p[e + 3] = a1.y;
+                            pk[i / 2] = pack_bf16x2(a0.x, a0.y);
+                            pk[i / 2 + 1] = pack_bf16x2(a1.x, a1.y);
+                        }
+                        *reinterpret_cast<uint4 *>(s_p + tc::sw128(r, c)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
+                    return sum.x + sum.y <= kFwSumMax;  // (not of an infinity or NaN)
                 };
-                // with up to 32 rows the logits stay in registers from the vote to the exponentials; those of 64 rows
-                // beside their sums would not, and are read from TMEM again
-                constexpr bool KEEP = NR <= 32;
-                float y[KEEP ? NR / 16 : 1][16];
                 if (t == t0) {  // the references: the first key, or the 65th where the first page is bad
                     const int lead = flags & 1 ? 0 : 64;
                     if (r >> 5 == lead >> 5 && good) {
@@ -439,33 +418,23 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                             tc::tmem_ld16(tS + 16 * c, x);
                             if (lane == 0) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    ms[16 * c + i] = page_ok && base + lead < lims[16 * c + i] ? x[i] * sl2 : -INFINITY;
+                                for (int i = 0; i < 16; ++i) {
+                                    const int lim = lims[16 * c + i];
+                                    nms[16 * c + i] = lim < 0 ? 0.0f : page_ok && base + lead < lim ? -x[i] * sl2 : INFINITY;
+                                }
                             }
                         }
                     }
                     fw_bar(bid);
                 }
-                float top = -INFINITY;
-                if (good) {
-#pragma unroll
-                    for (int c = 0; c < NR / 16; ++c) {
-                        if (c >= nc) break;
-                        float(&yc)[16] = y[KEEP ? c : 0];
-                        logits(yc, c);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) top = fmaxf(top, yc[i]);
-                    }
-                } else {
-                    s_bad[sid] = 1;
-                }
-                const bool any = fw_bar_or(bid, top > kFwGrow);
+                bool high = false;
+                if (good) high = !probs();
+                else s_bad[sid] = 1;
+                const bool any = fw_bar_or(bid, high);
                 if (s_bad[sid]) {
                     ok = false;
                     break;
                 }
-                // the O^T product before has read P^T, and O^T is at rest
-                if (tiles > 0) good = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);
                 if (any) {
                     tc::fence_after();
                     // maxima over the tile's keys, of logit * log2(e)
@@ -484,10 +453,10 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     fw_bar(bid);
                     if (r < 16 * nc) {
                         const float mx = fmaxf(fmaxf(s_red[r], s_red[NR + r]), fmaxf(s_red[2 * NR + r], s_red[3 * NR + r]));
-                        const float old = ms[r];
+                        const float old = -nms[r];
                         const bool grow = mx - old > kFwGrow;  // from -inf, too; not where nothing is visible yet (-inf, NaN)
                         s_f[r] = grow ? ex2_approx(old - mx) : 1.0f;
-                        if (grow) ms[r] = mx;
+                        if (grow) nms[r] = -mx;
                     }
                     fw_bar(bid);
 #pragma unroll
@@ -508,38 +477,19 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                             tc::tmem_st16(tO + 16 * c, u);
                         }
                     }
-                    if constexpr (KEEP) {
-#pragma unroll
-                        for (int c = 0; c < NR / 16; ++c) {
-                            if (c >= nc) break;
-                            logits(y[c], c);
-                        }
-                    }
                     fw_bar(bid);  // the scratch has been read: P^T may go there
-                }
-#pragma unroll
-                for (int c = 0; c < NR / 16; ++c) {
-                    if (c >= nc) break;
-                    float(&yc)[16] = y[KEEP ? c : 0];
-                    if constexpr (!KEEP) logits(yc, c);
-#pragma unroll
-                    for (int hv = 0; hv < 2; ++hv) {
-                        uint32_t pk[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int e = 16 * c + 8 * hv + 2 * i;
-                            const float p0 = ex2_approx(yc[8 * hv + 2 * i]), p1 = ex2_approx(yc[8 * hv + 2 * i + 1]);
-                            l[e] += p0;
-                            l[e + 1] += p1;
-                            pk[i] = pack_bf16x2(p0, p1);
-                        }
-                        *reinterpret_cast<uint4 *>(s_p + tc::sw128(r, 2 * c + hv)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    }
+                    probs();
                 }
                 tc::fence_proxy_async_smem();  // P^T, and V rows made zero
                 tc::fence_before();
                 tc::mbar_arrive(bar(SM::kPFull + sid));
-                if (!good) s_bad[sid] = 1;
+#pragma unroll
+                for (int i = 0; i < NR; i += 2) {  // (the rows beyond the segment's hold sums of nothing)
+                    if (i >= 16 * nc) break;
+                    const float2 sum = add2({l[i], l[i + 1]}, {p[i], p[i + 1]});
+                    l[i] = sum.x;
+                    l[i + 1] = sum.y;
+                }
             }
             if (!ok) break;
             // the warp's row sums: each step halves the rows a lane holds
@@ -567,7 +517,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             fw_bar(bid);
             if (r < seg.nr) {
                 const float sum = (s_sum[r] + s_sum[NR + r]) + (s_sum[2 * NR + r] + s_sum[3 * NR + r]);
-                reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at + r] = make_float2(ms[r], sum);
+                reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at + r] = make_float2(-nms[r], sum);
             }
             if (!pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u)) s_bad[sid] = 1;  // seen at the next barrier
             tc::fence_after();
@@ -593,7 +543,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     if (d.wide) pdl_wait();  // the kernel before, whose partials the join reads, too
     pdl_launch_dependents();
     if (tid == 0) w.status[kPfCtas + blockIdx.x] = s_bad[0] | s_bad[1] | s_bad[2];
-    if (warp == kFwMmaWarp) {
+    if (warp == kFwSWarp) {
         tc::fence_after();
         tc::tmem_dealloc(tmem, SM::TMEM_COLS);
     }

@@ -56,20 +56,6 @@ static_assert(PfSmem<128>::dyn(256) <= 227 * 1024 && PfSmem<64>::dyn(256) <= 227
 // Do both streams read every tile of the segment, each for rows of its own?
 __device__ __forceinline__ bool pf_both(const PfSeg &s) { return s.nr > kPfTile; }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(r)
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
-    return reinterpret_cast<float2 &>(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return reinterpret_cast<float2 &>(r);
-}
-
 // Named barriers of the two warps (64 threads) that share 32 rows.
 __device__ __forceinline__ void pf_pair_bar(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool pf_pair_or(int id, bool v) {
@@ -248,7 +234,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                 // (the other rows are nobody's; zeros keep their logits small)
                 PfQRows at(seg, d, a.Hkv, k * kPfTile + qw * RPW + rsub);
                 for (int r = qw * RPW + rsub; r < kPfTile; r += kPfQWarps * RPW, at.advance(kPfQWarps * RPW)) {
-                    const bool in = r < rows;
+                    const bool in = r < rows && a.own_len[at.request] >= 0;  // (nor are those of empty rows of the batch)
                     cp_async16_u32(dst + (ch >> 3) * 16384 + tc::sw128(r, ch & 7),
                                    in ? a.q + (int64_t)at.row * D + ch * 8 : a.q, in ? 16 : 0);
                 }

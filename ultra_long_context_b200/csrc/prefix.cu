@@ -42,14 +42,14 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
     const int64_t cum = w.bcum[bl >> 5] + __shfl_sync(0xffffffffu, sum, b & 31) - wt;
     const bool live = __shfl_sync(0xffffffffu, (int)(len >= 0), b & 31) != 0;
     int np = 0, per = 1, nr = 0, rr = 0, rg = 0;      // prefix partials: np runs of `per` streams
-    int i0 = 0, no = 0, orr = 0, onr = 0, obase = 0;  // own partials: CTAs i0 .. i0 + no - 1, two streams each
+    int i0 = 0, no = 0, orr = 0, obase = 0;           // own partials: CTAs i0 .. i0 + no - 1
     int64_t x0 = 0;
     if (live) {
         const int rp = b * d.Ro + ro;
         rg = rp / d.gp;
         rr = rp - rg * d.gp;
         nr = min(d.gp, d.Rp - rg * d.gp);
-        per = nr > kPfTile ? 1 : 2;
+        per = d.wide && nr <= kPfTile ? 2 : 1;
         np = p.items > 0 ? p.nsplit : 0;
         if (wt > 0) {
             const int hr = h * d.Rgo + ro / kPfFewRows;
@@ -58,10 +58,9 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
             no = po.cta_of(x0 + wt - 1) - i0 + 1;
             obase = b * hr_n + hr;
             orr = ro % kPfFewRows;
-            onr = min(kPfFewRows, d.Ro - ro / kPfFewRows * kPfFewRows);
         }
     }
-    const int total = np * per + 2 * no;
+    const int total = np * per + no;
     // partial idx: its place (rows of D), or -1
     auto place = [&](int idx) -> int64_t {
         if (idx < np * per) {
@@ -70,10 +69,9 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
             if (st >= nt) return -1;
             return (int64_t)((k * a.Hkv + h) * d.Rgp + rg) * d.strideP + st * nr + rr;
         }
-        const int i = i0 + (idx - np * per) / 2, st = (idx - np * per) & 1;
+        const int i = i0 + (idx - np * per);
         const int nt = pf_tile_at(min(po.start(i + 1), x0 + wt) - x0) - pf_tile_at(max(po.start(i), x0) - x0);
-        if (st >= nt) return -1;
-        return (int64_t)(obase + i) * d.strideO + st * onr + orr;
+        return nt > 0 ? (int64_t)(obase + i) * d.strideO + orr : -1;
     };
     const float2 *mlp = reinterpret_cast<const float2 *>(w.mlp), *mlo = reinterpret_cast<const float2 *>(w.mlo);
     float M = -INFINITY;

@@ -48,7 +48,7 @@ struct PfDims {
     bool wide;             // the prefix goes to the wide kernel (the requests' own pages to the few-rows kernel always)
     int Rp, gp, Rgp;       // prefix rows per key head, in Rgp groups of gp
     int Ro, Rgo;           // own rows per request and key head, in groups of kPfFewRows
-    int strideP, strideO;  // rows of one segment's partials (two streams that share rows keep one each)
+    int strideP, strideO;  // rows of one segment's partials (in the wide kernel, two streams may each keep one of the same rows)
     int max_items, max_slots, blocks;  // blocks: of 32 requests
     // Which kernel ends the prefix sooner? A tile of 128 keys takes the few-rows kernel 1.15 us (D = 128; half that with
     // D = 64: its bytes) for 64 rows, the wide one 2.3 us for 256, and that is a launch of its own, 12 us before the
@@ -67,8 +67,8 @@ struct PfDims {
         gp = wide ? kPfWideRows : kPfFewRows;
         Rgp = (Rp + gp - 1) / gp;
         Rgo = (Ro + kPfFewRows - 1) / kPfFewRows;
-        strideP = wide ? kPfWideRows : 2 * (Rp < kPfFewRows ? Rp : kPfFewRows);
-        strideO = 2 * (Ro < kPfFewRows ? Ro : kPfFewRows);
+        strideP = wide ? kPfWideRows : Rp < kPfFewRows ? Rp : kPfFewRows;
+        strideO = Ro < kPfFewRows ? Ro : kPfFewRows;
         const int units = Hkv * Rgp;
         int ns = kPfItems / units;
         ns = ns < 1 ? 1 : ns;

@@ -9,18 +9,23 @@
 // their relative precision as long as nothing leaves their range. So m is the logit of the first key that the row sees
 // in the segment, and moves only when a later one exceeds it by more than 2^64 (sums of 2^64 over 2^30 keys, times
 // V, stay far below 2^127; what is 2^126 below m is less than 2^-126 of the sum, which is at least 1). Then the
-// warpgroup reduces the maxima over the keys and rescales O^T in TMEM; every other tile costs a thread N
-// exponentials and one barrier with a vote. Row sums stay per thread until the segment ends.
+// warpgroup reduces the maxima over the keys, rescales O^T in TMEM and does the tile again; every other tile costs a
+// thread one exponential per row and one barrier with a vote. Row sums stay per thread until the segment ends.
 //
 // Persistent, warp-specialised, one CTA per SM; the CTA's tiles are numbered through all its segments:
-//   warps 0-3, 4-7  softmax of the tiles n of even / odd number, each with an S^T, P^T, O^T (and m, l) of its own;
+//   warps 0-3, 4-7  softmax of the lower and the upper half of the rows, both on every tile (in turn on the tiles, 64 rows
+//               a thread, they took 1800 cycles a tile where this takes TODO, and kept two partials);
+//               S^T and P^T of two tiles, so that the products of one run under the softmax of the other;
 //   warp 8      issues S^T(n), in order, when its operands are there and S^T(n - 2) has been read;
-//   warp 9      issues O^T(n), in order, when P^T(n) and V are there. (Two warps that sleep in their waits; one that polled
-//               for both took its scheduler's issue slots from two softmax warps, 64 rows 3.1 -> TODO thousand cycles);
+//   warp 9      issues O^T(n), in order, when P^T(n) and V are there. (Two warps that sleep in their waits: one that polled
+//               for both took issue slots from the softmax warps beside it.) O^T of two segments, so that one is
+//               read out under the next one's products;
 //   warp 10     walks the segments, announces them to the other warps and copies K and V tiles by TMA, page by
 //               page (64 rows of one head are contiguous);
 //   warp 11     Q rows by cp.async, padded with zero rows to N.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "prefix.cuh"
 #include "profile.h"
@@ -29,7 +34,7 @@ namespace hsa {
 
 constexpr int kFwSWarp = 8, kFwOWarp = 9, kFwTmaWarp = 10, kFwQWarp = 11;
 constexpr int kFwThreads = 32 * (kFwQWarp + 1);
-constexpr float kFwGrow = 64.0f, kFwSumMax = 0x1p70f;  // a sum of 64 terms of at most 2^64
+constexpr float kFwGrow = 64.0f, kFwSumMax = 0x1p69f;  // a sum of 32 terms of at most 2^64
 constexpr int kFwFlags = 8;   // tiles whose page flags are kept (copies run at most KS tiles ahead of S^T)
 
 template <int D, int NR>  // NR: rows per segment at most
@@ -47,15 +52,15 @@ struct FwSmem {
                          kODone = kPFull + 2, kOEmpty = kODone + 2, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kPfRing,
                          NBAR = kSegEmpty + kPfRing;
     static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;
-    static constexpr uint32_t MS = RING + kPfRing * sizeof(PfNote);        // float[2][NR]: -m * scale * log2(e), inf while a row sees nothing
-    static constexpr uint32_t LIM = MS + 2 * NR * 4;                      // int[2][NR]
-    static constexpr uint32_t SUM = LIM + 2 * NR * 4;                     // float[2][4][NR]: row sums of a warp's keys
-    static constexpr uint32_t FLAG = SUM + 8 * NR * 4;                    // int[kFwFlags]
+    static constexpr uint32_t MS = RING + kPfRing * sizeof(PfNote);       // float[NR]: -m * scale * log2(e), inf while a row sees nothing
+    static constexpr uint32_t LIM = MS + NR * 4;                          // int[NR]: keys that the row sees
+    static constexpr uint32_t RED = LIM + NR * 4;                         // float[4][NR]: of a row and a warp's keys (maxima, sums)
+    static constexpr uint32_t FAC = RED + 4 * NR * 4;                     // float[NR]: rescaling
+    static constexpr uint32_t FLAG = FAC + NR * 4;                        // int[kFwFlags]
     static constexpr uint32_t MISC = FLAG + 4 * kFwFlags;                 // TMEM base, bad[2], -
     static constexpr uint32_t PLAN = (MISC + 16 + 15) / 16 * 16;
     static constexpr uint32_t BCUM = PLAN + (sizeof(PfPlan) + 15) / 16 * 16;  // int[blocks + 1]
     static constexpr size_t dyn(int blocks) { return BCUM + 4 * ((size_t)blocks + 1) + 1024; }  // slack: 1 KB alignment
-    // scratch of a warpgroup inside its P^T buffer, used while that holds nothing: float[4][NR], then float[NR]
     static constexpr uint32_t S_COL = 0, O_COL = 128, TMEM_COLS = 256;
 };
 static_assert(FwSmem<128, 64>::dyn(256) <= 227 * 1024 && FwSmem<128, 32>::dyn(256) <= 227 * 1024 &&
@@ -79,9 +84,21 @@ __device__ __forceinline__ void fw_bar(int id) { asm volatile("bar.sync %0, 128;
 
 template <int NR>
 __device__ __forceinline__ void fw_ld(uint32_t taddr, float (&v)[NR]) {  // NR consecutive columns of this thread's TMEM lane
-    if constexpr (NR == 16) tc::tmem_ld16(taddr, v);
-    else if constexpr (NR == 32) tc::tmem_ld32(taddr, v);
-    else tc::tmem_ld64(taddr, v);
+    if constexpr (NR == 8) tc::tmem_ld8(taddr, v);
+    else if constexpr (NR == 16) tc::tmem_ld16(taddr, v);
+    else tc::tmem_ld32(taddr, v);
+}
+template <int NR>
+__device__ __forceinline__ void fw_st(uint32_t taddr, const float (&v)[NR]) {
+    if constexpr (NR == 32) {
+        tc::tmem_st32f(taddr, v);
+    } else {
+        uint32_t u[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) u[i] = __float_as_uint(v[i]);
+        if constexpr (NR == 8) tc::tmem_st8(taddr, u);
+        else tc::tmem_st16(taddr, u);
+    }
 }
 
 template <int D, int NR>
@@ -95,8 +112,6 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     const uint32_t sb = (raw + 1023u) & ~1023u;  // 1 KB aligned (swizzle atoms)
     unsigned char *s = smem_raw + (sb - raw);
     PfNote *s_ring = reinterpret_cast<PfNote *>(s + SM::RING);
-    float *s_ms = reinterpret_cast<float *>(s + SM::MS);
-    int *s_lim = reinterpret_cast<int *>(s + SM::LIM);
     int *s_flag = reinterpret_cast<int *>(s + SM::FLAG);
     volatile int *s_bad = reinterpret_cast<volatile int *>(s + SM::MISC) + 1;  // [2] per warpgroup, [1] any other warp's, too
     PfPlan *s_plan = reinterpret_cast<PfPlan *>(s + SM::PLAN);
@@ -124,9 +139,9 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             tc::mbar_init(bar(SM::kQEmpty + i), 1);
             tc::mbar_init(bar(SM::kSFull + i), 1);
             tc::mbar_init(bar(SM::kInfo + i), 1);
-            tc::mbar_init(bar(SM::kPFull + i), 128);
+            tc::mbar_init(bar(SM::kPFull + i), 256);
             tc::mbar_init(bar(SM::kODone + i), 1);
-            tc::mbar_init(bar(SM::kOEmpty + i), 128);
+            tc::mbar_init(bar(SM::kOEmpty + i), 256);
         }
         for (int i = 0; i < kPfRing; ++i) {
             tc::mbar_init(bar(SM::kSegFull + i), 1);
@@ -284,8 +299,9 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         // ================= O^T products =================
         PfNote g;
         int n = 0;
-        uint32_t runs0 = 0, runs1 = 0;  // runs (of a segment's tiles in a stream) begun
         while (true) {
+            const int ob = seg_no & 1;
+            const uint32_t use = (uint32_t)(seg_no >> 1);
             ok = take(g);
             if (!ok || g.s.nr == 0) break;
             // A and B MN-major. The second 64 rows of A: dims 64 .. 127, or, with D = 64, whatever follows the tile (lanes
@@ -294,12 +310,8 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             for (int t = 0; t < g.s.nt; ++t, ++n) {
                 const int sid = n & 1, vs = n % VS;
                 ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
-                if (t < 2) {  // the run before has been read out of O^T
-                    const uint32_t runs = sid ? runs1 : runs0;
-                    if (ok && runs > 0) ok = pf_wait(bar(SM::kOEmpty + sid), (runs - 1) & 1u);
-                    if (sid) ++runs1;
-                    else ++runs0;
-                }
+                // O^T of the segment two before has been read out
+                if (ok && t == 0) ok = pf_wait(bar(SM::kOEmpty + ob), (use & 1u) ^ 1u);
                 if (ok) ok = pf_wait(bar(SM::kPFull + sid), (uint32_t)(n >> 1) & 1u);
                 if (!ok) break;
                 tc::fence_after();
@@ -307,8 +319,8 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 const uint64_t dp = tc::desc_mnmajor(sb + SM::P + sid * SM::PB, 16384);
 #pragma unroll
                 for (int k = 0; k < kPfTile / 16; ++k)
-                    tc::mma_bf16_ss_w(tmem + SM::O_COL + sid * 64, dv + (uint64_t)k * (2048 >> 4), dp + (uint64_t)k * (2048 >> 4), id,
-                                      t >= 2 || k > 0 ? 1u : 0u);
+                    tc::mma_bf16_ss_w(tmem + SM::O_COL + ob * 64, dv + (uint64_t)k * (2048 >> 4), dp + (uint64_t)k * (2048 >> 4), id,
+                                      t > 0 || k > 0 ? 1u : 0u);
                 tc::commit_w(bar(SM::kODone + sid));
                 tc::commit_w(bar(SM::kVEmpty + vs));
             }
@@ -316,49 +328,49 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         }
         __syncwarp();
     } else {
-        // ================= softmax of the tiles n % 2 == sid; thread = key, then thread = dim =================
-        const int sid = warp >> 2, r = tid & 127, wq = warp & 3, bid = 1 + sid;
+        // ================= softmax of rows row0 .. row0 + H - 1; thread = key, then thread = dim =================
+        constexpr int H = NR / 2;
+        const int half = warp >> 2, r = tid & 127, wq = warp & 3, bid = 1 + half, row0 = half * H;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-        const uint32_t tS = tmem + lane_off + SM::S_COL + sid * 64, tO = tmem + lane_off + SM::O_COL + sid * 64;
-        unsigned char *s_p = s + SM::P + sid * SM::PB;
-        float *s_red = reinterpret_cast<float *>(s_p), *s_f = s_red + 4 * NR;
-        float *nms = s_ms + sid * NR, *s_sum = reinterpret_cast<float *>(s + SM::SUM) + sid * 4 * NR;
-        int *lims = s_lim + sid * NR;
+        float *nms = reinterpret_cast<float *>(s + SM::MS) + row0, *s_fac = reinterpret_cast<float *>(s + SM::FAC) + row0;
+        float *s_red = reinterpret_cast<float *>(s + SM::RED) + half * 4 * H;
+        int *lims = reinterpret_cast<int *>(s + SM::LIM) + row0;
         const float sl2 = a.scale * 1.4426950408889634f;
-        uint32_t tiles = 0;
         PfNote g;
         // A warp whose wait ran out says so and still comes to the barriers, and the warpgroup leaves together
         while (true) {
-            if (!take(g)) s_bad[sid] = 1;
+            const int ob = seg_no & 1;
+            if (!take(g)) s_bad[half] = 1;
             fw_bar(bid);
-            if (s_bad[sid]) {
+            if (s_bad[half]) {
                 ok = false;
                 break;
             }
             if (g.s.nr == 0) break;
             const PfSeg &seg = g.s;
-            const int t0 = (sid ^ g.n0) & 1;
-            if (t0 >= seg.nt) continue;
-            const int min_lim = pf_min_limit(a, seg), nc = (seg.nr + 15) / 16;
-            if (r < NR) {  // rows that are nobody's: -1 (they see nothing, where it is asked: in tiles with an edge)
-                const int lim = r < seg.nr ? pf_limit(a, seg, d, r) : -1;
+            const uint32_t tO = tmem + lane_off + SM::O_COL + ob * 64 + row0;
+            const int min_lim = pf_min_limit(a, seg), rows = min(seg.nr - row0, H);  // this warpgroup's (none: it keeps step)
+            if (r < H) {  // rows that are nobody's: -1 (they see nothing, where it is asked: in tiles with an edge)
+                const int lim = r < rows ? pf_limit(a, seg, d, row0 + r) : -1;
                 lims[r] = lim == INT32_MAX ? -1 : lim;
             }
             fw_bar(bid);
-            float l[NR];
+            float l[H];
 #pragma unroll
-            for (int i = 0; i < NR; ++i) l[i] = 0.0f;
-            for (int t = t0; t < seg.nt; t += 2, ++tiles) {
-                const int n = g.n0 + t, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
-                bool good = pf_wait(bar(SM::kInfo + sid), tiles & 1u);
+            for (int i = 0; i < H; ++i) l[i] = 0.0f;
+            for (int t = 0; t < seg.nt; ++t) {
+                const int n = g.n0 + t, sid = n & 1, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
+                const uint32_t turn = (uint32_t)(n >> 1), tS = tmem + lane_off + SM::S_COL + sid * 64 + row0;
+                unsigned char *s_p = s + SM::P + sid * SM::PB;
+                bool good = pf_wait(bar(SM::kInfo + sid), turn & 1u);
                 const int flags = s_flag[n % kFwFlags];
                 const bool edge = flags != 3 || base + kPfTile > min_lim;
-                // the O^T product before has read P^T, and O^T is at rest (and so every V filling before this tile's in its slot
-                // is over, which makes the wait for it by its parity exact)
-                if (good && tiles > 0) good = pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u);
-                good = good && pf_wait(bar(SM::kSFull + sid), tiles & 1u);
+                // P^T of the tile two before has been read (and so every V filling before this tile's in its slot is over,
+                // which makes the wait for it by its parity exact)
+                if (good && n >= 2) good = pf_wait(bar(SM::kODone + sid), (turn - 1) & 1u);
+                good = good && pf_wait(bar(SM::kSFull + sid), turn & 1u);
                 tc::fence_after();
-                if (edge && good) {
+                if (edge && good && half == 0) {
                     good = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
                     // a key behind the sequence's end weighs nothing, but 0 x NaN is NaN: its V row becomes zero
                     if (good && base + r >= seg.len) {
@@ -371,15 +383,16 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     }
                     __syncwarp();
                 }
+                if (!good) s_bad[half] = 1;
                 const bool page_ok = (flags >> (r >> 6)) & 1;
-                float p[NR];
+                float p[H];
                 // P^T of this key to shared memory, kept in p for the row sums; false if a term leaves the range
-                auto probs = [&]() {
+                auto probs = [&](auto with_edge) {
                     float2 sum = {0.0f, 0.0f};
-                    fw_ld<NR>(tS, p);
+                    fw_ld<H>(tS, p);
 #pragma unroll
-                    for (int c = 0; c < NR / 8; ++c) {
-                        if (c >= 2 * nc) break;
+                    for (int c = 0; c < H / 8; ++c) {
+                        if (8 * c >= rows) break;
                         uint32_t pk[4];
 #pragma unroll
                         for (int i = 0; i < 8; i += 4) {
@@ -389,7 +402,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                             float2 a1 = fma2({p[e + 2], p[e + 3]}, {sl2, sl2}, {off.z, off.w});
                             a0 = {ex2_approx(a0.x), ex2_approx(a0.y)};
                             a1 = {ex2_approx(a1.x), ex2_approx(a1.y)};
-                            if (edge) {
+                            if constexpr (decltype(with_edge)::value) {
                                 const int key = base + r;
                                 const int4 lim = *reinterpret_cast<const int4 *>(lims + e);
                                 a0 = {page_ok && key < lim.x ? a0.x : 0.0f, page_ok && key < lim.y ? a0.y : 0.0f};
@@ -403,138 +416,115 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                             pk[i / 2] = pack_bf16x2(a0.x, a0.y);
                             pk[i / 2 + 1] = pack_bf16x2(a1.x, a1.y);
                         }
-                        *reinterpret_cast<uint4 *>(s_p + tc::sw128(r, c)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        *reinterpret_cast<uint4 *>(s_p + tc::sw128(r, row0 / 8 + c)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
                     return sum.x + sum.y <= kFwSumMax;  // (not of an infinity or NaN)
                 };
-                if (t == t0) {  // the references: the first key, or the 65th where the first page is bad
+                if (t == 0) {  // the references: the first key, or the 65th where the first page is bad
                     const int lead = flags & 1 ? 0 : 64;
-                    if (r >> 5 == lead >> 5 && good) {
+                    if (r >> 5 == lead >> 5 && good && rows > 0) {
+                        fw_ld<H>(tS, p);
+                        if (lane == 0) {
 #pragma unroll
-                        for (int c = 0; c < NR / 16; ++c) {
-                            if (c >= nc) break;
-                            float x[16];
-                            __syncwarp();
-                            tc::tmem_ld16(tS + 16 * c, x);
-                            if (lane == 0) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const int lim = lims[16 * c + i];
-                                    nms[16 * c + i] = lim < 0 ? 0.0f : page_ok && base + lead < lim ? -x[i] * sl2 : INFINITY;
-                                }
+                            for (int i = 0; i < H; ++i) {
+                                const int lim = lims[i];
+                                nms[i] = lim < 0 ? 0.0f : page_ok && base + lead < lim ? -p[i] * sl2 : INFINITY;
                             }
                         }
+                        __syncwarp();
                     }
                     fw_bar(bid);
                 }
                 bool high = false;
-                if (good) high = !probs();
-                else s_bad[sid] = 1;
+                if (good && rows > 0) high = edge ? !probs(std::true_type{}) : !probs(std::false_type{});
                 const bool any = fw_bar_or(bid, high);
-                if (s_bad[sid]) {
+                if (s_bad[half]) {
                     ok = false;
                     break;
                 }
                 if (any) {
+                    // O^T is at rest once the tile before is in it
+                    if (n >= 1 && !pf_wait(bar(SM::kODone + (sid ^ 1)), (uint32_t)((n - 1) >> 1) & 1u)) s_bad[half] = 1;
                     tc::fence_after();
                     // maxima over the tile's keys, of logit * log2(e)
+                    fw_ld<H>(tS, p);
 #pragma unroll
-                    for (int c = 0; c < NR / 16; ++c) {
-                        if (c >= nc) break;
-                        float x[16];
-                        tc::tmem_ld16(tS + 16 * c, x);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const bool see = !edge || (page_ok && base + r < lims[16 * c + i]);
-                            const uint32_t u = __reduce_max_sync(0xffffffffu, float_to_ordered(see ? x[i] * sl2 : -INFINITY));
-                            if (lane == i) s_red[wq * NR + 16 * c + i] = ordered_to_float(u);
-                        }
+                    for (int i = 0; i < H; ++i) {
+                        const bool see = !edge || (page_ok && base + r < lims[i]);
+                        const uint32_t u = __reduce_max_sync(0xffffffffu, float_to_ordered(see ? p[i] * sl2 : -INFINITY));
+                        if (lane == i % 32) s_red[wq * H + i] = ordered_to_float(u);
                     }
                     fw_bar(bid);
-                    if (r < 16 * nc) {
-                        const float mx = fmaxf(fmaxf(s_red[r], s_red[NR + r]), fmaxf(s_red[2 * NR + r], s_red[3 * NR + r]));
+                    if (r < H) {
+                        const float mx = fmaxf(fmaxf(s_red[r], s_red[H + r]), fmaxf(s_red[2 * H + r], s_red[3 * H + r]));
                         const float old = -nms[r];
                         const bool grow = mx - old > kFwGrow;  // from -inf, too; not where nothing is visible yet (-inf, NaN)
-                        s_f[r] = grow ? ex2_approx(old - mx) : 1.0f;
+                        s_fac[r] = grow ? ex2_approx(old - mx) : 1.0f;
                         if (grow) nms[r] = -mx;
                     }
                     fw_bar(bid);
+                    if (t > 0) fw_ld<H>(tO, p);
 #pragma unroll
-                    for (int c = 0; c < NR / 16; ++c) {
-                        if (c >= nc) break;
-                        float f[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            f[i] = s_f[16 * c + i];
-                            l[16 * c + i] *= f[i];
-                        }
-                        if (t > t0) {
-                            float o[16];
-                            uint32_t u[16];
-                            tc::tmem_ld16(tO + 16 * c, o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * f[i]);
-                            tc::tmem_st16(tO + 16 * c, u);
-                        }
+                    for (int i = 0; i < H; ++i) {
+                        const float f = s_fac[i];
+                        l[i] *= f;
+                        p[i] *= f;
                     }
-                    fw_bar(bid);  // the scratch has been read: P^T may go there
-                    probs();
+                    if (t > 0) fw_st<H>(tO, p);
+                    if (edge) probs(std::true_type{});
+                    else probs(std::false_type{});
                 }
                 tc::fence_proxy_async_smem();  // P^T, and V rows made zero
                 tc::fence_before();
                 tc::mbar_arrive(bar(SM::kPFull + sid));
 #pragma unroll
-                for (int i = 0; i < NR; i += 2) {  // (the rows beyond the segment's hold sums of nothing)
-                    if (i >= 16 * nc) break;
+                for (int i = 0; i < H; i += 2) {
+                    if (i >= rows) break;
                     const float2 sum = add2({l[i], l[i + 1]}, {p[i], p[i + 1]});
                     l[i] = sum.x;
                     l[i + 1] = sum.y;
                 }
             }
             if (!ok) break;
-            // the warp's row sums: each step halves the rows a lane holds
+            // the warp's row sums: each step halves the rows a lane holds (8, 16 or 32 rows over 32 lanes)
 #pragma unroll
-            for (int c = 0; c < NR / 16; ++c) {
-                if (c >= nc) break;
-                float v[16];
+            for (int h = 16; h >= H; h >>= 1)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = l[16 * c + i] + __shfl_xor_sync(0xffffffffu, l[16 * c + i], 16);
+                for (int i = 0; i < H; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], h);
 #pragma unroll
-                for (int h = 8; h > 0; h >>= 1) {
-                    const bool up = lane & h;
+            for (int h = H / 2; h > 0; h >>= 1) {
+                const bool up = lane & h;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (i < h) {
-                            const float send = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
-                            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, h);
-                        }
+                for (int i = 0; i < H / 2; ++i) {
+                    if (i < h) {
+                        const float send = up ? l[i] : l[i + h], keep = up ? l[i + h] : l[i];
+                        l[i] = keep + __shfl_xor_sync(0xffffffffu, send, h);
                     }
                 }
-                if (lane < 16) s_sum[wq * NR + 16 * c + lane] = v[0];
             }
-            const int64_t at = (int64_t)seg.part * (seg.b < 0 ? d.strideP : d.strideO) + (t0 == 0 ? 0 : seg.nr);
+            if (lane < H) s_red[wq * H + lane] = l[0];
+            const int64_t at = (int64_t)seg.part * (seg.b < 0 ? d.strideP : d.strideO) + row0;
             float *O = (seg.b < 0 ? w.Op : w.Oo) + at * D;
             fw_bar(bid);
-            if (r < seg.nr) {
-                const float sum = (s_sum[r] + s_sum[NR + r]) + (s_sum[2 * NR + r] + s_sum[3 * NR + r]);
+            if (r < rows) {
+                const float sum = (s_red[r] + s_red[H + r]) + (s_red[2 * H + r] + s_red[3 * H + r]);
                 reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at + r] = make_float2(-nms[r], sum);
             }
-            if (!pf_wait(bar(SM::kODone + sid), (tiles - 1) & 1u)) s_bad[sid] = 1;  // seen at the next barrier
+            const int last = g.n0 + seg.nt - 1;
+            if (!pf_wait(bar(SM::kODone + (last & 1)), (uint32_t)(last >> 1) & 1u)) s_bad[half] = 1;  // seen at the next barrier
             tc::fence_after();
-#pragma unroll
-            for (int c = 0; c < NR / 16; ++c) {
-                if (c >= nc) break;
-                float o[16];
-                __syncwarp();
-                tc::tmem_ld16(tO + 16 * c, o);
+            if (rows > 0) {
+                float o[H];
+                fw_ld<H>(tO, o);
                 if (r < D) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (16 * c + i < seg.nr) O[(size_t)(16 * c + i) * D + r] = o[i];
+                    for (int i = 0; i < H; ++i)
+                        if (i < rows) O[(size_t)i * D + r] = o[i];
                 }
+                __syncwarp();
             }
             tc::fence_before();
-            tc::mbar_arrive(bar(SM::kOEmpty + sid));
+            tc::mbar_arrive(bar(SM::kOEmpty + ob));
         }
     }
     if (!ok) s_bad[2] = 1;

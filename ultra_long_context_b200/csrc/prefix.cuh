@@ -22,7 +22,7 @@ constexpr int kPfWideRows = 256;  // in the wide kernel
 constexpr int kPfCtas = 148;      // at most: one per SM; the workspace is sized for it
 constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per head and row group)
 // Costs in half tiles: a tile, and what a segment's start and end take beside its tiles
-constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 2;
+constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 3;
 
 // The division of one kernel's work; every CTA computes the same, CTA 0 stores it for the join.
 //   prefix: per key head and row group (a unit), `nsplit` runs of `run` tiles; segment i = run i / units of unit
@@ -327,16 +327,22 @@ __device__ __forceinline__ void pf_prefetch_tmap(const CUtensorMap *m) {
 }
 
 // A bounded wait of a whole warp, with one answer for all lanes: the warp is converged behind it, which the
-// aligned tcgen05 loads and stores that follow need. A probe may suspend the thread for tens of microseconds, so
-// 2^15 of them are seconds.
+// aligned tcgen05 loads and stores that follow need. All lanes wait: where one did it for the others the warp was not put to
+// sleep, and twelve such warps took the issue slots of the softmax (every kernel 1.3 to 1.9 times slower). A probe
+// may suspend the thread for tens of microseconds, so 2^15 of them are seconds.
 __device__ __forceinline__ bool pf_wait(uint32_t mbar, uint32_t parity) {
-    return __all_sync(0xffffffffu, tc::mbar_wait_n(mbar, parity, 1u << 15)) != 0;
+    return __all_sync(0xffffffffu, tc::mbar_wait_n(mbar, parity & 1u, 1u << 15)) != 0;
 }
 __device__ __forceinline__ bool pf_wait_lane(uint32_t mbar, uint32_t parity) {
-    return tc::mbar_wait_n(mbar, parity, 1u << 15);
+    return tc::mbar_wait_n(mbar, parity & 1u, 1u << 15);
+}
+// One arrival for the warp, behind what all its lanes did.
+__device__ __forceinline__ void pf_arrive(uint32_t mbar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(mbar);
 }
 __device__ __forceinline__ bool pf_done(uint32_t mbar, uint32_t parity) {
-    return __all_sync(0xffffffffu, tc::mbar_test(mbar, parity)) != 0;
+    return __all_sync(0xffffffffu, tc::mbar_test(mbar, parity & 1u)) != 0;
 }
 __device__ __forceinline__ void pf_cp_async_arrive(uint32_t mbar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(mbar) : "memory");

@@ -16,7 +16,7 @@
 //   warps 0-3, 4-7  softmax of the lower and the upper half of the rows, both on every tile (in turn on the tiles, 64 rows
 //               a thread, they took 1800 cycles a tile where this takes TODO, and kept two partials);
 //               S^T and P^T of two tiles, so that the products of one run under the softmax of the other;
-//   warp 8      issues S^T(n), in order, when its operands are there and S^T(n - 2) has been read;
+//   warp 8      issues S^T(n), in order, when its operands are there and O^T(n - 2) is done (S^T and P^T are free);
 //   warp 9      issues O^T(n), in order, when P^T(n) and V are there. (Two warps that sleep in their waits: one that polled
 //               for both took issue slots from the softmax warps beside it.) O^T of two segments, so that one is
 //               read out under the next one's products;
@@ -48,7 +48,7 @@ struct FwSmem {
     static constexpr uint32_t K = 0, V = K + KS * OP, P = V + VS * OP, Q = P + 2 * PB;
     static constexpr uint32_t BAR = Q + 2 * QB;
     static constexpr int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = 2 * KS + VS, kQFull = 2 * KS + 2 * VS,
-                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kInfo = kSFull + 2, kPFull = kInfo + 2,
+                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 2,
                          kODone = kPFull + 2, kOEmpty = kODone + 2, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kPfRing,
                          NBAR = kSegEmpty + kPfRing;
     static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;
@@ -137,11 +137,10 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(SM::kQFull + i), 32);
             tc::mbar_init(bar(SM::kQEmpty + i), 1);
-            tc::mbar_init(bar(SM::kSFull + i), 1);
-            tc::mbar_init(bar(SM::kInfo + i), 1);
-            tc::mbar_init(bar(SM::kPFull + i), 256);
+            tc::mbar_init(bar(SM::kSFull + i), 2);  // the product, and the warp that issued it (page flags)
+            tc::mbar_init(bar(SM::kPFull + i), 8);  // a softmax warp each
             tc::mbar_init(bar(SM::kODone + i), 1);
-            tc::mbar_init(bar(SM::kOEmpty + i), 256);
+            tc::mbar_init(bar(SM::kOEmpty + i), 8);
         }
         for (int i = 0; i < kPfRing; ++i) {
             tc::mbar_init(bar(SM::kSegFull + i), 1);
@@ -276,13 +275,13 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             const uint64_t dq = tc::desc_kmajor(sb + SM::Q + q * SM::QB);
             for (int t = 0; t < g.s.nt; ++t, ++n) {
                 const int sid = n & 1, ks = n % KS;
-                ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS) & 1u) && (t > 0 || pf_wait(bar(SM::kQFull + q), use & 1u));
-                // P^T of the tile two before is written: its S^T has been read
-                if (ok && n >= 2) ok = pf_wait(bar(SM::kPFull + sid), (uint32_t)((n - 2) >> 1) & 1u);
+                ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS)) && (t > 0 || pf_wait(bar(SM::kQFull + q), use));
+                // S^T and P^T of the tile two before have been read
+                if (ok && n >= 2) ok = pf_wait(bar(SM::kODone + sid), (uint32_t)((n - 2) >> 1));
                 if (!ok) break;
                 tc::fence_after();
                 if (t == 0) tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
-                if (lane == 0) tc::mbar_arrive(bar(SM::kInfo + sid));  // hands on the page flags that came with K
+                if (lane == 0) tc::mbar_arrive(bar(SM::kSFull + sid));  // hands on the page flags that came with K
                 const uint64_t dk = tc::desc_kmajor(sb + SM::K + ks * SM::OP);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)  // (a descriptor's low bits are its address / 16)
@@ -309,10 +308,10 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             const uint32_t id = tc::idesc_bf16(128, (g.s.nr + 15) / 16 * 16, 1, 1);
             for (int t = 0; t < g.s.nt; ++t, ++n) {
                 const int sid = n & 1, vs = n % VS;
-                ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
+                ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS));
                 // O^T of the segment two before has been read out
-                if (ok && t == 0) ok = pf_wait(bar(SM::kOEmpty + ob), (use & 1u) ^ 1u);
-                if (ok) ok = pf_wait(bar(SM::kPFull + sid), (uint32_t)(n >> 1) & 1u);
+                if (ok && t == 0) ok = pf_wait(bar(SM::kOEmpty + ob), use ^ 1u);
+                if (ok) ok = pf_wait(bar(SM::kPFull + sid), (uint32_t)(n >> 1));
                 if (!ok) break;
                 tc::fence_after();
                 const uint64_t dv = tc::desc_mnmajor(sb + SM::V + vs * SM::OP, 16384);
@@ -362,27 +361,12 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 const int n = g.n0 + t, sid = n & 1, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
                 const uint32_t turn = (uint32_t)(n >> 1), tS = tmem + lane_off + SM::S_COL + sid * 64 + row0;
                 unsigned char *s_p = s + SM::P + sid * SM::PB;
-                bool good = pf_wait(bar(SM::kInfo + sid), turn & 1u);
+                // S^T is there, with its tile's page flags, and P^T of the tile two before has been read (so every V filling
+                // before this tile's in its slot is over, too, which makes the wait for it by its parity exact)
+                const bool good = pf_wait(bar(SM::kSFull + sid), turn);
+                tc::fence_after();
                 const int flags = s_flag[n % kFwFlags];
                 const bool edge = flags != 3 || base + kPfTile > min_lim;
-                // P^T of the tile two before has been read (and so every V filling before this tile's in its slot is over,
-                // which makes the wait for it by its parity exact)
-                if (good && n >= 2) good = pf_wait(bar(SM::kODone + sid), (turn - 1) & 1u);
-                good = good && pf_wait(bar(SM::kSFull + sid), turn & 1u);
-                tc::fence_after();
-                if (edge && good && half == 0) {
-                    good = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
-                    // a key behind the sequence's end weighs nothing, but 0 x NaN is NaN: its V row becomes zero
-                    if (good && base + r >= seg.len) {
-#pragma unroll
-                        for (int h = 0; h < SM::KH; ++h) {
-                            uint4 *row = reinterpret_cast<uint4 *>(s + SM::V + vs * SM::OP + h * 16384 + r * 128);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    __syncwarp();
-                }
                 if (!good) s_bad[half] = 1;
                 const bool page_ok = (flags >> (r >> 6)) & 1;
                 float p[H];
@@ -474,9 +458,21 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     if (edge) probs(std::true_type{});
                     else probs(std::false_type{});
                 }
+                // a key behind the sequence's end weighs nothing, but 0 x NaN is NaN: its V row becomes zero
+                if (half == 0 && base + kPfTile > seg.len) {
+                    if (!pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS))) s_bad[half] = 1;  // seen at the next barrier
+                    if (base + r >= seg.len) {
+#pragma unroll
+                        for (int h = 0; h < SM::KH; ++h) {
+                            uint4 *row = reinterpret_cast<uint4 *>(s + SM::V + vs * SM::OP + h * 16384 + r * 128);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                }
                 tc::fence_proxy_async_smem();  // P^T, and V rows made zero
                 tc::fence_before();
-                tc::mbar_arrive(bar(SM::kPFull + sid));
+                pf_arrive(bar(SM::kPFull + sid));
 #pragma unroll
                 for (int i = 0; i < H; i += 2) {
                     if (i >= rows) break;
@@ -524,7 +520,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 __syncwarp();
             }
             tc::fence_before();
-            tc::mbar_arrive(bar(SM::kOEmpty + ob));
+            pf_arrive(bar(SM::kOEmpty + ob));
         }
     }
     if (!ok) s_bad[2] = 1;

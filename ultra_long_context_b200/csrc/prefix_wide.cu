@@ -37,7 +37,7 @@ struct PfSmem {
     static constexpr uint32_t BAR = V + VS * OP;
     // mbarriers
     static constexpr int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = 2 * KS + VS, kQFull = 2 * KS + 2 * VS,
-                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kInfo = kSFull + 2, kPFull = kInfo + 2,
+                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 2,
                          kODone = kPFull + 2, kOEmpty = kODone + 2, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kPfRing,
                          NBAR = kSegEmpty + kPfRing;
     static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;  // PfNote[kPfRing]
@@ -108,11 +108,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(SM::kQFull + i), 32 * kPfQWarps);
             tc::mbar_init(bar(SM::kQEmpty + i), 1);
-            tc::mbar_init(bar(SM::kSFull + i), 1);
-            tc::mbar_init(bar(SM::kInfo + i), 1);
-            tc::mbar_init(bar(SM::kPFull + i), 32 * kPfStreamWarps);
+            tc::mbar_init(bar(SM::kSFull + i), 2);  // the product, and the warp that issued it (page flags)
+            tc::mbar_init(bar(SM::kPFull + i), kPfStreamWarps);
             tc::mbar_init(bar(SM::kODone + i), 1);
-            tc::mbar_init(bar(SM::kOEmpty + i), 32 * kPfStreamWarps);
+            tc::mbar_init(bar(SM::kOEmpty + i), kPfStreamWarps);
         }
         for (int i = 0; i < kPfRing; ++i) {
             tc::mbar_init(bar(SM::kSegFull + i), 1);
@@ -256,16 +255,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         int nt = 0, items = 0, u = 0, q0 = 0, turn = 0;  // of the segment at item i_s: u is the item's number in it
         bool both = false, end = false;
         uint32_t uses0 = 0, uses1 = 0;                   // fillings of the Q buffers before this segment's
-        int i_s = 0, i_o = 0;                            // next items
+        int i_s = 0, i_o = 0, v_last = -1;               // next items; the tile whose V was waited for last
         uint32_t issued[2] = {0, 0}, runs[2] = {0, 0};   // O products of a stream; its runs (one per segment) begun
         int tile[2] = {0, 0};                            // of the stream's item at O: its tile's number,
         bool first[2] = {false, false}, last[2] = {false, false};  // does it begin a run; is it the tile's last item
         auto issue_s = [&](const int sid) {
             const int t = both ? u >> 1 : u, n = g.n0 + t, ks = n % KS, q = both ? u & 1 : q0;
             const bool starts = both ? u < 2 : u == 0;  // the first to read its Q buffer
-            ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS) & 1u);
-            if (ok && starts) ok = pf_wait(bar(SM::kQFull + q), (q ? uses1 : uses0) & 1u);
-            if (ok && lane == 0) tc::mbar_arrive(bar(SM::kInfo + sid));  // hands on the page flags that came with K
+            if (!both || !(u & 1)) ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS));  // (once for a tile)
+            if (ok && starts) ok = pf_wait(bar(SM::kQFull + q), q ? uses1 : uses0);
+            if (ok && lane == 0) tc::mbar_arrive(bar(SM::kSFull + sid));  // hands on the page flags that came with K
             // S and P share columns: P of the stream's item before must have been read
             if (ok && issued[sid] > 0) ok = pf_wait(bar(SM::kODone + sid), (issued[sid] - 1) & 1u);
             if (!ok) return;
@@ -290,9 +289,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         auto issue_o = [&](const int sid) {
             const int n = tile[sid], vs = n % VS;
             // (what is there long before comes first, so that only the wait for P is followed by the products)
-            ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS) & 1u);
-            if (ok && first[sid] && runs[sid] > 1) ok = pf_wait(bar(SM::kOEmpty + sid), (runs[sid] - 2) & 1u);
-            if (ok) ok = pf_wait(bar(SM::kPFull + sid), issued[sid] & 1u);
+            if (n != v_last) ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS));  // (once for a tile)
+            v_last = n;
+            if (ok && first[sid] && runs[sid] > 1) ok = pf_wait(bar(SM::kOEmpty + sid), runs[sid]);
+            if (ok) ok = pf_wait(bar(SM::kPFull + sid), issued[sid]);
             if (!ok) return;
             tc::fence_after();
             const uint64_t dv = tc::desc_mnmajor(sb + SM::V + vs * SM::OP, 16384);
@@ -368,11 +368,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             for (int t = t0; t < seg.nt; t += dt, ++tiles) {
                 const int n = g.n0 + t, vs = n % VS;
                 const int base = (seg.tile0 + t) * kPfTile;
-                bool good = pf_wait(bar(SM::kInfo + sid), tiles & 1u);
+                bool good = pf_wait(bar(SM::kSFull + sid), tiles);
                 const int flags = s_flag[n % kPfFlags];
                 const int vis = (flags >> half) & 1 ? lim - base - 64 * half : 0;  // keys of this half that the row sees
                 const bool edge = __any_sync(0xffffffffu, vis < 64);
-                good = good && pf_wait(bar(SM::kSFull + sid), tiles & 1u);
                 tc::fence_after();
                 if (!good) s_badp[pid - 1] = 1;
                 if (active) {
@@ -468,7 +467,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                     tc::fence_proxy_async_smem();
                 }
                 tc::fence_before();
-                tc::mbar_arrive(bar(SM::kPFull + sid));
+                pf_arrive(bar(SM::kPFull + sid));
             }
             if (!ok) break;
             // (warps without a row wait as well: they must not come to the next segment's end before this one's)
@@ -501,7 +500,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                 pf_pair_bar(pid);  // s_row is written again by the next segment
             }
             tc::fence_before();
-            tc::mbar_arrive(bar(SM::kOEmpty + sid));
+            pf_arrive(bar(SM::kOEmpty + sid));
         }
     }
     if (!ok) *s_bad = 1;  // (any thread's)

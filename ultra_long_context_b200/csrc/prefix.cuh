@@ -22,7 +22,7 @@ constexpr int kPfWideRows = 256;  // in the wide kernel
 constexpr int kPfCtas = 148;      // at most: one per SM; the workspace is sized for it
 constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per head and row group)
 // Costs in half tiles: a tile, and what a segment's start and end take beside its tiles
-constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 3;
+constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 4;
 
 // The division of one kernel's work; every CTA computes the same, CTA 0 stores it for the join.
 //   prefix: per key head and row group (a unit), `nsplit` runs of `run` tiles; segment i = run i / units of unit
@@ -49,6 +49,7 @@ struct PfDims {
     int Rp, gp, Rgp;       // prefix rows per key head, in Rgp groups of gp
     int Ro, Rgo;           // own rows per request and key head, in groups of kPfFewRows
     int strideP, strideO;  // rows of one segment's partials (in the wide kernel, two streams may each keep one of the same rows)
+    int prefix_tile;       // cost of a prefix tile in half tiles: those of 64 rows and D = 64 take twice the time of their bytes
     int max_items, max_slots, blocks;  // blocks: of 32 requests
     // Which kernel ends the prefix sooner? A tile of 128 keys takes the few-rows kernel 1.15 us (D = 128; half that with
     // D = 64: its bytes) for 64 rows, the wide one 2.3 us for 256, and that is a launch of its own, 12 us before the
@@ -69,6 +70,7 @@ struct PfDims {
         Rgo = (Ro + kPfFewRows - 1) / kPfFewRows;
         strideP = wide ? kPfWideRows : Rp < kPfFewRows ? Rp : kPfFewRows;
         strideO = Ro < kPfFewRows ? Ro : kPfFewRows;
+        prefix_tile = kPfTileCost;
         const int units = Hkv * Rgp;
         int ns = kPfItems / units;
         ns = ns < 1 ? 1 : ns;
@@ -282,7 +284,7 @@ __device__ void pf_schedule(const PrefixArgs &a, const PfDims &d, bool prefix, b
             const int ns_max = min(max(kPfItems / units, 1), tiles);
             const float quarter = (float)ctas * 0.25f / (float)units;
             const int ns = min(max(lane < 16 ? lane + 1 : (int)((float)(lane - 15) * quarter), 1), ns_max);
-            const float run = ceilf(__fdividef((float)tiles, (float)ns) - 1e-3f), cost = kPfTileCost * run + kPfPrefixCost;
+            const float run = ceilf(__fdividef((float)tiles, (float)ns) - 1e-3f), cost = d.prefix_tile * run + kPfPrefixCost;
             const float items = (float)units * ceilf(__fdividef((float)tiles, run) - 1e-3f);
             const float waves = ceilf(__fdividef(items, (float)ctas) - 1e-3f) * cost;
             const float even = __fdividef(items * cost + (float)axis, (float)ctas);
@@ -293,7 +295,7 @@ __device__ void pf_schedule(const PrefixArgs &a, const PfDims &d, bool prefix, b
             p.nsplit = (tiles + p.run - 1) / p.run;
             p.items = units * p.nsplit;
         }
-        const int64_t cost = kPfTileCost * p.run + kPfPrefixCost;
+        const int64_t cost = d.prefix_tile * p.run + kPfPrefixCost;
         const int waves = p.items / ctas;
         p.lo_ctas = p.items - waves * ctas;
         const int64_t pc_hi = waves * cost, pc_lo = pc_hi + cost;

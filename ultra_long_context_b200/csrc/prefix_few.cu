@@ -15,8 +15,8 @@
 // Persistent, warp-specialised, one CTA per SM; the CTA's tiles are numbered through all its segments:
 //   warps 0-3, 4-7  softmax of the lower and the upper half of the rows, both on every tile (in turn on the tiles, 64 rows
 //               a thread, they took 1800 cycles a tile where this takes TODO, and kept two partials);
-//               S^T and P^T of two tiles, so that the products of one run under the softmax of the other;
-//   warp 8      issues S^T(n), in order, when its operands are there and O^T(n - 2) is done (S^T and P^T are free);
+//               S^T and P^T of two or four tiles, so that the products of one run under the softmax of another;
+//   warp 8      issues S^T(n), in order, when its operands are there and its S^T and P^T buffers have been read;
 //   warp 9      issues O^T(n), in order, when P^T(n) and V are there. (Two warps that sleep in their waits: one that polled
 //               for both took issue slots from the softmax warps beside it.) O^T of two segments, so that one is
 //               read out under the next one's products;
@@ -43,13 +43,16 @@ struct FwSmem {
     static constexpr uint32_t OP = KH * 16384;            // one K or V tile [128][D]
     static constexpr uint32_t QB = KH * NR * 128;         // Q rows [NR][D]
     static constexpr uint32_t PB = 16384;                 // P^T [128 keys][64 rows]
-    static constexpr int KS = D == 64 ? 4 : 2, VS = D == 64 ? 5 : NR == 64 ? 2 : 3;
-    static_assert(KS + 4 <= kFwFlags, "page flags");
-    static constexpr uint32_t K = 0, V = K + KS * OP, P = V + VS * OP, Q = P + 2 * PB;
+    static constexpr int KS = D == 64 ? 4 : 2, VS = D == 64 ? 4 : NR == 64 ? 2 : 3;
+    // S^T and P^T buffers. A tile goes through its products and its softmax in some 2500 cycles; its bytes take half
+    // as long with D = 64, so four tiles are on their way there, two with D = 128.
+    static constexpr int NB = D == 64 ? 4 : 2;
+    static_assert(KS + NB <= kFwFlags && VS >= NB, "page flags, V waits");
+    static constexpr uint32_t K = 0, V = K + KS * OP, P = V + VS * OP, Q = P + NB * PB;
     static constexpr uint32_t BAR = Q + 2 * QB;
     static constexpr int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = 2 * KS + VS, kQFull = 2 * KS + 2 * VS,
-                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 2,
-                         kODone = kPFull + 2, kOEmpty = kODone + 2, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kPfRing,
+                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + NB,
+                         kODone = kPFull + NB, kOEmpty = kODone + NB, kSegFull = kOEmpty + 2, kSegEmpty = kSegFull + kPfRing,
                          NBAR = kSegEmpty + kPfRing;
     static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;
     static constexpr uint32_t MS = RING + kPfRing * sizeof(PfNote);       // float[NR]: -m * scale * log2(e), inf while a row sees nothing
@@ -61,7 +64,7 @@ struct FwSmem {
     static constexpr uint32_t PLAN = (MISC + 16 + 15) / 16 * 16;
     static constexpr uint32_t BCUM = PLAN + (sizeof(PfPlan) + 15) / 16 * 16;  // int[blocks + 1]
     static constexpr size_t dyn(int blocks) { return BCUM + 4 * ((size_t)blocks + 1) + 1024; }  // slack: 1 KB alignment
-    static constexpr uint32_t S_COL = 0, O_COL = 128, TMEM_COLS = 256;
+    static constexpr uint32_t S_COL = 0, O_COL = NB * 64, TMEM_COLS = NB == 4 ? 512 : 256;
 };
 static_assert(FwSmem<128, 64>::dyn(256) <= 227 * 1024 && FwSmem<128, 32>::dyn(256) <= 227 * 1024 &&
                   FwSmem<64, 64>::dyn(256) <= 227 * 1024,
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                                                                    const __grid_constant__ CUtensorMap tmK,
                                                                    const __grid_constant__ CUtensorMap tmV) {
     using SM = FwSmem<D, NR>;
-    constexpr int KS = SM::KS, VS = SM::VS;
+    constexpr int KS = SM::KS, VS = SM::VS, NB = SM::NB;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;  // 1 KB aligned (swizzle atoms)
@@ -137,10 +140,12 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(SM::kQFull + i), 32);
             tc::mbar_init(bar(SM::kQEmpty + i), 1);
+            tc::mbar_init(bar(SM::kOEmpty + i), 8);
+        }
+        for (int i = 0; i < NB; ++i) {
             tc::mbar_init(bar(SM::kSFull + i), 2);  // the product, and the warp that issued it (page flags)
             tc::mbar_init(bar(SM::kPFull + i), 8);  // a softmax warp each
             tc::mbar_init(bar(SM::kODone + i), 1);
-            tc::mbar_init(bar(SM::kOEmpty + i), 8);
         }
         for (int i = 0; i < kPfRing; ++i) {
             tc::mbar_init(bar(SM::kSegFull + i), 1);
@@ -274,20 +279,20 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             const uint32_t id = tc::idesc_bf16(128, (g.s.nr + 15) / 16 * 16, 0, 0);
             const uint64_t dq = tc::desc_kmajor(sb + SM::Q + q * SM::QB);
             for (int t = 0; t < g.s.nt; ++t, ++n) {
-                const int sid = n & 1, ks = n % KS;
+                const int buf = n % NB, ks = n % KS;
                 ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS)) && (t > 0 || pf_wait(bar(SM::kQFull + q), use));
-                // S^T and P^T of the tile two before have been read
-                if (ok && n >= 2) ok = pf_wait(bar(SM::kODone + sid), (uint32_t)((n - 2) >> 1));
+                // S^T and P^T of the tile that had their buffers before have been read
+                if (ok && n >= NB) ok = pf_wait(bar(SM::kODone + buf), (uint32_t)(n / NB - 1));
                 if (!ok) break;
                 tc::fence_after();
                 if (t == 0) tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
-                if (lane == 0) tc::mbar_arrive(bar(SM::kSFull + sid));  // hands on the page flags that came with K
+                if (lane == 0) tc::mbar_arrive(bar(SM::kSFull + buf));  // hands on the page flags that came with K
                 const uint64_t dk = tc::desc_kmajor(sb + SM::K + ks * SM::OP);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)  // (a descriptor's low bits are its address / 16)
-                    tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * 64, dk + ((uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                    tc::mma_bf16_ss_w(tmem + SM::S_COL + buf * 64, dk + ((uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4),
                                       dq + ((uint64_t)((k >> 2) * (NR * 128) + (k & 3) * 32) >> 4), id, k > 0 ? 1u : 0u);
-                tc::commit_w(bar(SM::kSFull + sid));
+                tc::commit_w(bar(SM::kSFull + buf));
                 tc::commit_w(bar(SM::kKEmpty + ks));
                 if (t == g.s.nt - 1) tc::commit_w(bar(SM::kQEmpty + q));
             }
@@ -307,20 +312,20 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             // that are not read)
             const uint32_t id = tc::idesc_bf16(128, (g.s.nr + 15) / 16 * 16, 1, 1);
             for (int t = 0; t < g.s.nt; ++t, ++n) {
-                const int sid = n & 1, vs = n % VS;
+                const int buf = n % NB, vs = n % VS;
                 ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS));
                 // O^T of the segment two before has been read out
                 if (ok && t == 0) ok = pf_wait(bar(SM::kOEmpty + ob), use ^ 1u);
-                if (ok) ok = pf_wait(bar(SM::kPFull + sid), (uint32_t)(n >> 1));
+                if (ok) ok = pf_wait(bar(SM::kPFull + buf), (uint32_t)(n / NB));
                 if (!ok) break;
                 tc::fence_after();
                 const uint64_t dv = tc::desc_mnmajor(sb + SM::V + vs * SM::OP, 16384);
-                const uint64_t dp = tc::desc_mnmajor(sb + SM::P + sid * SM::PB, 16384);
+                const uint64_t dp = tc::desc_mnmajor(sb + SM::P + buf * SM::PB, 16384);
 #pragma unroll
                 for (int k = 0; k < kPfTile / 16; ++k)
                     tc::mma_bf16_ss_w(tmem + SM::O_COL + ob * 64, dv + (uint64_t)k * (2048 >> 4), dp + (uint64_t)k * (2048 >> 4), id,
                                       t > 0 || k > 0 ? 1u : 0u);
-                tc::commit_w(bar(SM::kODone + sid));
+                tc::commit_w(bar(SM::kODone + buf));
                 tc::commit_w(bar(SM::kVEmpty + vs));
             }
             if (!ok) break;
@@ -354,16 +359,23 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 lims[r] = lim == INT32_MAX ? -1 : lim;
             }
             fw_bar(bid);
-            float l[H];
+            float l[H], off[H];  // sums over this thread's keys; the references (nms) at hand
 #pragma unroll
-            for (int i = 0; i < H; ++i) l[i] = 0.0f;
+            for (int i = 0; i < H; ++i) l[i] = off[i] = 0.0f;
+            auto load_off = [&]() {
+#pragma unroll
+                for (int i = 0; i < H; i += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(nms + i);
+                    off[i] = v.x, off[i + 1] = v.y, off[i + 2] = v.z, off[i + 3] = v.w;
+                }
+            };
             for (int t = 0; t < seg.nt; ++t) {
-                const int n = g.n0 + t, sid = n & 1, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
-                const uint32_t turn = (uint32_t)(n >> 1), tS = tmem + lane_off + SM::S_COL + sid * 64 + row0;
-                unsigned char *s_p = s + SM::P + sid * SM::PB;
-                // S^T is there, with its tile's page flags, and P^T of the tile two before has been read (so every V filling
-                // before this tile's in its slot is over, too, which makes the wait for it by its parity exact)
-                const bool good = pf_wait(bar(SM::kSFull + sid), turn);
+                const int n = g.n0 + t, buf = n % NB, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
+                const uint32_t tS = tmem + lane_off + SM::S_COL + buf * 64 + row0;
+                unsigned char *s_p = s + SM::P + buf * SM::PB;
+                // S^T is there, with its tile's page flags, and P^T's buffer has been read (so every V filling before this
+                // tile's in its slot is over, too, which makes the wait for it by its parity exact)
+                const bool good = pf_wait(bar(SM::kSFull + buf), (uint32_t)(n / NB));
                 tc::fence_after();
                 const int flags = s_flag[n % kFwFlags];
                 const bool edge = flags != 3 || base + kPfTile > min_lim;
@@ -381,9 +393,8 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
 #pragma unroll
                         for (int i = 0; i < 8; i += 4) {
                             const int e = 8 * c + i;
-                            const float4 off = *reinterpret_cast<const float4 *>(nms + e);
-                            float2 a0 = fma2({p[e], p[e + 1]}, {sl2, sl2}, {off.x, off.y});
-                            float2 a1 = fma2({p[e + 2], p[e + 3]}, {sl2, sl2}, {off.z, off.w});
+                            float2 a0 = fma2({p[e], p[e + 1]}, {sl2, sl2}, {off[e], off[e + 1]});
+                            float2 a1 = fma2({p[e + 2], p[e + 3]}, {sl2, sl2}, {off[e + 2], off[e + 3]});
                             a0 = {ex2_approx(a0.x), ex2_approx(a0.y)};
                             a1 = {ex2_approx(a1.x), ex2_approx(a1.y)};
                             if constexpr (decltype(with_edge)::value) {
@@ -418,6 +429,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                         __syncwarp();
                     }
                     fw_bar(bid);
+                    load_off();
                 }
                 bool high = false;
                 if (good && rows > 0) high = edge ? !probs(std::true_type{}) : !probs(std::false_type{});
@@ -428,7 +440,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 }
                 if (any) {
                     // O^T is at rest once the tile before is in it
-                    if (n >= 1 && !pf_wait(bar(SM::kODone + (sid ^ 1)), (uint32_t)((n - 1) >> 1) & 1u)) s_bad[half] = 1;
+                    if (n >= 1 && !pf_wait(bar(SM::kODone + (n - 1) % NB), (uint32_t)((n - 1) / NB))) s_bad[half] = 1;
                     tc::fence_after();
                     // maxima over the tile's keys, of logit * log2(e)
                     fw_ld<H>(tS, p);
@@ -447,6 +459,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                         if (grow) nms[r] = -mx;
                     }
                     fw_bar(bid);
+                    load_off();
                     if (t > 0) fw_ld<H>(tO, p);
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
@@ -472,7 +485,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 }
                 tc::fence_proxy_async_smem();  // P^T, and V rows made zero
                 tc::fence_before();
-                pf_arrive(bar(SM::kPFull + sid));
+                pf_arrive(bar(SM::kPFull + buf));
 #pragma unroll
                 for (int i = 0; i < H; i += 2) {
                     if (i >= rows) break;
@@ -507,7 +520,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at + r] = make_float2(-nms[r], sum);
             }
             const int last = g.n0 + seg.nt - 1;
-            if (!pf_wait(bar(SM::kODone + (last & 1)), (uint32_t)(last >> 1) & 1u)) s_bad[half] = 1;  // seen at the next barrier
+            if (!pf_wait(bar(SM::kODone + last % NB), (uint32_t)(last / NB))) s_bad[half] = 1;  // seen at the next barrier
             tc::fence_after();
             if (rows > 0) {
                 float o[H];

@@ -110,6 +110,14 @@ struct PfSeg {
     const int32_t *table;
 };
 
+// Which of the two pages of a tile are there: bit 0, bit 1. The softmax threads look a tile ahead in the table themselves
+// (handed over through shared memory, the flags were 400 cycles late: behind the other warps' exponentials).
+__device__ __forceinline__ int pf_pages(const PfSeg &s, int t, int num_pages) {
+    const int p = 2 * (s.tile0 + t), n = t < s.nt ? (s.len + kChunk - 1) / kChunk : 0;
+    const int i0 = p < n ? s.table[p] : -1, i1 = p + 1 < n ? s.table[p + 1] : -1;
+    return (i0 >= 0 && i0 < num_pages ? 1 : 0) | (i1 >= 0 && i1 < num_pages ? 2 : 0);
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     uint64_t r;

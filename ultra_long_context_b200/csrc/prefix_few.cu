@@ -35,7 +35,6 @@ namespace hsa {
 constexpr int kFwSWarp = 8, kFwOWarp = 9, kFwTmaWarp = 10, kFwQWarp = 11;
 constexpr int kFwThreads = 32 * (kFwQWarp + 1);
 constexpr float kFwGrow = 64.0f, kFwSumMax = 0x1p69f;  // a sum of 32 terms of at most 2^64
-constexpr int kFwFlags = 8;   // tiles whose page flags are kept (copies run at most KS tiles ahead of S^T)
 
 template <int D, int NR>  // NR: rows per segment at most
 struct FwSmem {
@@ -47,7 +46,7 @@ struct FwSmem {
     // S^T and P^T buffers. A tile goes through its products and its softmax in some 2500 cycles; its bytes take half
     // as long with D = 64, so four tiles are on their way there, two with D = 128.
     static constexpr int NB = D == 64 ? 4 : 2;
-    static_assert(KS + NB <= kFwFlags && VS >= NB, "page flags, V waits");
+    static_assert(VS >= NB, "the softmax's waits for V");
     static constexpr uint32_t K = 0, V = K + KS * OP, P = V + VS * OP, Q = P + NB * PB;
     static constexpr uint32_t BAR = Q + 2 * QB;
     static constexpr int kKFull = 0, kKEmpty = KS, kVFull = 2 * KS, kVEmpty = 2 * KS + VS, kQFull = 2 * KS + 2 * VS,
@@ -59,8 +58,7 @@ struct FwSmem {
     static constexpr uint32_t LIM = MS + NR * 4;                          // int[NR]: keys that the row sees
     static constexpr uint32_t RED = LIM + NR * 4;                         // float[4][NR]: of a row and a warp's keys (maxima, sums)
     static constexpr uint32_t FAC = RED + 4 * NR * 4;                     // float[NR]: rescaling
-    static constexpr uint32_t FLAG = FAC + NR * 4;                        // int[kFwFlags]
-    static constexpr uint32_t MISC = FLAG + 4 * kFwFlags;                 // TMEM base, bad[2], -
+    static constexpr uint32_t MISC = FAC + NR * 4;                        // TMEM base, bad[2], -
     static constexpr uint32_t PLAN = (MISC + 16 + 15) / 16 * 16;
     static constexpr uint32_t BCUM = PLAN + (sizeof(PfPlan) + 15) / 16 * 16;  // int[blocks + 1]
     static constexpr size_t dyn(int blocks) { return BCUM + 4 * ((size_t)blocks + 1) + 1024; }  // slack: 1 KB alignment
@@ -115,7 +113,6 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     const uint32_t sb = (raw + 1023u) & ~1023u;  // 1 KB aligned (swizzle atoms)
     unsigned char *s = smem_raw + (sb - raw);
     PfNote *s_ring = reinterpret_cast<PfNote *>(s + SM::RING);
-    int *s_flag = reinterpret_cast<int *>(s + SM::FLAG);
     volatile int *s_bad = reinterpret_cast<volatile int *>(s + SM::MISC) + 1;  // [2] per warpgroup, [1] any other warp's, too
     PfPlan *s_plan = reinterpret_cast<PfPlan *>(s + SM::PLAN);
     int32_t *s_bcum = reinterpret_cast<int32_t *>(s + SM::BCUM);
@@ -143,7 +140,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             tc::mbar_init(bar(SM::kOEmpty + i), 8);
         }
         for (int i = 0; i < NB; ++i) {
-            tc::mbar_init(bar(SM::kSFull + i), 2);  // the product, and the warp that issued it (page flags)
+            tc::mbar_init(bar(SM::kSFull + i), 1);
             tc::mbar_init(bar(SM::kPFull + i), 8);  // a softmax warp each
             tc::mbar_init(bar(SM::kODone + i), 1);
         }
@@ -216,7 +213,6 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     ok = pf_wait_lane(bar(SM::kKEmpty + ks), ((uint32_t)(n / KS) & 1u) ^ 1u);
                     if (ok) {
                         const uint32_t dst = sb + SM::K + ks * SM::OP;
-                        s_flag[n % kFwFlags] = (g0 ? 1 : 0) | (g1 ? 2 : 0);
                         tc::mbar_arrive_expect_tx(bar(SM::kKFull + ks), SM::OP);
 #pragma unroll
                         for (int h = 0; h < SM::KH; ++h) {
@@ -286,7 +282,6 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 if (!ok) break;
                 tc::fence_after();
                 if (t == 0) tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
-                if (lane == 0) tc::mbar_arrive(bar(SM::kSFull + buf));  // hands on the page flags that came with K
                 const uint64_t dk = tc::desc_kmajor(sb + SM::K + ks * SM::OP);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)  // (a descriptor's low bits are its address / 16)
@@ -369,15 +364,17 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     off[i] = v.x, off[i + 1] = v.y, off[i + 2] = v.z, off[i + 3] = v.w;
                 }
             };
+            int flags = 0, flags_next = pf_pages(seg, 0, a.num_pages);
             for (int t = 0; t < seg.nt; ++t) {
+                flags = flags_next;
+                flags_next = pf_pages(seg, t + 1, a.num_pages);
                 const int n = g.n0 + t, buf = n % NB, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
                 const uint32_t tS = tmem + lane_off + SM::S_COL + buf * 64 + row0;
                 unsigned char *s_p = s + SM::P + buf * SM::PB;
-                // S^T is there, with its tile's page flags, and P^T's buffer has been read (so every V filling before this
+                // S^T is there, and P^T's buffer has been read (so every V filling before this
                 // tile's in its slot is over, too, which makes the wait for it by its parity exact)
                 const bool good = pf_wait(bar(SM::kSFull + buf), (uint32_t)(n / NB));
                 tc::fence_after();
-                const int flags = s_flag[n % kFwFlags];
                 const bool edge = flags != 3 || base + kPfTile > min_lim;
                 if (!good) s_bad[half] = 1;
                 const bool page_ok = (flags >> (r >> 6)) & 1;
@@ -487,11 +484,14 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 tc::fence_before();
                 pf_arrive(bar(SM::kPFull + buf));
 #pragma unroll
-                for (int i = 0; i < H; i += 2) {
-                    if (i >= rows) break;
-                    const float2 sum = add2({l[i], l[i + 1]}, {p[i], p[i + 1]});
-                    l[i] = sum.x;
-                    l[i + 1] = sum.y;
+                for (int c = 0; c < H; c += 8) {
+                    if (c >= rows) break;
+#pragma unroll
+                    for (int i = c; i < c + 8; i += 2) {
+                        const float2 sum = add2({l[i], l[i + 1]}, {p[i], p[i + 1]});
+                        l[i] = sum.x;
+                        l[i + 1] = sum.y;
+                    }
                 }
             }
             if (!ok) break;

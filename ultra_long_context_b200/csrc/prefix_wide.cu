@@ -24,7 +24,6 @@ namespace hsa {
 constexpr int kPfStreamWarps = 8;
 constexpr int kPfMmaWarp = 2 * kPfStreamWarps, kPfTmaWarp = kPfMmaWarp + 1, kPfQWarp = kPfMmaWarp + 2, kPfQWarps = 2;
 constexpr int kPfThreads = 32 * (kPfQWarp + kPfQWarps);
-constexpr int kPfFlags = 8;               // tiles whose page flags are kept
 constexpr float kPfGrow = 64.0f, kPfSumMax = 0x1p70f;  // a sum of 64 terms of at most 2^64
 
 template <int D>
@@ -32,7 +31,6 @@ struct PfSmem {
     static constexpr int KH = D / 64;                       // 128-byte column blocks of D
     static constexpr uint32_t OP = KH * 16384;              // one operand tile [128][D]
     static constexpr int KS = D == 128 ? 2 : 4, VS = D == 128 ? 2 : 4;
-    static_assert(KS + 2 <= kPfFlags, "page flags");
     static constexpr uint32_t Q = 0, K = 2 * OP, V = K + KS * OP;
     static constexpr uint32_t BAR = V + VS * OP;
     // mbarriers
@@ -42,8 +40,7 @@ struct PfSmem {
                          NBAR = kSegEmpty + kPfRing;
     static constexpr uint32_t RING = (BAR + 8 * NBAR + 15) / 16 * 16;  // PfNote[kPfRing]
     static constexpr uint32_t ROW = RING + kPfRing * sizeof(PfNote);   // float[2 streams][2 halves][128]: exchanged by a row's threads
-    static constexpr uint32_t FLAG = ROW + 2 * 2 * 128 * 4;  // int[kPfFlags]: which of a tile's two pages are good
-    static constexpr uint32_t BADP = FLAG + 4 * kPfFlags;    // int[8]: a wait of the pair of warps ran out
+    static constexpr uint32_t BADP = ROW + 2 * 2 * 128 * 4;  // int[8]: a wait of the pair of warps ran out
     static constexpr uint32_t TMEM = BADP + 32;
     static constexpr uint32_t BAD = TMEM + 4;
     static constexpr uint32_t PLAN = (BAD + 4 + 15) / 16 * 16;
@@ -82,7 +79,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     const uint32_t sb = (raw + 1023u) & ~1023u;  // 1 KB aligned (swizzle atoms)
     unsigned char *s = smem_raw + (sb - raw);
     PfNote *s_ring = reinterpret_cast<PfNote *>(s + SM::RING);
-    int *s_flag = reinterpret_cast<int *>(s + SM::FLAG);
     volatile int *s_badp = reinterpret_cast<volatile int *>(s + SM::BADP), *s_bad = reinterpret_cast<volatile int *>(s + SM::BAD);
     PfPlan *s_plan = reinterpret_cast<PfPlan *>(s + SM::PLAN);
     int32_t *s_bcum = reinterpret_cast<int32_t *>(s + SM::BCUM);
@@ -108,7 +104,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(SM::kQFull + i), 32 * kPfQWarps);
             tc::mbar_init(bar(SM::kQEmpty + i), 1);
-            tc::mbar_init(bar(SM::kSFull + i), 2);  // the product, and the warp that issued it (page flags)
+            tc::mbar_init(bar(SM::kSFull + i), 1);
             tc::mbar_init(bar(SM::kPFull + i), kPfStreamWarps);
             tc::mbar_init(bar(SM::kODone + i), 1);
             tc::mbar_init(bar(SM::kOEmpty + i), kPfStreamWarps);
@@ -184,7 +180,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                     ok = pf_wait_lane(bar(SM::kKEmpty + ks), ((uint32_t)(n / KS) & 1u) ^ 1u);
                     if (ok) {
                         const uint32_t dst = sb + SM::K + ks * SM::OP;
-                        s_flag[n % kPfFlags] = (g0 ? 1 : 0) | (g1 ? 2 : 0);
                         tc::mbar_arrive_expect_tx(bar(SM::kKFull + ks), SM::OP);
 #pragma unroll
                         for (int h = 0; h < SM::KH; ++h) {
@@ -264,7 +259,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             const bool starts = both ? u < 2 : u == 0;  // the first to read its Q buffer
             if (!both || !(u & 1)) ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS));  // (once for a tile)
             if (ok && starts) ok = pf_wait(bar(SM::kQFull + q), q ? uses1 : uses0);
-            if (ok && lane == 0) tc::mbar_arrive(bar(SM::kSFull + sid));  // hands on the page flags that came with K
             // S and P share columns: P of the stream's item before must have been read
             if (ok && issued[sid] > 0) ok = pf_wait(bar(SM::kODone + sid), (issued[sid] - 1) & 1u);
             if (!ok) return;
@@ -365,13 +359,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             const bool active = rr - lane < seg.nr;  // do this pair's warps hold any row?
             const int lim = mine ? pf_limit(a, seg, d, rr) : INT32_MAX;
             float ms = 0.0f, l = 0.0f;
+            int flags = 0, flags_next = pf_pages(seg, t0, a.num_pages);
             for (int t = t0; t < seg.nt; t += dt, ++tiles) {
+                flags = flags_next;
+                flags_next = pf_pages(seg, t + dt, a.num_pages);
                 const int n = g.n0 + t, vs = n % VS;
                 const int base = (seg.tile0 + t) * kPfTile;
-                bool good = pf_wait(bar(SM::kSFull + sid), tiles);
-                const int flags = s_flag[n % kPfFlags];
                 const int vis = (flags >> half) & 1 ? lim - base - 64 * half : 0;  // keys of this half that the row sees
                 const bool edge = __any_sync(0xffffffffu, vis < 64);
+                bool good = pf_wait(bar(SM::kSFull + sid), tiles);
                 tc::fence_after();
                 if (!good) s_badp[pid - 1] = 1;
                 if (active) {

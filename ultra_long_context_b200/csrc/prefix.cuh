@@ -110,12 +110,16 @@ struct PfSeg {
     const int32_t *table;
 };
 
-// Which of the two pages of a tile are there: bit 0, bit 1. The softmax threads look a tile ahead in the table themselves
-// (handed over through shared memory, the flags were 400 cycles late: behind the other warps' exponentials).
+// Is page `half` of the segment's tile t there? The softmax threads look a tile ahead in the table themselves (handed over
+// through shared memory, the answer was 400 cycles late: behind the other warps' exponentials).
+__device__ __forceinline__ bool pf_page(const PfSeg &s, int t, int half, int num_pages) {
+    const int p = 2 * (s.tile0 + t) + half;
+    const int id = t < s.nt && p < (s.len + kChunk - 1) / kChunk ? s.table[p] : -1;
+    return id >= 0 && id < num_pages;
+}
+// Both pages: bit 0, bit 1.
 __device__ __forceinline__ int pf_pages(const PfSeg &s, int t, int num_pages) {
-    const int p = 2 * (s.tile0 + t), n = t < s.nt ? (s.len + kChunk - 1) / kChunk : 0;
-    const int i0 = p < n ? s.table[p] : -1, i1 = p + 1 < n ? s.table[p + 1] : -1;
-    return (i0 >= 0 && i0 < num_pages ? 1 : 0) | (i1 >= 0 && i1 < num_pages ? 2 : 0);
+    return (pf_page(s, t, 0, num_pages) ? 1 : 0) | (pf_page(s, t, 1, num_pages) ? 2 : 0);
 }
 
 // Two fp32 operations in one instruction.

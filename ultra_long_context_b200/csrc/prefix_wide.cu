@@ -359,13 +359,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             const bool active = rr - lane < seg.nr;  // do this pair's warps hold any row?
             const int lim = mine ? pf_limit(a, seg, d, rr) : INT32_MAX;
             float ms = 0.0f, l = 0.0f;
-            int flags = 0, flags_next = pf_pages(seg, t0, a.num_pages);
+            // the half that holds the first key at hand, whose logit becomes the reference
+            const bool lead = half == (pf_pages(seg, t0, a.num_pages) & 1 ? 0 : 1);
+            bool there_next = pf_page(seg, t0, half, a.num_pages);
             for (int t = t0; t < seg.nt; t += dt, ++tiles) {
-                flags = flags_next;
-                flags_next = pf_pages(seg, t + dt, a.num_pages);
+                const bool there = there_next;
+                there_next = pf_page(seg, t + dt, half, a.num_pages);
                 const int n = g.n0 + t, vs = n % VS;
                 const int base = (seg.tile0 + t) * kPfTile;
-                const int vis = (flags >> half) & 1 ? lim - base - 64 * half : 0;  // keys of this half that the row sees
+                const int vis = there ? lim - base - 64 * half : 0;  // keys of this half that the row sees
                 const bool edge = __any_sync(0xffffffffu, vis < 64);
                 bool good = pf_wait(bar(SM::kSFull + sid), tiles);
                 tc::fence_after();
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                     __syncwarp();
                     tc::tmem_ld32(tS + 64 * half, x);
                     if (t == t0) {  // the row's reference: its first key, or the second page's where the first is bad
-                        if (half == (flags & 1 ? 0 : 1)) s_row[0] = vis > 0 ? x[0] * sl2 : -INFINITY;
+                        if (lead) s_row[0] = vis > 0 ? x[0] * sl2 : -INFINITY;
                         pf_pair_bar(pid);
                         ms = s_row[0];
                     }

@@ -127,7 +127,7 @@ def _pre(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(D=96), -2), (dict(page=128), -2), (dict(B=0), -1), (dict(B=8193), -2), (dict(H=7), -1), (dict(Hkv=0), -1),
     (dict(Tq=0), -1), (dict(Tq=65), -1), (dict(H=256, Hkv=1, Tq=5), -2), (dict(mpp=-1), -1), (dict(mp=-1), -1),
-    (dict(mpp=1 << 25), -2), (dict(num_pages=0), -1), (dict(num_pages=1 << 25), -2), (dict(q=None), -1), (dict(Kp=None), -1),
+    (dict(mpp=1 << 25), -2), (dict(mp=1 << 28), -2), (dict(B=64, mp=1 << 24), -2), (dict(num_pages=0), -1), (dict(num_pages=1 << 25), -2), (dict(q=None), -1), (dict(Kp=None), -1),
     (dict(Vp=None), -1), (dict(ptab=None), -1), (dict(plen=None), -1), (dict(tab=None), -1), (dict(own=None), -1),
     (dict(out=None), -1), (dict(q=ODD4), -1), (dict(Kp=ODD4), -1), (dict(out=ODD4), -1), (dict(lse=ODD2), -1), (dict(own=ODD4), -1),
     (dict(ptab=ODD2), -1), (dict(ws=None), -3), (dict(ws_bytes=8), -3), (dict(ws=ODD4), -3), (dict(B=8192, H=2048, Hkv=2048, mp=1), -2),

@@ -661,6 +661,8 @@ hsa_status hsa_prefix_decode(const hsa_bf16 *q, const hsa_bf16 *Kp, const hsa_bf
     if (max_prefix_pages >= (1 << 24) || max_pages >= (1 << 24))
         return fail(HSA_ERR_UNSUPPORTED, "tables must stay below 2^24 pages (2^30 tokens)");
     if ((double)B * H * Tq * D >= 2147483647.0) return fail(HSA_ERR_UNSUPPORTED, "B*H*Tq*D must stay below 2^31");
+    if ((double)B * max_pages >= 1073741824.0)
+        return fail(HSA_ERR_UNSUPPORTED, "B * max_pages must stay below 2^30 (the weights of the work are summed in 32 bits)");
     if (!q || !Kp || !Vp || !own_len || !out || (max_prefix_pages > 0 && (!prefix_table || !prefix_len)) ||
         (max_pages > 0 && !block_table))
         return fail(HSA_ERR_INVALID_ARG, "q, Kp, Vp, the lengths, their tables and out must not be NULL");

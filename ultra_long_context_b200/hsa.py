@@ -457,11 +457,11 @@ def hsa_page_plan(cache_len, new_len, block_table, free_pages, pool, max_tokens,
     if pool_out is not pool:
         _fits(pool_out, "pool_out", _I64T, (3,), dev)
     if cu_new is None:
-        cu_new = torch.empty(B + 1, dtype=_I32, device=dev)
+        cu_new = new_len.new_empty(B + 1)
     else:
         _fits(cu_new, "cu_new", _I32, (B + 1,), dev)
     if slots is None:
-        slots = torch.empty(max_tokens, dtype=_I64T, device=dev)
+        slots = cache_len.new_empty(max_tokens)
     else:
         _fits(slots, "slots", _I64T, (max_tokens,), dev)
     if total_len is None:

@@ -49,15 +49,15 @@ struct PfDims {
     int Rp, gp, Rgp;       // prefix rows per key head, in Rgp groups of gp
     int Ro, Rgo;           // own rows per request and key head, in groups of kPfFewRows
     int strideP, strideO;  // rows of one segment's partials (in the wide kernel, two streams may each keep one of the same rows)
-    int prefix_tile;       // cost of a prefix tile in half tiles: those of 64 rows and D = 64 take twice the time of their bytes
     int max_items, max_slots, blocks;  // blocks: of 32 requests
-    // Which kernel ends the prefix sooner? A tile of 128 keys takes the few-rows kernel 1.15 us (D = 128; half that with
-    // D = 64: its bytes) for 64 rows, the wide one 2.3 us for 256, and that is a launch of its own, 12 us before the
-    // first product ends. Both are measured; the tiles are those of the table, since the length is not known here.
+    // Which kernel ends the prefix sooner? A tile of 128 keys takes the few-rows kernel 1.35 us (D = 128; 1.07 with D = 64)
+    // for 64 rows, the wide one 2.3 us (2.1) for 256, and that is a launch of its own, worth 14 us. Both sides measured:
+    // 256 rows x 8 heads, D = 128, over 6144 / 9856 / 12160 tokens 39 / 48 / 56 us and 46 / 50 / 52, D = 64 over 70912
+    // 164 and 92. The tiles are those of the table, since the length is not known here.
     static bool pf_wide(int Rp, int Hkv, int D, int tiles) {
         const double per_sm = (double)Hkv * tiles / kPfCtas;
-        const double few = per_sm * ((Rp + kPfFewRows - 1) / kPfFewRows) * (D == 128 ? 1.15 : 0.6);
-        const double wide = 12.0 + per_sm * ((Rp + kPfWideRows - 1) / kPfWideRows) * 2.3;
+        const double few = per_sm * ((Rp + kPfFewRows - 1) / kPfFewRows) * (D == 128 ? 1.35 : 1.07);
+        const double wide = 14.0 + per_sm * ((Rp + kPfWideRows - 1) / kPfWideRows) * (D == 128 ? 2.3 : 2.1);
         return Rp > kPfFewRows && wide < few;
     }
     PfDims(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages) {
@@ -70,7 +70,6 @@ struct PfDims {
         Rgo = (Ro + kPfFewRows - 1) / kPfFewRows;
         strideP = wide ? kPfWideRows : Rp < kPfFewRows ? Rp : kPfFewRows;
         strideO = Ro < kPfFewRows ? Ro : kPfFewRows;
-        prefix_tile = kPfTileCost;
         const int units = Hkv * Rgp;
         int ns = kPfItems / units;
         ns = ns < 1 ? 1 : ns;
@@ -110,17 +109,19 @@ struct PfSeg {
     const int32_t *table;
 };
 
-// Is page `half` of the segment's tile t there? The softmax threads look a tile ahead in the table themselves (handed over
-// through shared memory, the answer was 400 cycles late: behind the other warps' exponentials).
-__device__ __forceinline__ bool pf_page(const PfSeg &s, int t, int half, int num_pages) {
-    const int p = 2 * (s.tile0 + t) + half;
-    const int id = t < s.nt && p < (s.len + kChunk - 1) / kChunk ? s.table[p] : -1;
-    return id >= 0 && id < num_pages;
-}
-// Both pages: bit 0, bit 1.
-__device__ __forceinline__ int pf_pages(const PfSeg &s, int t, int num_pages) {
-    return (pf_page(s, t, 0, num_pages) ? 1 : 0) | (pf_page(s, t, 1, num_pages) ? 2 : 0);
-}
+// Which of the 32 pages of a segment's tiles t .. t + 15 are there? A warp's lanes look one up each and vote; fetch() of the
+// next 16 tiles comes that much earlier. (Handed over by the copying warp, through shared memory, the answer was 400 cycles
+// late, behind the other warps' exponentials; so were lookups for every tile by every thread.)
+struct PfPages {
+    const int32_t *table;
+    int end, num_pages;  // the first page that is not the segment's
+    __device__ PfPages(const PfSeg &s, int pages) : table(s.table), end(min((s.len + kChunk - 1) / kChunk, 2 * (s.tile0 + s.nt))), num_pages(pages) {}
+    __device__ int fetch(int tile) const {  // (in the sequence)
+        const int p = 2 * tile + (threadIdx.x & 31);
+        return p < end ? table[p] : -1;
+    }
+    __device__ uint32_t there(int id) const { return __ballot_sync(0xffffffffu, id >= 0 && id < num_pages); }
+};
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -296,7 +297,7 @@ __device__ void pf_schedule(const PrefixArgs &a, const PfDims &d, bool prefix, b
             const int ns_max = min(max(kPfItems / units, 1), tiles);
             const float quarter = (float)ctas * 0.25f / (float)units;
             const int ns = min(max(lane < 16 ? lane + 1 : (int)((float)(lane - 15) * quarter), 1), ns_max);
-            const float run = ceilf(__fdividef((float)tiles, (float)ns) - 1e-3f), cost = d.prefix_tile * run + kPfPrefixCost;
+            const float run = ceilf(__fdividef((float)tiles, (float)ns) - 1e-3f), cost = kPfTileCost * run + kPfPrefixCost;
             const float items = (float)units * ceilf(__fdividef((float)tiles, run) - 1e-3f);
             const float waves = ceilf(__fdividef(items, (float)ctas) - 1e-3f) * cost;
             const float even = __fdividef(items * cost + (float)axis, (float)ctas);
@@ -307,7 +308,7 @@ __device__ void pf_schedule(const PrefixArgs &a, const PfDims &d, bool prefix, b
             p.nsplit = (tiles + p.run - 1) / p.run;
             p.items = units * p.nsplit;
         }
-        const int64_t cost = d.prefix_tile * p.run + kPfPrefixCost;
+        const int64_t cost = kPfTileCost * p.run + kPfPrefixCost;
         const int waves = p.items / ctas;
         p.lo_ctas = p.items - waves * ctas;
         const int64_t pc_hi = waves * cost, pc_lo = pc_hi + cost;

@@ -364,10 +364,15 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     off[i] = v.x, off[i + 1] = v.y, off[i + 2] = v.z, off[i + 3] = v.w;
                 }
             };
-            int flags = 0, flags_next = pf_pages(seg, 0, a.num_pages);
+            const PfPages pages(seg, a.num_pages);
+            int id_next = pages.fetch(seg.tile0);
+            uint32_t there = 0;
             for (int t = 0; t < seg.nt; ++t) {
-                flags = flags_next;
-                flags_next = pf_pages(seg, t + 1, a.num_pages);
+                if (t % 16 == 0) {
+                    there = pages.there(id_next);
+                    id_next = pages.fetch(seg.tile0 + t + 16);
+                }
+                const uint32_t flags = there >> 2 * (t & 15) & 3u;  // of this tile's two pages
                 const int n = g.n0 + t, buf = n % NB, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
                 const uint32_t tS = tmem + lane_off + SM::S_COL + buf * 64 + row0;
                 unsigned char *s_p = s + SM::P + buf * SM::PB;
@@ -375,9 +380,9 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 // tile's in its slot is over, too, which makes the wait for it by its parity exact)
                 const bool good = pf_wait(bar(SM::kSFull + buf), (uint32_t)(n / NB));
                 tc::fence_after();
-                const bool edge = flags != 3 || base + kPfTile > min_lim;
+                const bool edge = flags != 3u || base + kPfTile > min_lim;
                 if (!good) s_bad[half] = 1;
-                const bool page_ok = (flags >> (r >> 6)) & 1;
+                const bool page_ok = flags >> (r >> 6) & 1u;
                 float p[H];
                 // P^T of this key to shared memory, kept in p for the row sums; false if a term leaves the range
                 auto probs = [&](auto with_edge) {
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     return sum.x + sum.y <= kFwSumMax;  // (not of an infinity or NaN)
                 };
                 if (t == 0) {  // the references: the first key, or the 65th where the first page is bad
-                    const int lead = flags & 1 ? 0 : 64;
+                    const int lead = flags & 1u ? 0 : 64;
                     if (r >> 5 == lead >> 5 && good && rows > 0) {
                         fw_ld<H>(tS, p);
                         if (lane == 0) {

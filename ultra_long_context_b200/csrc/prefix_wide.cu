@@ -360,11 +360,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             const int lim = mine ? pf_limit(a, seg, d, rr) : INT32_MAX;
             float ms = 0.0f, l = 0.0f;
             // the half that holds the first key at hand, whose logit becomes the reference
-            const bool lead = half == (pf_pages(seg, t0, a.num_pages) & 1 ? 0 : 1);
-            bool there_next = pf_page(seg, t0, half, a.num_pages);
+            const PfPages pages(seg, a.num_pages);
+            uint32_t there_all = pages.there(pages.fetch(seg.tile0));
+            int id_next = pages.fetch(seg.tile0 + 16);
+            const bool lead = half == (there_all >> 2 * t0 & 1u ? 0 : 1);
             for (int t = t0; t < seg.nt; t += dt, ++tiles) {
-                const bool there = there_next;
-                there_next = pf_page(seg, t + dt, half, a.num_pages);
+                if ((t & 15) < dt && t >= 16) {
+                    there_all = pages.there(id_next);
+                    id_next = pages.fetch(seg.tile0 + (t & ~15) + 16);
+                }
+                const bool there = there_all >> (2 * (t & 15) + half) & 1u;
                 const int n = g.n0 + t, vs = n % VS;
                 const int base = (seg.tile0 + t) * kPfTile;
                 const int vis = there ? lim - base - 64 * half : 0;  // keys of this half that the row sees

@@ -246,10 +246,10 @@ struct PfQRows {
 // is never read (no limit, so that they do not slow the others' tiles).
 __device__ __forceinline__ int pf_limit(const PrefixArgs &a, const PfSeg &s, const PfDims &d, int rr) {
     const int r = s.r0 + rr;
-    const int64_t own = pf_clamp_len(a.own_len[s.b < 0 ? r / d.Ro : s.b], a.max_pages);
+    if (s.b >= 0) return max(0, s.len - a.Tq + (a.Tq == 1 ? 0 : r % a.Tq) + 1);
+    const int64_t own = pf_clamp_len(a.own_len[r / d.Ro], a.max_pages);
     if (own < 0) return INT32_MAX;
-    const int last = (int)own - a.Tq + r % d.Ro % a.Tq + 1;  // own tokens seen; below 0: prefix tokens not seen
-    return max(0, s.b < 0 ? s.len + min(last, 0) : last);
+    return max(0, s.len + min((int)own - a.Tq + (a.Tq == 1 ? 0 : r % d.Ro % a.Tq) + 1, 0));  // prefix tokens not seen
 }
 // A bound from below for all rows of the segment.
 __device__ __forceinline__ int pf_min_limit(const PrefixArgs &a, const PfSeg &s) { return max(0, s.len - a.Tq + 1); }

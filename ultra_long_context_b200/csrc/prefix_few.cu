@@ -176,10 +176,10 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         PfWalk walk(a, *s_plan, s_bcum, d);
         const int pages_all = a.num_pages;
         int n = 0;
-        bool more = true;
-        while (ok && more) {
-            PfNote g;
-            more = walk.next(g.s);
+        PfNote g;
+        bool more = walk.next(g.s);
+        int ids_first = 0;
+        while (ok) {
             if (!more) g.s.nr = 0;
             g.n0 = n;
             const int slot = seg_no % kPfRing;
@@ -191,17 +191,13 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             }
             ++seg_no;
             if (!more) break;
-            const PfSeg &seg = g.s;
-            const int last_page = min((seg.len + kChunk - 1) / kChunk, 2 * (seg.tile0 + seg.nt));
-            auto fetch = [&](int from) {  // this lane's page id of the batch that starts at page `from`
-                const int i = from + lane;
-                return i < last_page ? seg.table[i] : -1;
-            };
-            int ids = fetch(2 * seg.tile0), ids_next = 0;
+            const PfSeg seg = g.s;
+            const PfPages pages(seg, pages_all);
+            int ids = n == 0 ? pages.fetch(seg.tile0) : ids_first, ids_next = 0;
             for (int t = 0; t < seg.nt; ++t, ++n) {
                 if (t % 16 == 0) {
                     if (t > 0) ids = ids_next;
-                    ids_next = fetch(2 * (seg.tile0 + t) + 32);
+                    ids_next = pages.fetch(seg.tile0 + t + 16);
                 }
                 const int p0 = __shfl_sync(0xffffffffu, ids, 2 * (t & 15)), p1 = __shfl_sync(0xffffffffu, ids, 2 * (t & 15) + 1);
                 if (lane == 0) {
@@ -234,6 +230,10 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 }
                 ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
                 if (!ok) break;
+                if (t == min(seg.nt - 1, 1)) {  // the next segment and its first pages, while this one's copies run
+                    more = walk.next(g.s);
+                    if (more) ids_first = PfPages(g.s, pages_all).fetch(g.s.tile0);
+                }
             }
         }
         // every copy has landed before the CTA may exit, however the walk ended
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             PfQRows at(g.s, d, a.Hkv, rsub);
             for (int r = rsub; r < (g.s.nr + 15) / 16 * 16; r += RPW, at.advance(RPW)) {
                 // (zeros, too, for the empty rows of a padded batch: whatever stands there must not look like a large logit)
-                const bool in = r < g.s.nr && a.own_len[at.request] >= 0;
+                const bool in = r < g.s.nr && (g.s.b >= 0 || a.own_len[at.request] >= 0);
                 cp_async16_u32(dst + (ch >> 3) * (NR * 128) + tc::sw128(r, ch & 7),
                                in ? a.q + (int64_t)at.row * D + ch * 8 : a.q, in ? 16 : 0);
             }
@@ -327,13 +327,13 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         }
         __syncwarp();
     } else {
-        // ================= softmax of rows row0 .. row0 + H - 1; thread = key, then thread = dim =================
+        // ================= softmax of half of the rows; thread = key, then thread = dim =================
         constexpr int H = NR / 2;
-        const int half = warp >> 2, r = tid & 127, wq = warp & 3, bid = 1 + half, row0 = half * H;
+        const int half = warp >> 2, r = tid & 127, wq = warp & 3, bid = 1 + half;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-        float *nms = reinterpret_cast<float *>(s + SM::MS) + row0, *s_fac = reinterpret_cast<float *>(s + SM::FAC) + row0;
+        float *nms = reinterpret_cast<float *>(s + SM::MS) + half * H, *s_fac = reinterpret_cast<float *>(s + SM::FAC) + half * H;
         float *s_red = reinterpret_cast<float *>(s + SM::RED) + half * 4 * H;
-        int *lims = reinterpret_cast<int *>(s + SM::LIM) + row0;
+        int *lims = reinterpret_cast<int *>(s + SM::LIM) + half * H;
         const float sl2 = a.scale * 1.4426950408889634f;
         PfNote g;
         // A warp whose wait ran out says so and still comes to the barriers, and the warpgroup leaves together
@@ -347,8 +347,10 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             }
             if (g.s.nr == 0) break;
             const PfSeg &seg = g.s;
+            // this warpgroup's rows, by eights (none: it keeps step)
+            const int split = (seg.nr + 15) / 16 * 8, row0 = half ? split : 0, rows = half ? seg.nr - split : min(seg.nr, split);
             const uint32_t tO = tmem + lane_off + SM::O_COL + ob * 64 + row0;
-            const int min_lim = pf_min_limit(a, seg), rows = min(seg.nr - row0, H);  // this warpgroup's (none: it keeps step)
+            const int min_lim = pf_min_limit(a, seg);
             if (r < H) {  // rows that are nobody's: -1 (they see nothing, where it is asked: in tiles with an edge)
                 const int lim = r < rows ? pf_limit(a, seg, d, row0 + r) : -1;
                 lims[r] = lim == INT32_MAX ? -1 : lim;
@@ -364,77 +366,118 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     off[i] = v.x, off[i + 1] = v.y, off[i + 2] = v.z, off[i + 3] = v.w;
                 }
             };
+            float p[H];
+            // P^T of tile t's key to shared memory, kept in p for the row sums; false if a term leaves the range
+            auto probs = [&](int t, uint32_t tS, auto with_edge, uint32_t flags) {
+                const int buf = (g.n0 + t) % NB;
+                unsigned char *s_p = s + SM::P + buf * SM::PB;
+                float2 sum = {0.0f, 0.0f};
+                fw_ld<H>(tS, p);
+#pragma unroll
+                for (int c = 0; c < H / 8; ++c) {
+                    if (8 * c >= rows) break;
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const int e = 8 * c + i;
+                        float2 a0 = fma2({p[e], p[e + 1]}, {sl2, sl2}, {off[e], off[e + 1]});
+                        float2 a1 = fma2({p[e + 2], p[e + 3]}, {sl2, sl2}, {off[e + 2], off[e + 3]});
+                        a0 = {ex2_approx(a0.x), ex2_approx(a0.y)};
+                        a1 = {ex2_approx(a1.x), ex2_approx(a1.y)};
+                        if constexpr (decltype(with_edge)::value) {
+                            const int key = (seg.tile0 + t) * kPfTile + r;
+                            const bool page_ok = flags >> (r >> 6) & 1u;
+                            const int4 lim = *reinterpret_cast<const int4 *>(lims + e);
+                            a0 = {page_ok && key < lim.x ? a0.x : 0.0f, page_ok && key < lim.y ? a0.y : 0.0f};
+                            a1 = {page_ok && key < lim.z ? a1.x : 0.0f, page_ok && key < lim.w ? a1.y : 0.0f};
+                        }
+                        sum = add2(sum, add2(a0, a1));
+                        p[e] = a0.x;
+                        p[e + 1] = a0.y;
+                        p[e + 2] = a1.x;
+                        p[e + 3] = a1.y;
+                        pk[i / 2] = pack_bf16x2(a0.x, a0.y);
+                        pk[i / 2 + 1] = pack_bf16x2(a1.x, a1.y);
+                    }
+                    *reinterpret_cast<uint4 *>(s_p + tc::sw128(r, row0 / 8 + c)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+                return sum.x + sum.y <= kFwSumMax;  // (not of an infinity or NaN)
+            };
+            auto deliver = [&](int buf) {  // P^T (and V rows made zero) to the products; p to the row sums
+                tc::fence_proxy_async_smem();
+                tc::fence_before();
+                pf_arrive(bar(SM::kPFull + buf));
+#pragma unroll
+                for (int c = 0; c < H; c += 8) {
+                    if (c >= rows) break;
+#pragma unroll
+                    for (int i = c; i < c + 8; i += 2) {
+                        const float2 sum = add2({l[i], l[i + 1]}, {p[i], p[i + 1]});
+                        l[i] = sum.x;
+                        l[i + 1] = sum.y;
+                    }
+                }
+            };
             const PfPages pages(seg, a.num_pages);
-            int id_next = pages.fetch(seg.tile0);
+            int id_next = pages.fetch(seg.tile0), block_end = 0;  // of the 16 tiles whose pages `there` tells of
             uint32_t there = 0;
-            for (int t = 0; t < seg.nt; ++t) {
-                if (t % 16 == 0) {
+            const int whole = min_lim / kPfTile - seg.tile0;  // the tiles before this one lie before every row's end
+            bool redo = false;
+            for (int t = 0; t < seg.nt;) {
+                if (t == block_end) {
                     there = pages.there(id_next);
                     id_next = pages.fetch(seg.tile0 + t + 16);
+                    block_end += 16;
                 }
+                // Tiles that every row sees all of, in a loop of their own: with the rare things in the same loop, what
+                // the compiler did to keep the paths apart took 40% of a tile's time
+                const uint32_t gaps = ~(there & there >> 1) & 0x55555555u & ~0u << 2 * (t & 15);
+                const int stop = min(min(seg.nt, whole), gaps ? block_end - 16 + (__ffs(gaps) - 1) / 2 : block_end);
+                if (t > 0 && !redo) {
+                    for (; t < stop; ++t) {
+                        const int n = g.n0 + t, buf = n % NB;
+                        const uint32_t tS = tmem + lane_off + SM::S_COL + buf * 64 + row0;
+                        const bool good = pf_wait(bar(SM::kSFull + buf), (uint32_t)(n / NB));
+                        tc::fence_after();
+                        bool high = !good;
+                        if (rows > 0) high |= !probs(t, tS, std::false_type{}, 3u);
+                        redo = fw_bar_or(bid, high);
+                        if (redo) break;
+                        deliver(buf);
+                    }
+                    if (t >= seg.nt) break;
+                    if (t == block_end && !redo) continue;
+                }
+                redo = false;
+                // Any tile: the first, the ones with an edge, and those where a term left the range
                 const uint32_t flags = there >> 2 * (t & 15) & 3u;  // of this tile's two pages
                 const int n = g.n0 + t, buf = n % NB, vs = n % VS, base = (seg.tile0 + t) * kPfTile;
                 const uint32_t tS = tmem + lane_off + SM::S_COL + buf * 64 + row0;
-                unsigned char *s_p = s + SM::P + buf * SM::PB;
                 // S^T is there, and P^T's buffer has been read (so every V filling before this
                 // tile's in its slot is over, too, which makes the wait for it by its parity exact)
                 const bool good = pf_wait(bar(SM::kSFull + buf), (uint32_t)(n / NB));
                 tc::fence_after();
-                const bool edge = flags != 3u || base + kPfTile > min_lim;
                 if (!good) s_bad[half] = 1;
                 const bool page_ok = flags >> (r >> 6) & 1u;
-                float p[H];
-                // P^T of this key to shared memory, kept in p for the row sums; false if a term leaves the range
-                auto probs = [&](auto with_edge) {
-                    float2 sum = {0.0f, 0.0f};
-                    fw_ld<H>(tS, p);
-#pragma unroll
-                    for (int c = 0; c < H / 8; ++c) {
-                        if (8 * c >= rows) break;
-                        uint32_t pk[4];
-#pragma unroll
-                        for (int i = 0; i < 8; i += 4) {
-                            const int e = 8 * c + i;
-                            float2 a0 = fma2({p[e], p[e + 1]}, {sl2, sl2}, {off[e], off[e + 1]});
-                            float2 a1 = fma2({p[e + 2], p[e + 3]}, {sl2, sl2}, {off[e + 2], off[e + 3]});
-                            a0 = {ex2_approx(a0.x), ex2_approx(a0.y)};
-                            a1 = {ex2_approx(a1.x), ex2_approx(a1.y)};
-                            if constexpr (decltype(with_edge)::value) {
-                                const int key = base + r;
-                                const int4 lim = *reinterpret_cast<const int4 *>(lims + e);
-                                a0 = {page_ok && key < lim.x ? a0.x : 0.0f, page_ok && key < lim.y ? a0.y : 0.0f};
-                                a1 = {page_ok && key < lim.z ? a1.x : 0.0f, page_ok && key < lim.w ? a1.y : 0.0f};
-                            }
-                            sum = add2(sum, add2(a0, a1));
-                            p[e] = a0.x;
-                            p[e + 1] = a0.y;
-                            p[e + 2] = a1.x;
-                            p[e + 3] = a1.y;
-                            pk[i / 2] = pack_bf16x2(a0.x, a0.y);
-                            pk[i / 2 + 1] = pack_bf16x2(a1.x, a1.y);
-                        }
-                        *reinterpret_cast<uint4 *>(s_p + tc::sw128(r, row0 / 8 + c)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    }
-                    return sum.x + sum.y <= kFwSumMax;  // (not of an infinity or NaN)
-                };
                 if (t == 0) {  // the references: the first key, or the 65th where the first page is bad
                     const int lead = flags & 1u ? 0 : 64;
                     if (r >> 5 == lead >> 5 && good && rows > 0) {
                         fw_ld<H>(tS, p);
                         if (lane == 0) {
 #pragma unroll
-                            for (int i = 0; i < H; ++i) {
-                                const int lim = lims[i];
-                                nms[i] = lim < 0 ? 0.0f : page_ok && base + lead < lim ? -p[i] * sl2 : INFINITY;
-                            }
+                            for (int i = 0; i < H; i += 4) *reinterpret_cast<float4 *>(s_fac + i) = make_float4(p[i], p[i + 1], p[i + 2], p[i + 3]);
                         }
                         __syncwarp();
+                        if (lane < H) {
+                            const int lim = lims[lane];
+                            nms[lane] = lim < 0 ? 0.0f : page_ok && base + lead < lim ? -s_fac[lane] * sl2 : INFINITY;
+                        }
                     }
                     fw_bar(bid);
                     load_off();
                 }
                 bool high = false;
-                if (good && rows > 0) high = edge ? !probs(std::true_type{}) : !probs(std::false_type{});
+                if (good && rows > 0) high = !probs(t, tS, std::true_type{}, flags);
                 const bool any = fw_bar_or(bid, high);
                 if (s_bad[half]) {
                     ok = false;
@@ -448,7 +491,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     fw_ld<H>(tS, p);
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
-                        const bool see = !edge || (page_ok && base + r < lims[i]);
+                        const bool see = page_ok && base + r < lims[i];
                         const uint32_t u = __reduce_max_sync(0xffffffffu, float_to_ordered(see ? p[i] * sl2 : -INFINITY));
                         if (lane == i % 32) s_red[wq * H + i] = ordered_to_float(u);
                     }
@@ -470,8 +513,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                         p[i] *= f;
                     }
                     if (t > 0) fw_st<H>(tO, p);
-                    if (edge) probs(std::true_type{});
-                    else probs(std::false_type{});
+                    probs(t, tS, std::true_type{}, flags);
                 }
                 // a key behind the sequence's end weighs nothing, but 0 x NaN is NaN: its V row becomes zero
                 if (half == 0 && base + kPfTile > seg.len) {
@@ -485,19 +527,8 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                         }
                     }
                 }
-                tc::fence_proxy_async_smem();  // P^T, and V rows made zero
-                tc::fence_before();
-                pf_arrive(bar(SM::kPFull + buf));
-#pragma unroll
-                for (int c = 0; c < H; c += 8) {
-                    if (c >= rows) break;
-#pragma unroll
-                    for (int i = c; i < c + 8; i += 2) {
-                        const float2 sum = add2({l[i], l[i + 1]}, {p[i], p[i + 1]});
-                        l[i] = sum.x;
-                        l[i + 1] = sum.y;
-                    }
-                }
+                deliver(buf);
+                ++t;
             }
             if (!ok) break;
             // the warp's row sums: each step halves the rows a lane holds (8, 16 or 32 rows over 32 lanes)

@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                         for (int h = 0; h < SM::KH; ++h) {
                             uint4 *row = reinterpret_cast<uint4 *>(s + SM::V + vs * SM::OP + h * 16384 + r * 128);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+                            for (int i = 0; i < 8; ++i) row[i ^ (r & 7)] = make_uint4(0, 0, 0, 0);  // (eight lanes, all banks)
                         }
                     }
                 }

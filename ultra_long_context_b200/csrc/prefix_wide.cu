@@ -16,6 +16,8 @@
 //   warps 18-19 Q rows by cp.async, padded with zero rows.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "prefix.cuh"
 #include "profile.h"
 
@@ -358,68 +360,80 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             const bool mine = rr < seg.nr;
             const bool active = rr - lane < seg.nr;  // do this pair's warps hold any row?
             const int lim = mine ? pf_limit(a, seg, d, rr) : INT32_MAX;
-            float ms = 0.0f, l = 0.0f;
-            // the half that holds the first key at hand, whose logit becomes the reference
-            const PfPages pages(seg, a.num_pages);
-            uint32_t there_all = pages.there(pages.fetch(seg.tile0));
-            int id_next = pages.fetch(seg.tile0 + 16);
-            const bool lead = half == (there_all >> 2 * t0 & 1u ? 0 : 1);
-            for (int t = t0; t < seg.nt; t += dt, ++tiles) {
-                if ((t & 15) < dt && t >= 16) {
-                    there_all = pages.there(id_next);
-                    id_next = pages.fetch(seg.tile0 + (t & ~15) + 16);
+            float ms = 0.0f, l = 0.0f, x[32];
+            uint32_t pk[32];  // P of this half as bf16 pairs
+            // 32 keys at a time: the logits of 64 beside their P would not fit a thread's 96 registers
+            auto probs = [&](const int c, auto with_edge, const int vis) {
+                const float2 scale2 = {sl2, sl2}, off2 = {-ms, -ms};
+                float2 s2[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                tc::tmem_ld32(tS + 64 * half + 32 * c, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 y = fma2({x[2 * i], x[2 * i + 1]}, scale2, off2);
+                    float2 p = {ex2_approx(y.x), ex2_approx(y.y)};
+                    if constexpr (decltype(with_edge)::value) {
+                        const int k = 32 * c + 2 * i;
+                        p = {k < vis ? p.x : 0.0f, k + 1 < vis ? p.y : 0.0f};
+                    }
+                    s2[i & 1] = add2(s2[i & 1], p);
+                    pk[16 * c + i] = pack_bf16x2(p.x, p.y);
                 }
-                const bool there = there_all >> (2 * (t & 15) + half) & 1u;
-                const int n = g.n0 + t, vs = n % VS;
+                return (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+            };
+            const PfPages pages(seg, a.num_pages);
+            int id_next = pages.fetch(seg.tile0), block_end = 0;  // of the 16 tiles whose pages `there_all` tells of
+            uint32_t there_all = 0;
+            // the tiles before this one lie before the sequence's end, for each of the pair's rows, too
+            const int whole = min((int)__reduce_min_sync(0xffffffffu, (uint32_t)lim), seg.len) / kPfTile - seg.tile0;
+            bool redo = false;
+            for (int t = t0; t < seg.nt;) {
+                if (t >= block_end) {
+                    there_all = pages.there(id_next);
+                    id_next = pages.fetch(seg.tile0 + block_end + 16);
+                    block_end += 16;
+                }
+                // Tiles that every row sees all of, in a loop of their own (see prefix_few.cu)
+                const uint32_t gaps = ~(there_all & there_all >> 1) & 0x55555555u & ~0u << 2 * (t & 15);
+                const int stop = min(min(seg.nt, whole), gaps ? block_end - 16 + (__ffs(gaps) - 1) / 2 : block_end);
+                if (t > t0 && active && !redo) {
+                    for (; t < stop; t += dt, ++tiles) {
+                        const bool good = pf_wait(bar(SM::kSFull + sid), tiles);
+                        tc::fence_after();
+                        float sum = probs(0, std::false_type{}, 64);
+                        sum += probs(1, std::false_type{}, 64);
+                        redo = pf_pair_or(pid, !good || sum > kPfSumMax);
+                        if (redo) break;
+                        tc::tmem_st32(tS + 64 * half, pk);
+                        l += sum;
+                        tc::fence_before();
+                        pf_arrive(bar(SM::kPFull + sid));
+                    }
+                    if (t >= seg.nt) break;
+                    if (t >= block_end) continue;
+                }
+                redo = false;
+                // Any tile: the first, the ones with an edge, and those where a term left the range
+                const int flags = there_all >> 2 * (t & 15) & 3u, n = g.n0 + t, vs = n % VS;
                 const int base = (seg.tile0 + t) * kPfTile;
-                const int vis = there ? lim - base - 64 * half : 0;  // keys of this half that the row sees
-                const bool edge = __any_sync(0xffffffffu, vis < 64);
+                const int vis = flags >> half & 1 ? lim - base - 64 * half : 0;  // keys of this half that the row sees
                 bool good = pf_wait(bar(SM::kSFull + sid), tiles);
                 tc::fence_after();
                 if (!good) s_badp[pid - 1] = 1;
                 if (active) {
-                    uint32_t pk[32];  // P of this half as bf16 pairs
-                    // 32 keys at a time: the logits of 64 beside their P would not fit a thread's 96 registers
-                    auto probs = [&](const float (&x)[32], const int c) {
-                        const float2 scale2 = {sl2, sl2}, off2 = {-ms, -ms};
-                        float2 s2[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-                        if (edge) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 y = fma2({x[2 * i], x[2 * i + 1]}, scale2, off2);
-                                const int k = 32 * c + 2 * i;
-                                const float2 p = {k < vis ? ex2_approx(y.x) : 0.0f, k + 1 < vis ? ex2_approx(y.y) : 0.0f};
-                                s2[i & 1] = add2(s2[i & 1], p);
-                                pk[16 * c + i] = pack_bf16x2(p.x, p.y);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 y = fma2({x[2 * i], x[2 * i + 1]}, scale2, off2);
-                                const float2 p = {ex2_approx(y.x), ex2_approx(y.y)};
-                                s2[i & 1] = add2(s2[i & 1], p);
-                                pk[16 * c + i] = pack_bf16x2(p.x, p.y);
-                            }
-                        }
-                        return (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-                    };
-                    float x[32];
-                    __syncwarp();
-                    tc::tmem_ld32(tS + 64 * half, x);
                     if (t == t0) {  // the row's reference: its first key, or the second page's where the first is bad
-                        if (lead) s_row[0] = vis > 0 ? x[0] * sl2 : -INFINITY;
+                        if (half == (flags & 1 ? 0 : 1)) {
+                            tc::tmem_ld32(tS + 64 * half, x);
+                            s_row[0] = vis > 0 ? x[0] * sl2 : -INFINITY;
+                        }
                         pf_pair_bar(pid);
                         ms = s_row[0];
                     }
-                    float sum = probs(x, 0);
-                    tc::tmem_ld32(tS + 64 * half + 32, x);
-                    sum += probs(x, 1);
-                    const bool any = pf_pair_or(pid, sum > kPfSumMax);
-                    if (s_badp[pid - 1]) {
-                        ok = false;
-                        break;
-                    }
-                    if (any) {
+                    float sum;
+#pragma unroll 1
+                    for (bool again = false;; again = true) {
+                        sum = probs(0, std::true_type{}, vis);
+                        sum += probs(1, std::true_type{}, vis);
+                        if (again || !pf_pair_or(pid, sum > kPfSumMax)) break;
                         float mx = -INFINITY;
 #pragma unroll 1
                         for (int c = 0; c < 2; ++c) {
@@ -446,10 +460,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                                 tc::tmem_st32f(tO + c, x);
                             }
                         }
-                        tc::tmem_ld32(tS + 64 * half, x);
-                        sum = probs(x, 0);
-                        tc::tmem_ld32(tS + 64 * half + 32, x);
-                        sum += probs(x, 1);
+                    }
+                    if (s_badp[pid - 1]) {
+                        ok = false;
+                        break;
                     }
                     tc::tmem_st32(tS + 64 * half, pk);
                     l += sum;
@@ -464,13 +478,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                         for (int h = 0; h < SM::KH; ++h) {
                             uint4 *row = reinterpret_cast<uint4 *>(s + SM::V + vs * SM::OP + h * 16384 + r * 128);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+                            for (int i = 0; i < 8; ++i) row[i ^ (r & 7)] = make_uint4(0, 0, 0, 0);  // (eight lanes, all banks)
                         }
                     }
                     tc::fence_proxy_async_smem();
                 }
                 tc::fence_before();
                 pf_arrive(bar(SM::kPFull + sid));
+                t += dt;
+                ++tiles;
             }
             if (!ok) break;
             // (warps without a row wait as well: they must not come to the next segment's end before this one's)

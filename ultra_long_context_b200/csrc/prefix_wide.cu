@@ -11,9 +11,11 @@
 //               logits stay in registers). The work is a sequence of items that go to the streams in turn: a
 //               segment of more than 128 rows has two items per tile, one for each 128 rows; a smaller one has one
 //               (and each stream keeps a partial of its own). So one stream's products run under the other's softmax;
-//   warp 16     MMA issuer, in a fixed order: S(i + 1), then O(i);
-//   warp 17     K and V tiles by TMA, page by page (64 rows of one head are contiguous);
-//   warps 18-19 Q rows by cp.async, padded with zero rows.
+//   warp 16     issues the products S of the items, in order;
+//   warp 17     issues the products O, in order (one warp for both spent 2300 cycles on an item, half of them in waits
+//               for what was there already and in its own bookkeeping);
+//   warp 18     walks the segments and copies K and V tiles by TMA, page by page (64 rows of one head are contiguous);
+//   warp 19     Q rows by cp.async, padded with zero rows.
 #include <cuda.h>
 
 #include <type_traits>
@@ -24,7 +26,7 @@
 namespace hsa {
 
 constexpr int kPfStreamWarps = 8;
-constexpr int kPfMmaWarp = 2 * kPfStreamWarps, kPfTmaWarp = kPfMmaWarp + 1, kPfQWarp = kPfMmaWarp + 2, kPfQWarps = 2;
+constexpr int kPfSWarp = 2 * kPfStreamWarps, kPfOWarp = kPfSWarp + 1, kPfTmaWarp = kPfSWarp + 2, kPfQWarp = kPfSWarp + 3, kPfQWarps = 1;
 constexpr int kPfThreads = 32 * (kPfQWarp + kPfQWarps);
 constexpr float kPfGrow = 64.0f, kPfSumMax = 0x1p70f;  // a sum of 64 terms of at most 2^64
 
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     auto bar = [&](int i) { return sb + SM::BAR + 8u * (uint32_t)i; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (warp == kPfMmaWarp) tc::tmem_alloc(sb + SM::TMEM, SM::TMEM_COLS);
+    if (warp == kPfSWarp) tc::tmem_alloc(sb + SM::TMEM, SM::TMEM_COLS);
     if (warp == kPfTmaWarp && lane == 0) {
         pf_prefetch_tmap(&tmK);
         pf_prefetch_tmap(&tmV);
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         }
         for (int i = 0; i < kPfRing; ++i) {
             tc::mbar_init(bar(SM::kSegFull + i), 1);
-            tc::mbar_init(bar(SM::kSegEmpty + i), 2 * kPfStreamWarps + kPfQWarps + 1);  // the warps but this ring's writer
+            tc::mbar_init(bar(SM::kSegEmpty + i), 2 * kPfStreamWarps + kPfQWarps + 2);  // the warps but this ring's writer
         }
         tc::fence_mbar_init();
     }
@@ -241,98 +243,75 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         }
         cp_async_commit();
         cp_async_wait<0>();  // nothing in flight when the CTA exits
-    } else if (warp == kPfMmaWarp) {
-        // ================= MMA issuer: the whole warp runs the loop, one elected lane issues =================
-        constexpr uint32_t idesc_s = tc::idesc_bf16(kPfTile, kPfTile, 0, 0);
-        constexpr uint32_t idesc_o = tc::idesc_bf16(kPfTile, D, 0, 1);
-        // Every filling of every slot is waited for in order. Nothing waits for an O that is not issued yet: S(i + 1) needs
-        // O(i - 1), and its K, in the copies' order, slots that O(i - 1) and earlier ones release; a segment that is not
-        // announced yet is waited for only when no O is due (its announcement comes after the copies of the one before).
-        PfNote g{};
-        int nt = 0, items = 0, u = 0, q0 = 0, turn = 0;  // of the segment at item i_s: u is the item's number in it
-        bool both = false, end = false;
-        uint32_t uses0 = 0, uses1 = 0;                   // fillings of the Q buffers before this segment's
-        int i_s = 0, i_o = 0, v_last = -1;               // next items; the tile whose V was waited for last
-        uint32_t issued[2] = {0, 0}, runs[2] = {0, 0};   // O products of a stream; its runs (one per segment) begun
-        int tile[2] = {0, 0};                            // of the stream's item at O: its tile's number,
-        bool first[2] = {false, false}, last[2] = {false, false};  // does it begin a run; is it the tile's last item
-        auto issue_s = [&](const int sid) {
-            const int t = both ? u >> 1 : u, n = g.n0 + t, ks = n % KS, q = both ? u & 1 : q0;
-            const bool starts = both ? u < 2 : u == 0;  // the first to read its Q buffer
-            if (!both || !(u & 1)) ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS));  // (once for a tile)
-            if (ok && starts) ok = pf_wait(bar(SM::kQFull + q), q ? uses1 : uses0);
-            // S and P share columns: P of the stream's item before must have been read
-            if (ok && issued[sid] > 0) ok = pf_wait(bar(SM::kODone + sid), (issued[sid] - 1) & 1u);
-            if (!ok) return;
-            tc::fence_after();
-            if (starts) tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
-            const uint64_t dq = tc::desc_kmajor(sb + SM::Q + q * SM::OP), dk = tc::desc_kmajor(sb + SM::K + ks * SM::OP);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {  // (a descriptor's low bits are its address / 16)
-                const uint64_t off = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * kPfTile, dq + off, dk + off, idesc_s, k > 0 ? 1u : 0u);
-            }
-            tc::commit_w(bar(SM::kSFull + sid));
-            tile[sid] = n;
-            first[sid] = u < 2;
-            last[sid] = !both || (u & 1);
-            if (first[sid]) ++runs[sid];
-            if (last[sid]) tc::commit_w(bar(SM::kKEmpty + ks));
-            if (u >= items - (both ? 2 : 1)) tc::commit_w(bar(SM::kQEmpty + q));
-            ++u;
-            ++i_s;
-        };
-        auto issue_o = [&](const int sid) {
-            const int n = tile[sid], vs = n % VS;
-            // (what is there long before comes first, so that only the wait for P is followed by the products)
-            if (n != v_last) ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS));  // (once for a tile)
-            v_last = n;
-            if (ok && first[sid] && runs[sid] > 1) ok = pf_wait(bar(SM::kOEmpty + sid), runs[sid]);
-            if (ok) ok = pf_wait(bar(SM::kPFull + sid), issued[sid]);
-            if (!ok) return;
-            tc::fence_after();
-            const uint64_t dv = tc::desc_mnmajor(sb + SM::V + vs * SM::OP, 16384);
-#pragma unroll
-            for (int k = 0; k < kPfTile / 16; ++k)  // a page's P stands where its S began
-                tc::mma_bf16_ts_w(tmem + SM::O_COL + sid * D, tmem + SM::S_COL + sid * kPfTile + (k >> 2) * 64 + (k & 3) * 8,
-                                  dv + (uint64_t)k * (2048 >> 4), idesc_o, !first[sid] || k > 0 ? 1u : 0u);
-            tc::commit_w(bar(SM::kODone + sid));
-            if (last[sid]) tc::commit_w(bar(SM::kVEmpty + vs));
-            ++issued[sid];
-            ++i_o;
-        };
-        while (ok) {
-            if (u == items && !end && i_s < i_o + 2) {
-                const int slot = seg_no % kPfRing;
-                if (i_o == i_s || pf_done(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kPfRing) & 1u)) {
-                    // the last segment's Q buffers have been counted as used
-                    ok = take(g);
+    } else if (warp == kPfSWarp) {
+        // ================= S products: the whole warp runs the loop, one elected lane issues =================
+        // Item i is item i / 2 of stream i % 2. Every filling of every slot is waited for, in order (here and below).
+        constexpr uint32_t idesc = tc::idesc_bf16(kPfTile, kPfTile, 0, 0);
+        PfNote g;
+        uint32_t uses0 = 0, uses1 = 0;  // fillings of the Q buffers before this segment's
+        int turn = 0;
+        while (true) {
+            ok = take(g);
+            if (!ok || g.s.nr == 0) break;
+            const bool both = pf_both(g.s);
+            const int q0 = both ? 0 : turn;
+            if (!both) turn ^= 1;
+            int i = g.i0;
+            for (int t = 0; t < g.s.nt && ok; ++t) {
+                const int n = g.n0 + t, ks = n % KS;
+                ok = pf_wait(bar(SM::kKFull + ks), (uint32_t)(n / KS));
+                for (int q = q0; ok && q < q0 + (both ? 2 : 1); ++q, ++i) {
+                    const int sid = i & 1;
+                    if (t == 0) ok = pf_wait(bar(SM::kQFull + q), q ? uses1 : uses0);
+                    // S and P share columns: P of the stream's item before must have been read
+                    if (ok && i >= 2) ok = pf_wait(bar(SM::kODone + sid), (uint32_t)(i / 2 - 1));
                     if (!ok) break;
-                    uses0 += items > 0 && (both || q0 == 0);
-                    uses1 += items > 0 && (both || q0 == 1);
-                    end = g.s.nr == 0;
-                    both = pf_both(g.s);
-                    nt = g.s.nt;
-                    items = end ? 0 : both ? 2 * nt : nt;
-                    u = 0;
-                    if (!end && !both) {
-                        q0 = turn;
-                        turn ^= 1;
+                    tc::fence_after();
+                    if (t == 0) tc::fence_proxy_async_smem();  // the Q rows came by cp.async (generic proxy)
+                    const uint64_t dq = tc::desc_kmajor(sb + SM::Q + q * SM::OP), dk = tc::desc_kmajor(sb + SM::K + ks * SM::OP);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {  // (a descriptor's low bits are its address / 16)
+                        const uint64_t off = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                        tc::mma_bf16_ss_w(tmem + SM::S_COL + sid * kPfTile, dq + off, dk + off, idesc, k > 0 ? 1u : 0u);
                     }
+                    tc::commit_w(bar(SM::kSFull + sid));
+                    if (t == g.s.nt - 1) tc::commit_w(bar(SM::kQEmpty + q));
                 }
+                if (ok) tc::commit_w(bar(SM::kKEmpty + ks));
             }
-            if (u < items && i_s < i_o + 2) {
-                if (i_s & 1) issue_s(1);
-                else issue_s(0);
+            if (!ok) break;
+            uses0 += both || q0 == 0;
+            uses1 += both || q0 == 1;
+        }
+        __syncwarp();
+    } else if (warp == kPfOWarp) {
+        // ================= O products =================
+        constexpr uint32_t idesc = tc::idesc_bf16(kPfTile, D, 0, 1);
+        PfNote g;
+        uint32_t runs0 = 0, runs1 = 0;  // of a stream: sums begun in O, one per segment in which it has an item
+        while (true) {
+            ok = take(g);
+            if (!ok || g.s.nr == 0) break;
+            const int per = pf_both(g.s) ? 2 : 1, items = per * g.s.nt;
+            for (int u = 0; u < items; ++u) {
+                const int i = g.i0 + u, sid = i & 1, n = g.n0 + (per == 2 ? u >> 1 : u), vs = n % VS;
+                if (per == 1 || !(u & 1)) ok = pf_wait(bar(SM::kVFull + vs), (uint32_t)(n / VS));  // (once for a tile)
+                if (u < 2) {  // the stream's first: O of its segment before has been read out
+                    const uint32_t run = sid ? runs1++ : runs0++;
+                    if (ok && run > 0) ok = pf_wait(bar(SM::kOEmpty + sid), run - 1);
+                }
+                if (ok) ok = pf_wait(bar(SM::kPFull + sid), (uint32_t)(i / 2));
                 if (!ok) break;
-                if (i_s == i_o + 1) continue;  // the very first, or the only one at hand: one more S before its O
+                tc::fence_after();
+                const uint64_t dv = tc::desc_mnmajor(sb + SM::V + vs * SM::OP, 16384);
+#pragma unroll
+                for (int k = 0; k < kPfTile / 16; ++k)  // a page's P stands where its S began
+                    tc::mma_bf16_ts_w(tmem + SM::O_COL + sid * D, tmem + SM::S_COL + sid * kPfTile + (k >> 2) * 64 + (k & 3) * 8,
+                                      dv + (uint64_t)k * (2048 >> 4), idesc, u >= 2 || k > 0 ? 1u : 0u);
+                tc::commit_w(bar(SM::kODone + sid));
+                if (per == 1 || (u & 1)) tc::commit_w(bar(SM::kVEmpty + vs));
             }
-            if (i_o < i_s) {
-                if (i_o & 1) issue_o(1);
-                else issue_o(0);
-            } else if (end) {
-                break;
-            }
+            if (!ok) break;
         }
         __syncwarp();
     } else {
@@ -526,7 +505,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     tc::fence_before();
     __syncthreads();
     if (tid == 0) w.status[blockIdx.x] = *s_bad;
-    if (warp == kPfMmaWarp) {
+    if (warp == kPfSWarp) {
         tc::fence_after();
         tc::tmem_dealloc(tmem, SM::TMEM_COLS);
     }

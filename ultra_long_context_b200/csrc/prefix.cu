@@ -1,5 +1,7 @@
 // prefix.cu -- the shared-prefix decode: its launches, its workspace, and the join of the segments' partials.
 // How the work is divided stands in prefix.cuh.
+#include <type_traits>
+
 #include "prefix.cuh"
 #include "profile.h"
 
@@ -7,114 +9,99 @@ namespace hsa {
 
 // Joins a row's partials: M = max m_i, out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i. `wpr` warps of a block (1, 2, 4
 // or 8) share a row's partials, each with a maximum of its own, so that a few rows of many partials are not
-// read one after the other.
-constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32;
+// read one after the other. Bound by latency: the plan, then a row's statistics and, at the same time, its first
+// partials. blockIdx.y is the request.
+constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32, kPfJoinLoads = 8;
+constexpr int kPfJoinFill = 16;  // warps per SM, about, from which on rows are not split further
 
 template <int D>
 __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const PrefixArgs a, const PfDims d, const PfWork w,
-                                                                     int ctas, int wpr) {
+                                                                     int ctas, int wpr, int request_rows) {
+    constexpr int V = D / 32;  // columns per lane
+    using Vec = std::conditional_t<V == 4, float4, float2>;
     __shared__ float s_acc[kPfJoinWarps][D], s_M[kPfJoinWarps], s_L[kPfJoinWarps];
     pdl_launch_dependents();  // what follows may set itself up; it waits for this grid's end before it reads
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wi = warp & (wpr - 1);
+    const int b = blockIdx.y, bl = b & ~31, hr_n = a.Hkv * d.Rgo;
+    const int want = (int)blockIdx.x * (kPfJoinWarps / wpr) + warp / wpr, rem = min(want, request_rows - 1);
+    const int h = rem / d.Ro, ro = rem - h * d.Ro;  // (row counts stay below 2^31 / D)
+    const int rp = b * d.Ro + ro, rg = rp / d.gp, rr = rp - rg * d.gp, nr = min(d.gp, d.Rp - rg * d.gp);
+    const int per = d.wide && nr <= kPfTile ? 2 : 1;  // streams with a partial of the row
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    if (blockIdx.x == 0 && threadIdx.x < 32) {
+    if (blockIdx.x == 0 && b == 0 && warp == 0) {
         int bad = 0;
         for (int i = lane; i < ctas; i += 32) bad |= (d.wide ? w.status[i] : 0) | w.status[kPfCtas + i];
         bad = __any_sync(0xffffffffu, bad != 0);
         if (lane == 0) *w.err = bad;
     }
-    const int warp = threadIdx.x >> 5, wi = warp & (wpr - 1);
-    const int64_t rows = (int64_t)a.B * a.H * a.Tq;
-    const int64_t want = (int64_t)blockIdx.x * (kPfJoinWarps / wpr) + warp / wpr, row = min(want, rows - 1);
     const PfPlan p = *w.planP, po = *w.planO;
-    const int b = (int)(row / ((int64_t)a.H * a.Tq)), hr_n = a.Hkv * d.Rgo;
-    const int rem = (int)(row % ((int64_t)a.H * a.Tq)), h = rem / d.Ro, ro = rem % d.Ro;
+    const int cum0 = w.bcum[bl >> 5];
     // the lengths of the row's block of 32 requests, a lane each
-    const int bl = b & ~31;
     const int64_t len = bl + lane < a.B ? pf_clamp_len(a.own_len[bl + lane], a.max_pages) : -1;
-    int sum = pf_weight(len);
-    const int wt = __shfl_sync(0xffffffffu, sum, b & 31);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-    }
-    const int64_t cum = w.bcum[bl >> 5] + __shfl_sync(0xffffffffu, sum, b & 31) - wt;
+    const int wl = pf_weight(len), wt = __shfl_sync(0xffffffffu, wl, b & 31);
+    const int cum = cum0 + __reduce_add_sync(0xffffffffu, lane < (b & 31) ? wl : 0);
     const bool live = __shfl_sync(0xffffffffu, (int)(len >= 0), b & 31) != 0;
-    int np = 0, per = 1, nr = 0, rr = 0, rg = 0;      // prefix partials: np runs of `per` streams
-    int i0 = 0, no = 0, orr = 0, obase = 0;           // own partials: CTAs i0 .. i0 + no - 1
-    int64_t x0 = 0;
-    if (live) {
-        const int rp = b * d.Ro + ro;
-        rg = rp / d.gp;
-        rr = rp - rg * d.gp;
-        nr = min(d.gp, d.Rp - rg * d.gp);
-        per = d.wide && nr <= kPfTile ? 2 : 1;
-        np = p.items > 0 ? p.nsplit : 0;
-        if (wt > 0) {
-            const int hr = h * d.Rgo + ro / kPfFewRows;
-            x0 = cum * hr_n + (int64_t)hr * wt;
-            i0 = po.cta_of(x0);
-            no = po.cta_of(x0 + wt - 1) - i0 + 1;
-            obase = b * hr_n + hr;
-            orr = ro % kPfFewRows;
-        }
+    const int np = live && p.items > 0 ? p.nsplit * per : 0;  // prefix partials, and own ones: CTAs i0 .. i0 + no - 1
+    int i0 = 0, no = 0;
+    const int hr = h * d.Rgo + ro / kPfFewRows;
+    const int64_t x0 = (int64_t)cum * hr_n + (int64_t)hr * wt;
+    if (wt > 0) {
+        i0 = po.cta_of(x0);
+        no = po.cta_of(x0 + wt - 1) - i0 + 1;
     }
-    const int total = np * per + no;
+    const int total = np + no;
     // partial idx: its place (rows of D), or -1
-    auto place = [&](int idx) -> int64_t {
-        if (idx < np * per) {
-            const int k = idx / per, st = idx - k * per;
-            const int nt = min(p.run, p.tiles - k * p.run);
-            if (st >= nt) return -1;
-            return (int64_t)((k * a.Hkv + h) * d.Rgp + rg) * d.strideP + st * nr + rr;
+    auto place = [&](int idx) -> int {
+        if (idx < np) {
+            const int k = per == 2 ? idx >> 1 : idx, st = per == 2 ? idx & 1 : 0;
+            return st < min(p.run, p.tiles - k * p.run) ? ((k * a.Hkv + h) * d.Rgp + rg) * d.strideP + st * nr + rr : -1;
         }
-        const int i = i0 + (idx - np * per);
+        const int i = i0 + (idx - np);
         const int nt = pf_tile_at(min(po.start(i + 1), x0 + wt) - x0) - pf_tile_at(max(po.start(i), x0) - x0);
-        return nt > 0 ? (int64_t)(obase + i) * d.strideO + orr : -1;
+        return nt > 0 ? (b * hr_n + hr + i) * d.strideO + ro % kPfFewRows : -1;
     };
-    const float2 *mlp = reinterpret_cast<const float2 *>(w.mlp), *mlo = reinterpret_cast<const float2 *>(w.mlo);
-    float M = -INFINITY;
-    for (int idx = wi + wpr * lane; idx < total; idx += 32 * wpr) {
-        const int64_t at = place(idx);
-        if (at >= 0) M = fmaxf(M, (idx < np * per ? mlp : mlo)[at].x);
-    }
+    float M = -INFINITY, acc[V] = {}, L = 0.0f;
+    for (int base = wi; base < total; base += 32 * wpr) {
+        const int idx = base + wpr * lane, at = idx < total ? place(idx) : -1;
+        float2 ml = {-INFINITY, 0.0f};
+        if (at >= 0) ml = reinterpret_cast<const float2 *>(idx < np ? w.mlp : w.mlo)[at];
+        const float *src = at < 0 ? nullptr : (idx < np ? w.Op : w.Oo) + (size_t)at * D;
+        const int cnt = min(32, (total - base + wpr - 1) / wpr);
+        float f = 0.0f;
+#pragma unroll 1
+        for (int k0 = 0; k0 < cnt; k0 += kPfJoinLoads) {
+            Vec o[kPfJoinLoads];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    constexpr int V = D / 32;  // columns per lane
-    float acc[V] = {}, L = 0.0f;
-    if (M > -INFINITY) {
-        for (int base = wi; base < total; base += 32 * wpr) {
-            const int idx = base + wpr * lane;
-            int64_t at = idx < total ? place(idx) : -1;
-            float f = 0.0f;
-            if (at >= 0) {
-                const float2 ml = (idx < np * per ? mlp : mlo)[at];
-                f = ml.x > -INFINITY ? ex2_approx(ml.x - M) : 0.0f;
-                L = fmaf(ml.y, f, L);
+            for (int k = 0; k < kPfJoinLoads; ++k) {
+                const auto O = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k0 + k));
+                o[k] = Vec{};
+                if (O) o[k] = *reinterpret_cast<const Vec *>(O + lane * V);
             }
-            const float *src = at < 0 || f == 0.0f ? nullptr : (idx < np * per ? w.Op : w.Oo) + at * D;
-            const int cnt = min(32, (total - base + wpr - 1) / wpr);
-#pragma unroll 8
-            for (int k = 0; k < cnt; ++k) {
-                const float fk = __shfl_sync(0xffffffffu, f, k);
-                const float *O = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k));
-                if (!O) continue;
+            if (k0 == 0) {
+                float top = ml.x;
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                const float M1 = fmaxf(M, top), g = M > -INFINITY ? ex2_approx(M - M1) : 0.0f;
+                f = ml.x > -INFINITY ? ex2_approx(ml.x - M1) : 0.0f;
+                M = M1;
+                L = fmaf(ml.y, f, L * g);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] *= g;
+            }
+#pragma unroll
+            for (int k = 0; k < kPfJoinLoads; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, k0 + k);
+                if (fk == 0.0f) continue;  // (what a row without a visible key left there may be anything)
+                acc[0] = fmaf(fk, o[k].x, acc[0]);
+                acc[1] = fmaf(fk, o[k].y, acc[1]);
                 if constexpr (V == 4) {
-                    const float4 o = *reinterpret_cast<const float4 *>(O + lane * V);
-                    acc[0] = fmaf(fk, o.x, acc[0]);
-                    acc[1] = fmaf(fk, o.y, acc[1]);
-                    acc[2] = fmaf(fk, o.z, acc[2]);
-                    acc[3] = fmaf(fk, o.w, acc[3]);
-                } else {
-                    const float2 o = *reinterpret_cast<const float2 *>(O + lane * V);
-                    acc[0] = fmaf(fk, o.x, acc[0]);
-                    acc[1] = fmaf(fk, o.y, acc[1]);
+                    acc[2] = fmaf(fk, o[k].z, acc[2]);
+                    acc[3] = fmaf(fk, o[k].w, acc[3]);
                 }
             }
         }
-        L = warp_sum(L);
     }
+    L = warp_sum(L);
     if (wpr > 1) {
 #pragma unroll
         for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
@@ -137,7 +124,8 @@ __global__ void __launch_bounds__(kPfJoinThreads) prefix_join_kernel(const Prefi
             for (int i = 0; i < V; ++i) acc[i] = fmaf(s_acc[warp + k][lane * V + i], f, acc[i]);
         }
     }
-    if (want >= rows) return;
+    if (want >= request_rows) return;
+    const int64_t row = (int64_t)b * request_rows + rem;
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     uint32_t *out = reinterpret_cast<uint32_t *>(a.out + row * D + lane * V);
 #pragma unroll
@@ -180,14 +168,14 @@ cudaError_t launch_prefix_decode(const PrefixArgs &a, cudaStream_t s) {
     if (d.wide) e = launch_prefix_wide(a, d, w, ctas, s);
     if (e == cudaSuccess) e = launch_prefix_few(a, d, w, ctas, s);
     if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)a.B * a.H * a.Tq;
+    const int request_rows = a.H * a.Tq;
     int wpr = kPfJoinWarps;
-    while (wpr > 1 && rows * wpr > 16 * kPfCtas) wpr /= 2;  // about 16 warps per SM at most
+    while (wpr > 1 && kPfJoinWarps / wpr < request_rows && (int64_t)a.B * request_rows * wpr > kPfJoinFill * kPfCtas) wpr /= 2;
     const int per_block = kPfJoinWarps / wpr;
-    const unsigned grid = (unsigned)((rows + per_block - 1) / per_block);
+    const dim3 grid((request_rows + per_block - 1) / per_block, a.B);
     HSA_PROF("prefix_join", s);
-    return a.D == 128 ? launch_pdl(prefix_join_kernel<128>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wpr)
-                      : launch_pdl(prefix_join_kernel<64>, dim3(grid), dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wpr);
+    return a.D == 128 ? launch_pdl(prefix_join_kernel<128>, grid, dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wpr, request_rows)
+                      : launch_pdl(prefix_join_kernel<64>, grid, dim3(kPfJoinThreads), 0, s, a, d, w, ctas, wpr, request_rows);
 }
 
 }  // namespace hsa

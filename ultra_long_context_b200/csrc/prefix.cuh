@@ -24,6 +24,11 @@ constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per he
 // Costs in half tiles: a tile, and what a segment's start and end take beside its tiles
 constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 4;
 
+// a / b for a >= 0, b > 0, in 32 bits where they suffice (a 64-bit division takes several times as long)
+__device__ __forceinline__ int64_t pf_div(int64_t a, int64_t b) {
+    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // The division of one kernel's work; every CTA computes the same, CTA 0 stores it for the join.
 //   prefix: per key head and row group (a unit), `nsplit` runs of `run` tiles; segment i = run i / units of unit
 //   i % units goes to CTA i % ctas, so that the row groups of one run, which read the same keys, do so at about the
@@ -39,7 +44,7 @@ struct PfPlan {
         return x < axis ? x : axis;
     }
     __device__ int cta_of(int64_t x) const {
-        return x < lo_ctas * cap_lo ? (int)(x / cap_lo) : lo_ctas + (int)((x - lo_ctas * cap_lo) / cap_hi);
+        return x < lo_ctas * cap_lo ? (int)pf_div(x, cap_lo) : lo_ctas + (int)pf_div(x - lo_ctas * cap_lo, cap_hi);
     }
 };
 
@@ -94,11 +99,6 @@ __device__ __forceinline__ int pf_tiles(int64_t n) { return n > 0 ? (int)((n + k
 __device__ __forceinline__ int pf_weight(int64_t n) { return n > 0 ? kPfTileCost * pf_tiles(n) + kPfOwnCost : 0; }
 // Tile boundary of a place on a stretch: 0 at its start, the number of tiles at its end, never decreasing.
 __device__ __forceinline__ int pf_tile_at(int64_t at) { return (int)(max(at - kPfOwnCost + kPfTileCost - 1, (int64_t)0) / kPfTileCost); }
-
-// a / b for a >= 0, b > 0, in 32 bits where they suffice (a 64-bit division takes several times as long)
-__device__ __forceinline__ int64_t pf_div(int64_t a, int b) {
-    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
 
 struct PfSeg {
     int h, b;            // key head; request (own segments; -1: prefix)

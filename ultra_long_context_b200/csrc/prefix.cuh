@@ -22,7 +22,7 @@ constexpr int kPfWideRows = 256;  // in the wide kernel
 constexpr int kPfCtas = 148;      // at most: one per SM; the workspace is sized for it
 constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per head and row group)
 // Costs in half tiles: a tile, and what a segment's start and end take beside its tiles
-constexpr int kPfTileCost = 2, kPfPrefixCost = 3, kPfOwnCost = 4;
+constexpr int kPfTileCost = 2, kPfPrefixCost = 5, kPfOwnCost = 5;
 
 // a / b for a >= 0, b > 0, in 32 bits where they suffice (a 64-bit division takes several times as long)
 __device__ __forceinline__ int64_t pf_div(int64_t a, int64_t b) {
@@ -55,14 +55,17 @@ struct PfDims {
     int Ro, Rgo;           // own rows per request and key head, in groups of kPfFewRows
     int strideP, strideO;  // rows of one segment's partials (in the wide kernel, two streams may each keep one of the same rows)
     int max_items, max_slots, blocks;  // blocks: of 32 requests
-    // Which kernel ends the prefix sooner? A tile of 128 keys takes the few-rows kernel 1.35 us (D = 128; 1.07 with D = 64)
-    // for 64 rows, the wide one 2.3 us (2.1) for 256, and that is a launch of its own, worth 14 us. Both sides measured:
-    // 256 rows x 8 heads, D = 128, over 6144 / 9856 / 12160 tokens 39 / 48 / 56 us and 46 / 50 / 52, D = 64 over 70912
-    // 164 and 92. The tiles are those of the table, since the length is not known here.
+    // Which kernel ends the prefix sooner? A tile of 128 keys takes the few-rows kernel 0.92 us (D = 128; 0.75 with D = 64)
+    // for 64 rows, the wide one 2.3 us (1.8) for 256 and 1.5 us (1.0) for up to 128, and that is a launch of its own with
+    // larger tiles to fill: 20 us (12). Both sides measured, D = 128: 512 rows x 4 heads over 14208 / 28416 / 56832 tokens
+    // 38 / 67 / 111 us and 53 / 66 / 92, 1024 rows 65 / 110 / 209 and 73 / 100 / 150, 128 rows x 8 heads over 59136 68 and
+    // 71; D = 64: 512 rows 35 / 56 / 90 and 40 / 50 / 70. The tiles are those of the table, since the length is not known here.
     static bool pf_wide(int Rp, int Hkv, int D, int tiles) {
+        const bool d128 = D == 128;
         const double per_sm = (double)Hkv * tiles / kPfCtas;
-        const double few = per_sm * ((Rp + kPfFewRows - 1) / kPfFewRows) * (D == 128 ? 1.35 : 1.07);
-        const double wide = 14.0 + per_sm * ((Rp + kPfWideRows - 1) / kPfWideRows) * (D == 128 ? 2.3 : 2.1);
+        const double few = per_sm * ((Rp + kPfFewRows - 1) / kPfFewRows) * (d128 ? 0.92 : 0.75);
+        const double wide_tile = Rp > kPfTile ? (d128 ? 2.3 : 1.8) : (d128 ? 1.5 : 1.0);
+        const double wide = (d128 ? 20.0 : 12.0) + per_sm * ((Rp + kPfWideRows - 1) / kPfWideRows) * wide_tile;
         return Rp > kPfFewRows && wide < few;
     }
     PfDims(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages) {

@@ -173,8 +173,13 @@ def check_decode(q, Kp, Vp, pre, prefix, table, own, scale, squeeze=False, room=
     D = q.shape[-1]
     pre = np.concatenate([pre, np.full(room, -1, np.int32)])
     args = [torch.tensor(x, device=DEV) for x in (pre, [prefix], table, own)]
+    hsa.hsa_profile_enable(room > 0)
     out, lse = hsa.hsa_prefix_decode(q.squeeze(2) if squeeze else q, Kp, Vp, args[0], args[1], args[2], args[3], scale=scale, **kw)
     torch.cuda.synchronize()
+    if room:
+        if not 256 < q.shape[0] * q.shape[1] * q.shape[2] // Kp.shape[1] <= 320:
+            assert "prefix_wide" in hsa.hsa_profile_summary()
+        hsa.hsa_profile_enable(False)
     ref = paged.prefix_decode(npy(q), npy(Kp), npy(Vp), pre, prefix, table, own, scale if scale > 0 else D ** -0.5)
     got, got_lse = npy(out).astype(np.float64).reshape(ref["out"].shape), npy(lse).astype(np.float64).reshape(ref["lse"].shape)
     tol, tol_lse = paged.prefix_tolerance(ref, D)
@@ -221,7 +226,7 @@ def test_prefix_decode_equals_the_plain_form(case):
     check_decode(*decode_case(21, **case))
 
 
-WIDE = 4000   # with a table this long, batches of more than 64 rows per key head take the kernel for wide products
+WIDE = 60000   # with a table this long, batches of more than 64 rows per key head (but 257 to 320) take the kernel for wide products
 
 
 @pytest.mark.parametrize("case", [c for c in DECODES if c["B"] * c["H"] * c["Tq"] // c["Hkv"] > 64] + [
@@ -236,12 +241,17 @@ def test_prefix_decode_of_wide_batches_equals_the_plain_form(case):
     check_decode(*decode_case(41, **case), room=WIDE)
 
 
+@pytest.mark.parametrize("room", [0, WIDE])
+@pytest.mark.parametrize("B", [20, 40, 45])
 @pytest.mark.parametrize("sharp,scale", [(8.0, 0.0), (1.0, 2.0), (0.02, 0.0)])
-def test_wide_prefix_decode_of_peaked_and_flat_rows(sharp, scale):
-    check_decode(*decode_case(42, B=40, H=8, Hkv=2, Tq=1, D=128, prefix=2500, own=[i for i in range(40)], sharp=sharp, scale=scale), room=WIDE)
+def test_prefix_decode_of_peaked_and_flat_rows_in_groups(sharp, scale, B, room):
+    """Row groups that end early: 80, 160 and 180 rows per key head, in groups of 64 or of 256."""
+    for D in (64, 128):
+        check_decode(*decode_case(42, B=B, H=8, Hkv=2, Tq=1, D=D, prefix=2500, own=[i for i in range(B)], sharp=sharp, scale=scale), room=room)
 
 
-def test_wide_prefix_decode_maxima_that_keep_growing():
+@pytest.mark.parametrize("room", [0, WIDE])
+def test_prefix_decode_maxima_that_keep_growing_in_groups(room):
     """Rows of which some move their reference in every tile while others of the same tile do not."""
     for D, flip in ((64, False), (128, True), (128, False)):
         q, Kp, Vp, pre, prefix, table, own, scale = decode_case(43, B=90, H=2, Hkv=2, Tq=1, D=D, prefix=1500, own=[1] * 90, poison=False)
@@ -249,7 +259,7 @@ def test_wide_prefix_decode_maxima_that_keep_growing():
         if flip:
             size = size.flip(0)
         Kp[torch.tensor(pre.astype(np.int64), device=DEV)] = (q[::2].float().mean(0)[:, 0][None, :, None] * 8 * size[:, None, None, None]).to(BF16)
-        check_decode(q, Kp, Vp, pre, prefix, table, own, scale, room=WIDE)
+        check_decode(q, Kp, Vp, pre, prefix, table, own, scale, room=room)
 
 
 def test_wide_prefix_decode_leaves_out_bad_pages():

@@ -253,12 +253,8 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             if (!ok) break;
             const uint32_t dst = sb + SM::Q + q * SM::QB;
             PfQRows at(g.s, d, a.Hkv, rsub);
-            for (int r = rsub; r < (g.s.nr + 15) / 16 * 16; r += RPW, at.advance(RPW)) {
-                // (zeros, too, for the empty rows of a padded batch: whatever stands there must not look like a large logit)
-                const bool in = r < g.s.nr && (g.s.b >= 0 || a.own_len[at.request] >= 0);
-                cp_async16_u32(dst + (ch >> 3) * (NR * 128) + tc::sw128(r, ch & 7),
-                               in ? a.q + (int64_t)at.row * D + ch * 8 : a.q, in ? 16 : 0);
-            }
+            pf_copy_q<D, RPW>(a, at, rsub, g.s.nr, (g.s.nr + 15) / 16 * 16, g.s.b < 0,
+                              [&](int r) { return dst + (ch >> 3) * (NR * 128) + tc::sw128(r, ch & 7); }, ch);
             pf_cp_async_arrive(bar(SM::kQFull + q));  // fires when this thread's copies have landed
         }
         cp_async_commit();
@@ -505,14 +501,19 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     }
                     fw_bar(bid);
                     load_off();
-                    if (t > 0) fw_ld<H>(tO, p);
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const float f = s_fac[i];
-                        l[i] *= f;
-                        p[i] *= f;
+                    for (int c = 0; c < H; c += 8) {  // (the columns behind are the other warpgroup's)
+                        if (c >= rows) break;
+                        float o[8];
+                        if (t > 0) tc::tmem_ld8(tO + c, o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float f = s_fac[c + i];
+                            l[c + i] *= f;
+                            o[i] *= f;
+                        }
+                        if (t > 0) fw_st<8>(tO + c, o);
                     }
-                    if (t > 0) fw_st<H>(tO, p);
                     probs(t, tS, std::true_type{}, flags);
                 }
                 // a key behind the sequence's end weighs nothing, but 0 x NaN is NaN: its V row becomes zero

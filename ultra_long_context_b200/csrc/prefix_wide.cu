@@ -26,8 +26,8 @@
 namespace hsa {
 
 constexpr int kPfStreamWarps = 8;
-constexpr int kPfSWarp = 2 * kPfStreamWarps, kPfOWarp = kPfSWarp + 1, kPfTmaWarp = kPfSWarp + 2, kPfQWarp = kPfSWarp + 3, kPfQWarps = 1;
-constexpr int kPfThreads = 32 * (kPfQWarp + kPfQWarps);
+constexpr int kPfSWarp = 2 * kPfStreamWarps, kPfOWarp = kPfSWarp + 1, kPfTmaWarp = kPfSWarp + 2, kPfQWarp = kPfSWarp + 3;
+constexpr int kPfThreads = 32 * (kPfQWarp + 1);
 constexpr float kPfGrow = 64.0f, kPfSumMax = 0x1p70f;  // a sum of 64 terms of at most 2^64
 
 template <int D>
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             tc::mbar_init(bar(SM::kVEmpty + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(bar(SM::kQFull + i), 32 * kPfQWarps);
+            tc::mbar_init(bar(SM::kQFull + i), 32);
             tc::mbar_init(bar(SM::kQEmpty + i), 1);
             tc::mbar_init(bar(SM::kSFull + i), 1);
             tc::mbar_init(bar(SM::kPFull + i), kPfStreamWarps);
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         }
         for (int i = 0; i < kPfRing; ++i) {
             tc::mbar_init(bar(SM::kSegFull + i), 1);
-            tc::mbar_init(bar(SM::kSegEmpty + i), 2 * kPfStreamWarps + kPfQWarps + 2);  // the warps but this ring's writer
+            tc::mbar_init(bar(SM::kSegEmpty + i), kPfThreads / 32 - 1);  // the warps but this ring's writer
         }
         tc::fence_mbar_init();
     }
@@ -210,10 +210,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         // every copy has landed before the CTA may exit, however the walk ended
         for (int i = max(0, n - KS); i < n; ++i) pf_wait(bar(SM::kKFull + i % KS), (uint32_t)(i / KS) & 1u);
         for (int i = max(0, n - VS); i < n; ++i) pf_wait(bar(SM::kVFull + i % VS), (uint32_t)(i / VS) & 1u);
-    } else if (warp >= kPfQWarp) {
+    } else if (warp == kPfQWarp) {
         // ================= Q rows =================
         constexpr int CPR = D / 8, RPW = 32 / CPR;  // 16-byte chunks per row, rows per warp-wide copy
-        const int qw = warp - kPfQWarp, rsub = lane / CPR, ch = lane % CPR;
+        const int rsub = lane / CPR, ch = lane % CPR;
         uint32_t uses[2] = {0, 0};
         int turn = 0;
         PfNote g;
@@ -229,13 +229,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                 ++uses[q];
                 const int rows = min(kPfTile, seg.nr - k * kPfTile);
                 const uint32_t dst = sb + SM::Q + q * SM::OP;
-                // (the other rows are nobody's; zeros keep their logits small)
-                PfQRows at(seg, d, a.Hkv, k * kPfTile + qw * RPW + rsub);
-                for (int r = qw * RPW + rsub; r < kPfTile; r += kPfQWarps * RPW, at.advance(kPfQWarps * RPW)) {
-                    const bool in = r < rows && a.own_len[at.request] >= 0;  // (nor are those of empty rows of the batch)
-                    cp_async16_u32(dst + (ch >> 3) * 16384 + tc::sw128(r, ch & 7),
-                                   in ? a.q + (int64_t)at.row * D + ch * 8 : a.q, in ? 16 : 0);
-                }
+                PfQRows at(seg, d, a.Hkv, k * kPfTile + rsub);
+                pf_copy_q<D, RPW>(a, at, rsub, rows, kPfTile, true, [&](int r) { return dst + (ch >> 3) * 16384 + tc::sw128(r, ch & 7); }, ch);
                 pf_cp_async_arrive(bar(SM::kQFull + q));  // fires when this thread's copies have landed
             }
             if (!ok) break;
@@ -491,8 +486,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                     tc::tmem_ld32(tO + c, o);
                     if (mine) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            reinterpret_cast<float4 *>(O + c)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 32; i += 8) pf_store8(O + c + i, o + i);
                     }
                 }
                 pf_pair_bar(pid);  // s_row is written again by the next segment

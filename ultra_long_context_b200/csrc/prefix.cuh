@@ -247,21 +247,21 @@ struct PfQRows {
 
 // Copies a segment's q rows r0, r0 + STEP, .. below `end` to dst(row) by cp.async, the 16 bytes `ch` of each; zeros for the
 // rows from `rows` on, which are nobody's, and for the empty rows of a padded batch (where `padded` asks for it): whatever
-// stands there must not look like a large logit. Eight rows at a time: one by one, each behind the lookup of its request's
+// stands there must not look like a large logit. Four rows at a time: one by one, each behind the lookup of its request's
 // length, 128 rows took a warp 10600 cycles.
 template <int D, int STEP, class Dst>
 __device__ __forceinline__ void pf_copy_q(const PrefixArgs &a, PfQRows &at, int r0, int rows, int end, bool padded, Dst dst, int ch) {
-    for (int r = r0; r < end; r += 8 * STEP) {
-        int row[8];
-        bool in[8];
+    for (int r = r0; r < end; r += 4 * STEP) {
+        int row[4];
+        bool in[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
             row[j] = at.row;
             in[j] = r + j * STEP < rows && (!padded || a.own_len[at.request] >= 0);
             if (r + j * STEP < end) at.advance(STEP);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
             if (r + j * STEP < end)
                 cp_async16_u32(dst(r + j * STEP), in[j] ? a.q + (int64_t)row[j] * D + ch * 8 : a.q, in[j] ? 16 : 0);
     }

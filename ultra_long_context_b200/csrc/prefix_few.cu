@@ -502,17 +502,14 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                     fw_bar(bid);
                     load_off();
 #pragma unroll
-                    for (int c = 0; c < H; c += 8) {  // (the columns behind are the other warpgroup's)
-                        if (c >= rows) break;
+                    for (int i = 0; i < H; ++i) l[i] *= s_fac[i];
+#pragma unroll 1
+                    for (int c = 0; t > 0 && c < rows; c += 8) {  // (the columns behind are the other warpgroup's)
                         float o[8];
-                        if (t > 0) tc::tmem_ld8(tO + c, o);
+                        tc::tmem_ld8(tO + c, o);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float f = s_fac[c + i];
-                            l[c + i] *= f;
-                            o[i] *= f;
-                        }
-                        if (t > 0) fw_st<8>(tO + c, o);
+                        for (int i = 0; i < 8; ++i) o[i] *= s_fac[c + i];
+                        fw_st<8>(tO + c, o);
                     }
                     probs(t, tS, std::true_type{}, flags);
                 }

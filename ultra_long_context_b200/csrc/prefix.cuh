@@ -223,47 +223,27 @@ struct PfWalk {
     }
 };
 
-// The rows of a segment in q / out, walked upwards (a division per row made the copy of 256 rows take 20 us).
-struct PfQRows {
-    int request, row, rem, wrap, jump;  // of the row at hand; its place among its request's; where the next's begin, and how far
-    __device__ PfQRows(const PfSeg &s, const PfDims &d, int Hkv, int rr) {  // rows stay below 2^31 / D
-        const int r = s.r0 + rr;
-        request = s.b < 0 ? r / d.Ro : s.b;
-        rem = s.b < 0 ? r - request * d.Ro : r;
-        row = (request * Hkv + s.h) * d.Ro + rem;
-        wrap = s.b < 0 ? d.Ro : INT32_MAX;
-        jump = (Hkv - 1) * d.Ro;
-    }
-    __device__ void advance(int by) {
-        row += by;
-        rem += by;
-        while (rem >= wrap) {
-            rem -= wrap;
-            row += jump;
-            ++request;
-        }
-    }
-};
-
-// Copies a segment's q rows r0, r0 + STEP, .. below `end` to dst(row) by cp.async, the 16 bytes `ch` of each; zeros for the
-// rows from `rows` on, which are nobody's, and for the empty rows of a padded batch (where `padded` asks for it): whatever
-// stands there must not look like a large logit. Four rows at a time: one by one, each behind the lookup of its request's
-// length, 128 rows took a warp 10600 cycles.
-template <int D, int STEP, class Dst>
-__device__ __forceinline__ void pf_copy_q(const PrefixArgs &a, PfQRows &at, int r0, int rows, int end, bool padded, Dst dst, int ch) {
-    for (int r = r0; r < end; r += 4 * STEP) {
-        int row[4];
-        bool in[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            row[j] = at.row;
-            in[j] = r + j * STEP < rows && (!padded || a.own_len[at.request] >= 0);
-            if (r + j * STEP < end) at.advance(STEP);
+// Copies the q rows `first` .. of a segment to dst(0, chunk), dst(1, chunk), .. below `end` by cp.async, by a whole warp; zeros for the
+// rows from `rows` on, which are nobody's, and for the empty rows of a padded batch: whatever stands there must not look
+// like a large logit. A lane looks up one row of 32 (row by row, each behind its request's length, 128 rows took a
+// warp 10600 cycles).
+template <int D, class Dst>
+__device__ __forceinline__ void pf_copy_q(const PrefixArgs &a, const PfDims &d, const PfSeg &s, int first, int rows, int end, Dst dst) {
+    constexpr int CPR = D / 8, RPW = 32 / CPR;  // 16-byte chunks per row, rows per warp-wide copy
+    const int lane = threadIdx.x & 31, rsub = lane / CPR, ch = lane % CPR;
+    for (int r0 = 0; r0 < end; r0 += 32) {
+        const int r = s.r0 + first + r0 + lane;
+        int row = -1;  // rows stay below 2^31 / D
+        if (r0 + lane < rows) {
+            const int request = s.b < 0 ? r / d.Ro : s.b, rem = s.b < 0 ? r - request * d.Ro : r;
+            if (s.b >= 0 || a.own_len[request] >= 0) row = (request * a.Hkv + s.h) * d.Ro + rem;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (r + j * STEP < end)
-                cp_async16_u32(dst(r + j * STEP), in[j] ? a.q + (int64_t)row[j] * D + ch * 8 : a.q, in[j] ? 16 : 0);
+        for (int j = 0; j < CPR; ++j) {
+            const int rr = j * RPW + rsub, from = __shfl_sync(0xffffffffu, row, rr);
+            if (r0 + rr < end)
+                cp_async16_u32(dst(r0 + rr, ch), from >= 0 ? a.q + (int64_t)from * D + ch * 8 : a.q, from >= 0 ? 16 : 0);
+        }
     }
 }
 

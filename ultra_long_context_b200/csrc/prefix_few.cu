@@ -241,8 +241,6 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         for (int i = max(0, n - VS); i < n; ++i) pf_wait(bar(SM::kVFull + i % VS), (uint32_t)(i / VS) & 1u);
     } else if (warp == kFwQWarp) {
         // ================= Q rows =================
-        constexpr int CPR = D / 8, RPW = 32 / CPR;  // 16-byte chunks per row, rows per warp-wide copy
-        const int rsub = lane / CPR, ch = lane % CPR;
         PfNote g;
         while (true) {
             const int q = seg_no & 1;
@@ -252,9 +250,8 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
             ok = pf_wait(bar(SM::kQEmpty + q), (use & 1u) ^ 1u);
             if (!ok) break;
             const uint32_t dst = sb + SM::Q + q * SM::QB;
-            PfQRows at(g.s, d, a.Hkv, rsub);
-            pf_copy_q<D, RPW>(a, at, rsub, g.s.nr, (g.s.nr + 15) / 16 * 16, g.s.b < 0,
-                              [&](int r) { return dst + (ch >> 3) * (NR * 128) + tc::sw128(r, ch & 7); }, ch);
+            pf_copy_q<D>(a, d, g.s, 0, g.s.nr, (g.s.nr + 15) / 16 * 16,
+                         [&](int r, int ch) { return dst + (ch >> 3) * (NR * 128) + tc::sw128(r, ch & 7); });
             pf_cp_async_arrive(bar(SM::kQFull + q));  // fires when this thread's copies have landed
         }
         cp_async_commit();

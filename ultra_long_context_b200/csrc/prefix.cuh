@@ -55,17 +55,18 @@ struct PfDims {
     int Ro, Rgo;           // own rows per request and key head, in groups of kPfFewRows
     int strideP, strideO;  // rows of one segment's partials (in the wide kernel, two streams may each keep one of the same rows)
     int max_items, max_slots, blocks;  // blocks: of 32 requests
-    // Which kernel ends the prefix sooner? A tile of 128 keys takes the few-rows kernel 0.92 us (D = 128; 0.75 with D = 64)
-    // for 64 rows, the wide one 2.3 us (1.8) for 256 and 1.5 us (1.0) for up to 128, and that is a launch of its own with
-    // larger tiles to fill: 20 us (12). Both sides measured, D = 128: 512 rows x 4 heads over 14208 / 28416 / 56832 tokens
-    // 38 / 67 / 111 us and 53 / 66 / 92, 1024 rows 65 / 110 / 209 and 73 / 100 / 150, 128 rows x 8 heads over 59136 68 and
-    // 71; D = 64: 512 rows 35 / 56 / 90 and 40 / 50 / 70. The tiles are those of the table, since the length is not known here.
+    // Which kernel ends the prefix sooner? A tile of 128 keys takes the few-rows kernel 0.94 us (D = 128; 0.77 with D = 64)
+    // for 64 rows, the wide one 2.05 us (1.65) for 256 and 1.4 us (1.07) for up to 128, and that is a launch of its own with
+    // larger tiles to fill: 15 us (8). Both sides measured, D = 128: 512 rows x 4 heads over 14208 / 28416 / 56832 tokens
+    // 38 / 61 / 110 us and 43 / 56 / 81, 1024 rows 66 / 110 / 208 and 63 / 89 / 135, 128 rows x 8 heads over 28416 / 59136
+    // 42 / 67 and 48 / 66; D = 64: 512 rows 36 / 54 / 93 and 37 / 46 / 65. The tiles are those of the table, since the
+    // length is not known here.
     static bool pf_wide(int Rp, int Hkv, int D, int tiles) {
         const bool d128 = D == 128;
         const double per_sm = (double)Hkv * tiles / kPfCtas;
-        const double few = per_sm * ((Rp + kPfFewRows - 1) / kPfFewRows) * (d128 ? 0.92 : 0.75);
-        const double wide_tile = Rp > kPfTile ? (d128 ? 2.3 : 1.8) : (d128 ? 1.5 : 1.0);
-        const double wide = (d128 ? 20.0 : 12.0) + per_sm * ((Rp + kPfWideRows - 1) / kPfWideRows) * wide_tile;
+        const double few = per_sm * ((Rp + kPfFewRows - 1) / kPfFewRows) * (d128 ? 0.94 : 0.77);
+        const double wide_tile = Rp > kPfTile ? (d128 ? 2.05 : 1.65) : (d128 ? 1.4 : 1.07);
+        const double wide = (d128 ? 15.0 : 8.0) + per_sm * ((Rp + kPfWideRows - 1) / kPfWideRows) * wide_tile;
         return Rp > kPfFewRows && wide < few;
     }
     PfDims(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages) {

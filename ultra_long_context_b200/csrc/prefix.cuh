@@ -21,7 +21,8 @@ constexpr int kPfFewRows = 64;    // rows per segment at most: in the few-rows k
 constexpr int kPfWideRows = 256;  // in the wide kernel
 constexpr int kPfCtas = 148;      // at most: one per SM; the workspace is sized for it
 constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per head and row group)
-// Costs in half tiles: a tile, and what a segment's start and end take beside its tiles
+// Costs in half tiles: a tile, and what a segment's start and end take beside its tiles, some 5000 cycles (24 requests x 4
+// tokens over 20K: 35.7 us; with 3 and 4 for the two 36.2, with 3 and 5 40.8; other shapes within 1%)
 constexpr int kPfTileCost = 2, kPfPrefixCost = 5, kPfOwnCost = 5;
 
 // a / b for a >= 0, b > 0, in 32 bits where they suffice (a 64-bit division takes several times as long)
@@ -356,7 +357,7 @@ __device__ __forceinline__ void pf_prefetch_tmap(const CUtensorMap *m) {
 
 // A bounded wait of a whole warp, with one answer for all lanes: the warp is converged behind it, which the
 // aligned tcgen05 loads and stores that follow need. All lanes wait: where one did it for the others the warp was not put to
-// sleep, and twelve such warps took the issue slots of the softmax (every kernel 1.3 to 1.9 times slower). A probe
+// sleep, and twelve such warps took the issue slots of the softmax (every case 1.3 to 1.9 times slower). A probe
 // may suspend the thread for tens of microseconds, so 2^15 of them are seconds.
 __device__ __forceinline__ bool pf_wait(uint32_t mbar, uint32_t parity) {
     return __all_sync(0xffffffffu, tc::mbar_wait_n(mbar, parity & 1u, 1u << 15)) != 0;
@@ -368,9 +369,6 @@ __device__ __forceinline__ bool pf_wait_lane(uint32_t mbar, uint32_t parity) {
 __device__ __forceinline__ void pf_arrive(uint32_t mbar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(mbar);
-}
-__device__ __forceinline__ bool pf_done(uint32_t mbar, uint32_t parity) {
-    return __all_sync(0xffffffffu, tc::mbar_test(mbar, parity & 1u)) != 0;
 }
 __device__ __forceinline__ void pf_cp_async_arrive(uint32_t mbar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(mbar) : "memory");

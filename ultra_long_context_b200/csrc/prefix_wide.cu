@@ -6,6 +6,11 @@
 // logit of the first key that the row sees in the segment, so no maximum is taken at all; a tile whose row sum exceeds
 // 2^70 moves it (rarely): the pair of warps then reduces the maximum, rescales O in TMEM and does the tile again.
 //
+// Measured, per tile of 128 keys and 256 rows on an SM: D = 128 1.89 us out of L2 (1.32 PFLOP/s over 148 SMs), 2.43 us out of
+// HBM; D = 64 1.50 and 1.56. Tensor cores and exponentials are busy half of that time each: a stream's chain bounds it,
+// its products S and O wait for one another through four barriers, since P stands in the columns of S. (A third stream
+// would need 256 more columns of TMEM, P in shared memory 64 KB that the operands hold.) Start 9 us, end 4 us.
+//
 // Persistent, warp-specialised kernel, one CTA per SM:
 //   warps 0-7, 8-15 softmax of two STREAMS: two threads per row, one for each page of the tile (a thread's 64
 //               logits stay in registers). The work is a sequence of items that go to the streams in turn: a

@@ -329,8 +329,9 @@ def test_prefix_decode_batch_of_8192():
     rng = np.random.default_rng(4)
     own = rng.integers(-1, 3, 8192)
     own[[0, 4000, 8191]] = (500, 130, 64)
-    q, Kp, Vp, pre, prefix, table, own, scale = decode_case(27, B=8192, H=1, Hkv=1, Tq=1, D=64, prefix=200, own=own, poison=False)
-    check_decode(q, Kp, Vp, pre, prefix, table, own, scale)
+    case = decode_case(27, B=8192, H=1, Hkv=1, Tq=1, D=64, prefix=200, own=own, poison=False)
+    check_decode(*case)
+    check_decode(*case, room=WIDE)
 
 
 def test_prefix_decode_pools_past_two_to_the_31_elements():

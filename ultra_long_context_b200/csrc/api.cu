@@ -563,7 +563,9 @@ hsa_status hsa_backward_varlen(const hsa_bf16 *Qs, const hsa_bf16 *Q, const hsa_
 
 // ---- paged cache ----
 
-// Pages are one chunk; the batch bound is that of the kernels' shared-memory tables.
+static_assert(HSA_PAGED_MAX_BATCH == hsa::kPagedMaxBatch, "the bound that include/hsa.h names");
+
+// Pages are one chunk.
 static hsa_status check_paged(int Hkv, int D, int page, int num_pages) {
     if (Hkv < 1) return fail(HSA_ERR_INVALID_ARG, "Hkv must be >= 1 (got %d)", Hkv);
     if (D < 1) return fail(HSA_ERR_INVALID_ARG, "D must be >= 1 (got %d)", D);

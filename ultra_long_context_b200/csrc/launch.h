@@ -176,7 +176,8 @@ cudaError_t launch_varlen_rows(const void *src, void *dst, const int32_t *cu, in
                                bool pack, bool fill_pad, uint32_t fill, cudaStream_t s);
 
 // The current device's number of SMs, and a kernel's dynamic shared memory limit raised to `bytes`, asked of the
-// driver once per device (and kernel): a serving step's small launches are bound by the host.
+// driver once per device (and kernel): a serving step's small launches are bound by the host. `bytes` is the most that the
+// kernel ever takes, the same in every call: of two threads with different ones, one would lower the other's limit.
 int sm_count();
 template <auto Kern>
 cudaError_t allow_smem(size_t bytes) {
@@ -192,6 +193,7 @@ cudaError_t allow_smem(size_t bytes) {
 }
 
 // Paged cache (page.cu). Pages of kChunk tokens; arguments as in include/hsa.h.
+constexpr int kPagedMaxBatch = 8192;  // the kernels' tables of requests stand in shared memory
 struct PagePlanArgs {
     const int64_t *cache_len;
     const int32_t *new_len;

@@ -234,7 +234,7 @@ size_t page_plan_smem(int B) { return (size_t)B * (sizeof(int64_t) + 4 * sizeof(
 
 cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t s) {
     const size_t smem = page_plan_smem(a.B);
-    cudaError_t e = allow_smem<page_plan_kernel>(smem);
+    cudaError_t e = allow_smem<page_plan_kernel>(page_plan_smem(kPagedMaxBatch));
     if (e != cudaSuccess) return e;
     // a thread to each token and request up to one block of 1024, then more blocks
     const int64_t work = (int64_t)a.max_tokens + a.B;

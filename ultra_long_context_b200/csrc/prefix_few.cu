@@ -69,8 +69,8 @@ struct FwSmem {
     static constexpr size_t dyn(int blocks) { return BCUM + 4 * ((size_t)blocks + 1) + 1024; }  // slack: 1 KB alignment
     static constexpr uint32_t S_COL = 0, O_COL = NB * 64, TMEM_COLS = NB == 4 ? 512 : 256;
 };
-static_assert(FwSmem<128, 64>::dyn(256) <= 227 * 1024 && FwSmem<128, 32>::dyn(256) <= 227 * 1024 &&
-                  FwSmem<64, 64>::dyn(256) <= 227 * 1024,
+static_assert(FwSmem<128, 64>::dyn(kPagedMaxBatch / 32) <= 227 * 1024 && FwSmem<128, 32>::dyn(kPagedMaxBatch / 32) <= 227 * 1024 &&
+                  FwSmem<64, 64>::dyn(kPagedMaxBatch / 32) <= 227 * 1024,
               "shared memory budget");
 
 // Named barrier of a warpgroup that also ORs a predicate.
@@ -579,7 +579,7 @@ static cudaError_t launch_few(const PrefixArgs &a, const PfDims &d, const PfWork
     if (!make_tmap_bf16(&tk, a.Kp, rows, D, kChunk) || !make_tmap_bf16(&tv, a.Vp, rows, D, kChunk))
         return cudaErrorInvalidValue;
     const size_t smem = FwSmem<D, NR>::dyn(d.blocks);
-    cudaError_t e = allow_smem<prefix_few_kernel<D, NR>>(smem);
+    cudaError_t e = allow_smem<prefix_few_kernel<D, NR>>(FwSmem<D, NR>::dyn(kPagedMaxBatch / 32));
     if (e != cudaSuccess) return e;
     HSA_PROF("prefix_few", s);
     return launch_pdl(prefix_few_kernel<D, NR>, dim3(ctas), dim3(kFwThreads), smem, s, a, d, w, tk, tv);

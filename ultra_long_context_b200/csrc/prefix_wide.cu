@@ -57,7 +57,7 @@ struct PfSmem {
     static constexpr size_t dyn(int blocks) { return BCUM + 4 * ((size_t)blocks + 1) + 1024; }  // slack: 1 KB alignment
     static constexpr uint32_t S_COL = 0, O_COL = 2 * kPfTile, TMEM_COLS = 512;
 };
-static_assert(PfSmem<128>::dyn(256) <= 227 * 1024 && PfSmem<64>::dyn(256) <= 227 * 1024, "shared memory budget");
+static_assert(PfSmem<128>::dyn(kPagedMaxBatch / 32) <= 227 * 1024 && PfSmem<64>::dyn(kPagedMaxBatch / 32) <= 227 * 1024, "shared memory budget");
 
 // 2^y for two numbers, by the pipe of the fused multiply-adds: 2^n 2^f with n = round(y), by which a sum with 1.5 2^23 leaves
 // the integer in its last bits, and |f| <= 1/2. The polynomial interpolates 2^f at the six Chebyshev nodes of the
@@ -535,7 +535,7 @@ static cudaError_t launch_wide(const PrefixArgs &a, const PfDims &d, const PfWor
     if (!make_tmap_bf16(&tk, a.Kp, rows, D, kChunk) || !make_tmap_bf16(&tv, a.Vp, rows, D, kChunk))
         return cudaErrorInvalidValue;
     const size_t smem = PfSmem<D>::dyn(d.blocks);
-    cudaError_t e = allow_smem<prefix_wide_kernel<D>>(smem);
+    cudaError_t e = allow_smem<prefix_wide_kernel<D>>(PfSmem<D>::dyn(kPagedMaxBatch / 32));
     if (e != cudaSuccess) return e;
     HSA_PROF("prefix_wide", s);
     return launch_pdl(prefix_wide_kernel<D>, dim3(ctas), dim3(kPfThreads), smem, s, a, d, w, tk, tv);

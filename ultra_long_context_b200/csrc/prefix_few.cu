@@ -147,7 +147,11 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     tc::fence_after();
     const uint32_t tmem = *reinterpret_cast<uint32_t *>(s + SM::MISC);
     if (!d.wide) pdl_wait();  // what precedes the call in its stream is visible from here on
-    pf_schedule<kFwThreads>(a, d, !d.wide, true, s_plan, s_bcum);
+    int64_t plen = 0;
+    if (warp == kFwQWarp && !d.wide && a.max_prefix_pages > 0) plen = pf_clamp_len(a.prefix_len[0], a.max_prefix_pages);
+    pf_schedule<kFwThreads>(a, d, !d.wide, true, s_plan, s_bcum, [&](int wp) {
+        if (wp == kFwQWarp && plen > 0) pf_prefetch_first<D>(a, d, plen, (int)gridDim.x);
+    });
     pf_publish<kFwThreads>(d, !d.wide, true, s_plan, s_bcum, w);
     bool ok = true;
 

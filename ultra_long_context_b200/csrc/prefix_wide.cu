@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     const uint32_t tmem = *reinterpret_cast<uint32_t *>(s + SM::TMEM);
     pdl_wait();  // what precedes the call in its stream is visible from here on
     pdl_launch_dependents();  // the few-rows kernel may come in as SMs fall free; the join waits for this grid's end
-    pf_schedule<kPfThreads>(a, d, true, false, s_plan, s_bcum);
+    pf_schedule<kPfThreads>(a, d, true, false, s_plan, s_bcum, [](int) {});
     pf_publish<kPfThreads>(d, true, false, s_plan, s_bcum, w);
     bool ok = true;
 

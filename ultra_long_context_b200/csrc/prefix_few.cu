@@ -7,8 +7,8 @@
 //   O^T += V^T P^T (D x N, fp32 in TMEM; thread = dim)
 // The reference m of a row need not be its maximum: the final quotient cancels it, and P (bf16) and the fp32 sums keep
 // their relative precision as long as nothing leaves their range. So m is the logit of the first key that the row sees
-// in the segment, and moves only when a later one exceeds it by more than 2^64 (sums of 2^64 over 2^30 keys, times
-// V, stay far below 2^127; what is 2^126 below m is less than 2^-126 of the sum, which is at least 1). Then the
+// in the segment, and moves only when a later one exceeds it by more than 2^64 (a term stays below 2^69, its sum over 2^30
+// keys, times V below 2^28, below 2^127; what is 2^126 below m is less than 2^-126 of the sum, which is at least 1). Then the
 // warpgroup reduces the maxima over the keys, rescales O^T in TMEM and does the tile again; every other tile costs a
 // thread one exponential per row and one barrier with a vote. Row sums stay per thread until the segment ends.
 //

@@ -6,6 +6,7 @@ name is called on the current torch stream. Every step of HSA runs in the CUDA l
 no fallback. If the library is missing or cannot be loaded, the first call raises.
 """
 import ctypes
+import functools
 import math
 import os
 
@@ -519,6 +520,9 @@ def hsa_prefix_decode_workspace_size(B, H, Hkv, D, max_prefix_pages, max_pages, 
     return lib().hsa_prefix_decode_workspace_size(B, H, Hkv, Tq, D, max_prefix_pages, max_pages)
 
 
+_prefix_workspace_size = functools.lru_cache(maxsize=1024)(hsa_prefix_decode_workspace_size)  # of the sizes alone
+
+
 def hsa_prefix_decode(q, Kp, Vp, prefix_table, prefix_len, block_table, own_len, scale=0.0, out=None, lse=None,
                       workspace=None, stream=None):
     """Softmax attention of a decode batch whose requests share a prefix, the prefix computed once for all.
@@ -549,12 +553,12 @@ def hsa_prefix_decode(q, Kp, Vp, prefix_table, prefix_len, block_table, own_len,
     else:
         _fits(out, "out", _BF16, shape, dev)
     if lse is None:
-        lse = torch.empty(shape[:-1], dtype=_F32, device=dev)
+        lse = q.new_empty(shape[:-1], dtype=_F32)
     else:
         _fits(lse, "lse", _F32, shape[:-1], dev)
     if workspace is None:
-        need = hsa_prefix_decode_workspace_size(B, H, Hkv, D, npre, width, Tq)
-        workspace = torch.empty(need + 256, dtype=torch.uint8, device=dev)  # + 256: an aligned window always fits
+        # + 256: an aligned window always fits
+        workspace = q.new_empty(_prefix_workspace_size(B, H, Hkv, D, npre, width, Tq) + 256, dtype=torch.uint8)
     ws = workspace.data_ptr()
     pad = -ws % 256
     st = lib().hsa_prefix_decode(q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), pages, prefix_table.data_ptr(), npre,

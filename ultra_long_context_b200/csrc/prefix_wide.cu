@@ -9,7 +9,7 @@
 // Measured, per tile of 128 keys and 256 rows on an SM: D = 128 1.89 us out of L2 (1.32 PFLOP/s over 148 SMs), 2.43 us out of
 // HBM; D = 64 1.50 and 1.56. Tensor cores and exponentials are busy half of that time each: a stream's chain bounds it,
 // its products S and O wait for one another through four barriers, since P stands in the columns of S. (A third stream
-// would need 256 more columns of TMEM, P in shared memory 64 KB that the operands hold.) Start 9 us, end 4 us.
+// would need 256 more columns of TMEM, P in shared memory 64 KB that the operands hold.) Start 7 us (schedule 2.4, 128 query rows 2.5 each), end 5 us.
 //
 // Persistent, warp-specialised kernel, one CTA per SM:
 //   warps 0-7, 8-15 softmax of two STREAMS: two threads per row, one for each page of the tile (a thread's 64

@@ -1,0 +1,42 @@
+"""What the paged calls' binding refuses before the library is called; the library's entries are stubs here that note a call."""
+import types
+
+import pytest
+import torch
+
+from ultra_long_context_b200 import hsa
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    made = []
+
+    def entry(name):
+        return lambda *a: made.append((name, a)) or 0
+
+    names = ("hsa_page_plan", "hsa_page_append", "hsa_prefix_decode")
+    monkeypatch.setattr(hsa, "_lib", types.SimpleNamespace(**{n: entry(n) for n in names}))
+    monkeypatch.setattr(hsa, "_stream_of", lambda dev, stream: 0)
+    return made
+
+
+def decode_args(B=2, H=2, Hkv=1, D=64, pages=3, npre=1, width=2, device="cpu"):
+    pool = torch.zeros(2, pages, Hkv, 64, D, dtype=BF16, device=device)
+    return (torch.zeros(B, H, D, dtype=BF16, device=device), pool[0], pool[1], torch.zeros(npre, dtype=torch.int32, device=device),
+            torch.zeros(1, dtype=torch.int64, device=device), torch.zeros(B, width, dtype=torch.int32, device=device),
+            torch.zeros(B, dtype=torch.int64, device=device))
+
+
+@pytest.mark.parametrize("workspace,error", [
+    (torch.empty(1 << 16, dtype=torch.uint8, device="meta"), ValueError),     # another device
+    (torch.empty(1 << 16, 2, dtype=torch.uint8)[:, 0], ValueError),            # a view with gaps
+    (1 << 20, TypeError),
+])
+def test_prefix_decode_refuses_a_workspace_that_it_cannot_use(calls, workspace, error):
+    with pytest.raises(error, match="workspace"):
+        hsa.hsa_prefix_decode(*decode_args(), workspace=workspace)
+    assert not calls
+    hsa.hsa_prefix_decode(*decode_args(), workspace=torch.empty(1 << 16, dtype=torch.uint8))
+    assert [n for n, _ in calls] == ["hsa_prefix_decode"]

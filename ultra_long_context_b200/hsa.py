@@ -559,6 +559,10 @@ def hsa_prefix_decode(q, Kp, Vp, prefix_table, prefix_len, block_table, own_len,
     if workspace is None:
         # + 256: an aligned window always fits
         workspace = q.new_empty(_prefix_workspace_size(B, H, Hkv, D, npre, width, Tq) + 256, dtype=torch.uint8)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    elif workspace.device != dev or not workspace.is_contiguous():  # the kernels write all of its bytes
+        raise ValueError(f"workspace must be contiguous and on {dev}, got one on {workspace.device}")
     ws = workspace.data_ptr()
     pad = -ws % 256
     st = lib().hsa_prefix_decode(q.data_ptr(), Kp.data_ptr(), Vp.data_ptr(), pages, prefix_table.data_ptr(), npre,

@@ -320,7 +320,8 @@ hsa_status hsa_page_append(const hsa_bf16 *K, int64_t k_stride, const hsa_bf16 *
  * too, and their values in V below 2^28 (the fp32 sums carry factors of up to 2^69 over up to 2^30 keys).
  * max_prefix_pages or max_pages may be 0 (its table may then be NULL). H / Hkv * Tq <= 1024, 1 <= Tq <= 64,
  * tables of less than 2^24 pages, B * max_pages < 2^30.
- * Each prefix page is read once for up to 64 or 256 rows (request, query head, token) of its key head. */
+ * Each prefix page is read once for up to 64 or 256 rows (request, query head, token) of its key head.
+ * The workspace's size is 0 for sizes that the call refuses. */
 size_t hsa_prefix_decode_workspace_size(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages, int max_pages);
 
 hsa_status hsa_prefix_decode(const hsa_bf16 *q, const hsa_bf16 *Kp, const hsa_bf16 *Vp, int num_pages,

@@ -1,4 +1,6 @@
 """What the paged calls' binding refuses before the library is called; the library's entries are stubs here that note a call."""
+import subprocess
+import sys
 import types
 
 import pytest
@@ -40,3 +42,14 @@ def test_prefix_decode_refuses_a_workspace_that_it_cannot_use(calls, workspace, 
     assert not calls
     hsa.hsa_prefix_decode(*decode_args(), workspace=torch.empty(1 << 16, dtype=torch.uint8))
     assert [n for n, _ in calls] == ["hsa_prefix_decode"]
+
+
+@pytest.mark.parametrize("args", [
+    (8192, 1 << 27, 1 << 17, 128, 8, 8),         # 2^32 row groups
+    (8192, 1 << 17, 1 << 17, 128, 8, 8), (64, 8, 8, 128, 1 << 24, 8), (1, 8, 8, 128, 8, 1 << 24), (128, 8, 8, 128, 8, 1 << 23),
+])
+def test_prefix_decode_workspace_size_is_zero_for_sizes_that_the_call_refuses(args):
+    """In a process of its own: a division by zero would end it."""
+    code = f"from ultra_long_context_b200 import hsa; print(hsa.hsa_prefix_decode_workspace_size(*{args}))"
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert run.returncode == 0 and run.stdout.strip() == "0", (run.returncode, run.stdout)

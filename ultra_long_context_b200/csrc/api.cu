@@ -642,6 +642,10 @@ size_t hsa_prefix_decode_workspace_size(int B, int H, int Hkv, int Tq, int D, in
     if (B < 1 || B > HSA_PAGED_MAX_BATCH || H < 1 || Hkv < 1 || H % Hkv != 0 || Tq < 1 || Tq > 64 ||
         (int64_t)(H / Hkv) * Tq > 1024 || D < 1 || max_prefix_pages < 0 || max_pages < 0)
         return 0;
+    // sizes that the call refuses, too: the layout counts rows and segments in 32 bits
+    if (max_prefix_pages >= (1 << 24) || max_pages >= (1 << 24) || (double)B * max_pages >= 1073741824.0 ||
+        (double)B * H * Tq * D >= 2147483647.0)
+        return 0;
     return hsa::prefix_workspace(B, H, Hkv, Tq, D, max_prefix_pages, max_pages);
 }
 

@@ -1,0 +1,317 @@
+"""The shared-prefix decode over long runs: segments of more than 32 tiles of keys, whose partial sums, references and rings
+of buffers go round, in both kernels and in the launch order that a user's call has. The plain form here runs in fp64 on the GPU,
+and page ids repeat in the prefix's table, so that a long prefix needs a small pool only."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged
+from ultra_long_context_b200 import hsa
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF16 = torch.bfloat16
+TILE = 128   # keys that the kernels take at a time
+
+
+def _tokens(pool, ids, n, h):
+    """The first n tokens of one key head in the pages `ids` [..., pages], fp64, and whether they are there."""
+    ok = (ids >= 0) & (ids < pool.shape[0])
+    rows = pool[torch.where(ok, ids, 0), h].double().flatten(-3, -2)
+    there = ok.repeat_interleave(64, -1) & (torch.arange(rows.shape[-2], device=DEV) < n)
+    return torch.where(there[..., None], rows, 0.0), there
+
+
+def plain_decode(q, Kp, Vp, pre, P, table, own, run=0):
+    """Row by row over the visible tokens, fp64. `run` > 0: also the share of (row, run of `run` prefix tiles) in which a tile
+    after the first holds a logit that is over the one of the run's first key by more than 2^64."""
+    B, H, Tq, D = q.shape
+    Hkv = Kp.shape[1]
+    G = H // Hkv
+    pre, table, own = pre.long(), table.long(), own.clamp(max=table.shape[1] * 64)
+    P = min(max(P, 0), 64 * pre.numel())
+    pre = pre[:-(-P // 64)]
+    scale = D ** -0.5
+    res = {k: torch.zeros((B, H, Tq) + ((D,) if k in ("out", "mean_abs") else ()), dtype=torch.float64, device=DEV)
+           for k in ("out", "mean_abs", "lse", "reach", "keys")}
+    moved = []
+    last = P + own[:, None] - Tq + torch.arange(Tq, device=DEV)                  # [B, Tq]: the last token that a row sees
+    last = torch.where(own[:, None] < 0, -1, last)
+    step = max(1, (1 << 27) // (G * Tq * max(1, P)))                              # requests at a time
+    for h in range(Hkv):
+        kp, there = _tokens(Kp, pre, P, h)
+        vp = _tokens(Vp, pre, P, h)[0]
+        for b in range(0, B, step):
+            e = min(B, b + step)
+            rows = q[b:e, h * G:(h + 1) * G].double()                             # [b, G, Tq, D]
+            ko, owned = _tokens(Kp, table[b:e], own[b:e, None], h)
+            vo = _tokens(Vp, table[b:e], own[b:e, None], h)[0]
+            see_p = there & (torch.arange(kp.shape[0], device=DEV) <= last[b:e, None, :, None])
+            see_o = owned[:, None, None] & (P + torch.arange(ko.shape[1], device=DEV) <= last[b:e, None, :, None])
+            sp = scale * rows @ kp.T
+            so = scale * rows @ ko.transpose(1, 2)[:, None]
+            if run:
+                first = sp[..., ::run * TILE]
+                top = torch.where(see_p, sp, -math.inf)
+                top[..., torch.arange(top.shape[-1], device=DEV) // TILE % run == 0] = -math.inf
+                pad = -top.shape[-1] % (run * TILE)
+                top = torch.nn.functional.pad(top, (0, pad), value=-math.inf).unflatten(-1, (-1, run * TILE)).amax(-1)
+                moved.append((((top - first) * math.log2(math.e) > 64)).double().mean())
+            s = torch.cat([torch.where(see_p, sp, -math.inf), torch.where(see_o, so, -math.inf)], -1)
+            lse = torch.logsumexp(s, -1)
+            w = torch.exp(s - torch.where(lse == -math.inf, 0.0, lse)[..., None])
+            wp, wo = w[..., :kp.shape[0]], w[..., kp.shape[0]:]
+            at = np.s_[b:e, h * G:(h + 1) * G]
+            res["out"][at] = wp @ vp + wo @ vo[:, None]
+            res["mean_abs"][at] = wp @ vp.abs() + wo @ vo.abs()[:, None]
+            res["lse"][at] = lse
+            far = torch.cat([torch.where(see_p, rows.abs() @ kp.abs().T, 0.0), torch.where(see_o, rows.abs() @ ko.abs().transpose(1, 2)[:, None], 0.0)], -1)
+            res["reach"][at] = scale * far.amax(-1)
+            res["keys"][at] = (see_p.expand_as(sp).sum(-1) + see_o.expand_as(so).sum(-1)).double()
+            del s, w, wp, wo, far, sp, so, see_p
+    ref = {k: v.cpu().numpy() for k, v in res.items()}
+    ref["moved"] = float(torch.stack(moved).mean()) if moved else 0.0
+    return ref
+
+
+def run_case(seed, B, H, Hkv, D, prefix, own, Tq=1, shape="flat", pages=48, bad=()):
+    """A prefix of `pages` pages in an order that repeats them. shape: flat (normal logits); up and down (logits that climb, or
+    fall, by 2^160 over 20 tiles and jump back, for a third of the rows; that do the opposite for another third).
+    bad: places of the prefix's table that hold no page."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    cpu = torch.Generator().manual_seed(seed)
+    own = torch.as_tensor(own).expand(B).clone()
+    held = (own.clamp(min=0) + 63) // 64
+    npre, width = (prefix + 63) // 64, int(held.max()) + 1
+    total = pages + int(held.sum()) + 2
+    pool = torch.randn(2, total, Hkv, 64, D, generator=g, device=DEV)
+    q = torch.randn(B, H, Tq, D, generator=g, device=DEV)
+    table = torch.full((B, width), -1, dtype=torch.int32)
+    has = torch.arange(width)[None] < held[:, None]
+    table[has] = (pages + 1 + torch.arange(int(held.sum()))).to(torch.int32)
+    if shape == "flat":
+        pre = torch.randint(0, pages, (npre,), generator=cpu)
+    else:
+        # the logit of a row with sign 1 in page p: 2^160 in all, by the first column alone, beside half of the noise
+        assert pages >= 40
+        level = torch.arange(40, device=DEV) / 39 * 160 / math.log2(math.e)
+        pool[0, :40] *= 0.5
+        pool[0, :40, :, :, 0] = (level * D ** 0.5 / 8)[:, None, None]
+        q[..., 0] = 8.0 * (torch.arange(B * H * Tq, device=DEV).view(B, H, Tq) % 3 - 1)
+        pre = torch.arange(npre) % 40
+        if shape == "down":
+            pre = 39 - pre
+    last = pages    # the prefix's last page is one of its own: what follows its tokens is NaN
+    if prefix % 64:
+        pre[-1] = last
+        pool[:, last, :, prefix % 64:] = math.nan
+    for b in range(B):
+        if own[b] > 0 and own[b] % 64:
+            pool[:, int(table[b, held[b] - 1]), :, int(own[b]) % 64:] = math.nan
+    for k, p in enumerate(bad):
+        pre[p] = (-1, total, 2**31 - 1, -2**31)[k % 4]
+    pool = pool.to(BF16)
+    return q.to(BF16), pool[0].contiguous(), pool[1].contiguous(), pre.to(torch.int32).to(DEV), prefix, table.to(DEV), own.to(DEV)
+
+
+def workspace(q, Kp, pre, table):
+    B, H, Tq, D = q.shape
+    n = hsa.hsa_prefix_decode_workspace_size(B, H, Kp.shape[1], D, pre.numel(), table.shape[1], Tq)
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=DEV)
+    return ws[-ws.data_ptr() % 256:]
+
+
+def division(ws):
+    """How the last call cut its prefix: (tiles, tiles per segment, segments), which stand behind the workspace's first block."""
+    _, _, tiles, run, _, items = ws[256:256 + 24].view(torch.int32).tolist()
+    return tiles, run, items
+
+
+def kernels_of(call):
+    hsa.hsa_profile_enable(True)
+    try:
+        res = call()
+        torch.cuda.synchronize()
+        return res, hsa.hsa_profile_summary()
+    finally:
+        hsa.hsa_profile_enable(False)
+
+
+def check(case, wide, room=0, min_run=33, moved=False):
+    q, Kp, Vp, pre, P, table, own = case
+    D = q.shape[-1]
+    if room:
+        pre = torch.cat([pre, torch.full((room,), -1, dtype=torch.int32, device=DEV)])
+    ws = workspace(q, Kp, pre, table)
+    plen = torch.tensor([P], device=DEV)
+
+    def call():
+        return hsa.hsa_prefix_decode(q, Kp, Vp, pre, plen, table, own, workspace=ws)
+
+    out, lse = call()     # as a user calls it, the kernels starting under one another
+    hsa.hsa_workspace_status(ws)
+    tiles, run, items = division(ws)
+    assert tiles == -(-P // TILE) and run >= min_run, (tiles, run, items)
+    again, names = kernels_of(call)
+    assert ("prefix_wide" in names) == wide, names
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    ref = plain_decode(q, Kp, Vp, pre, P, table, own, run=run if moved else 0)
+    if moved:
+        assert ref["moved"] > 0.05, ref["moved"]
+    tol, tol_lse = paged.prefix_tolerance(ref, D)
+    got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    none = ref["keys"] == 0
+    assert (got[none] == 0).all() and np.isneginf(got_lse[none]).all()
+    off = np.abs(got - ref["out"]) - tol
+    assert np.isfinite(got).all() and (off <= 0).all(), (int((off > 0).sum()), float(off.max()), np.argwhere(off > 0)[:4].tolist())
+    off = np.abs(got_lse[~none] - ref["lse"][~none]) - tol_lse[~none]
+    assert (off <= 0).all(), (int((off > 0).sum()), float(off.max()))
+    return run, items
+
+
+# Row groups of the few-rows kernel (at most 64 rows a key head, by eights over two warpgroups); 16, 32 and 64 columns.
+FEW = [dict(B=3, H=2, Hkv=2), dict(B=5, H=2, Hkv=1), dict(B=16, H=8, Hkv=8), dict(B=9, H=6, Hkv=2), dict(B=32, H=4, Hkv=4), dict(B=31, H=4, Hkv=2),
+       dict(B=64, H=2, Hkv=2), dict(B=7, H=6, Hkv=2, Tq=3)]
+# Row groups of the wide kernel: one stream an item (up to 128 rows), two, and groups that end early
+WIDE = [dict(B=65, H=2, Hkv=2), dict(B=25, H=16, Hkv=4), dict(B=128, H=2, Hkv=2), dict(B=43, H=6, Hkv=2), dict(B=64, H=16, Hkv=4),
+        dict(B=75, H=8, Hkv=2), dict(B=48, H=16, Hkv=2), dict(B=20, H=12, Hkv=2, Tq=3)]
+
+
+def long_prefix(c, D, wide):
+    """Tokens that make runs of more than 32 tiles over 148 SMs, an odd number, not whole pages."""
+    rows = c["B"] * (c["H"] // c["Hkv"]) * c.get("Tq", 1)
+    units = c["Hkv"] * (-(-rows // 256) if wide else 1)
+    return 150 // units * 37 * TILE + 61
+
+
+def own_of(c, seed):
+    own = torch.randint(0, 300, (c["B"],), generator=torch.Generator().manual_seed(seed))
+    own[::7] = 0
+    own[3::11] = -1
+    return own
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", ["flat", "up", "down"])
+@pytest.mark.parametrize("c", FEW)
+def test_few_rows_over_long_runs(c, shape, D):
+    P = long_prefix(c, D, False)
+    check(run_case(51, D=D, prefix=P, own=own_of(c, 1), shape=shape, **c), wide=False, moved=shape != "flat")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", ["flat", "up", "down"])
+@pytest.mark.parametrize("c", WIDE)
+def test_wide_batches_over_long_runs(c, shape, D):
+    P = long_prefix(c, D, True)
+    check(run_case(52, D=D, prefix=P, own=own_of(c, 2), shape=shape, **c), wide=True, room=60000, moved=shape != "flat")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", ["flat", "up"])
+@pytest.mark.parametrize("c,wide", [(FEW[2], False), (FEW[4], False), (WIDE[1], True), (WIDE[4], True), (WIDE[5], True)])
+def test_bad_pages_late_in_long_runs(c, wide, shape, D):
+    """Places without a page in every part of the runs: their first pages, the second of a tile, whole tiles, behind the 16 tiles
+    whose pages are looked up together, the last one."""
+    P = long_prefix(c, D, wide)
+    n = -(-P // 64)
+    bad = sorted({*range(0, n, 149), *range(1, n, 83), *range(66, n, 132), *range(67, n, 132), *range(34, n, 97), n - 1})
+    check(run_case(53, D=D, prefix=P, own=own_of(c, 3), shape=shape, bad=bad, **c), wide=wide, room=60000 if wide else 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", ["flat", "up", "down"])
+@pytest.mark.parametrize("B,Hkv,rows", [(80, 32, 32), (300, 64, 2)])
+def test_more_segments_than_sms(B, Hkv, rows, shape, D):
+    """Several segments one after the other on an SM, their queries and sums in turn in the same buffers: 2560 rows in groups of
+    256 (two streams a tile) and 600 (the last group 88, one stream a tile)."""
+    c = dict(B=B, H=Hkv * rows, Hkv=Hkv)
+    run, items = check(run_case(54, D=D, prefix=35 * TILE - 17, own=own_of(c, 4), shape=shape, **c), wide=True, room=60000, min_run=1)
+    assert items > 148
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("wide", [False, True])
+def test_calls_back_to_back_equal_the_plain_form(wide, D):
+    """Sixty calls without a pause, over queries and lengths that the stream changes between them; each of the answers as when it
+    is computed alone, and as the plain form has it."""
+    c = WIDE[5] if wide else FEW[4]
+    q, Kp, Vp, pre, P, table, own = run_case(55, D=D, prefix=9000, own=own_of(c, 5), **c)
+    pre = torch.cat([pre, torch.full((60000 if wide else 0,), -1, dtype=torch.int32, device=DEV)])
+    ws = workspace(q, Kp, pre, table)
+    lens = [(9000, own), (4097, own.clamp(max=64)), (1, own.clamp(max=1)), (8999, own.flip(0).minimum(own))]
+    queries = [torch.roll(q, k, 0) for k in range(3)]
+    plens = [torch.tensor([n], device=DEV) for n, _ in lens]
+    x, plen, mine = torch.empty_like(q), torch.empty_like(plens[0]), torch.empty_like(own)
+    torch.cuda.synchronize()
+    got = []
+    for k in range(60):
+        x.copy_(queries[k % 3])
+        plen.copy_(plens[k % 4])
+        mine.copy_(lens[k % 4][1])
+        got.append(hsa.hsa_prefix_decode(x, Kp, Vp, pre, plen, table, mine, workspace=ws))
+    torch.cuda.synchronize()
+    for k in range(12):
+        P, o = lens[k % 4]
+        (out, lse), names = kernels_of(lambda: hsa.hsa_prefix_decode(queries[k % 3], Kp, Vp, pre, plens[k % 4], table, o))
+        assert ("prefix_wide" in names) == wide
+        for n in range(k, 60, 12):
+            assert torch.equal(got[n][0], out) and torch.equal(got[n][1], lse), n
+        ref = plain_decode(queries[k % 3], Kp, Vp, pre, P, table, o)
+        tol, tol_lse = paged.prefix_tolerance(ref, D)
+        some = ref["keys"] > 0
+        assert (np.abs(out.double().cpu().numpy() - ref["out"]) <= tol).all()
+        assert (np.abs(lse.double().cpu().numpy()[some] - ref["lse"][some]) <= tol_lse[some]).all()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_serving_loop_of_a_wide_batch_without_a_pause(graph):
+    """Steps of plan, append and decode whose prefix goes to the wide kernel, in one stream with nothing between them: the early
+    start of the few-rows kernel under the wide one must see what the append before them wrote."""
+    B, H, Hkv, D, width, T = 70, 8, 2, 128, 6, 70
+    F, steps, doc = 900, 12, 5000
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    Kp, Vp = (torch.full((F, Hkv, 64, D), math.nan, dtype=BF16, device=DEV) for _ in range(2))
+    ring = torch.randperm(F, generator=torch.Generator().manual_seed(2)).to(torch.int32).to(DEV)
+    pool = torch.tensor([0, F, 0], device=DEV)
+    doc_table = torch.full((1, 60000), -1, dtype=torch.int32, device=DEV)
+    kv = torch.randn(2, doc, Hkv, D, generator=gen, device=DEV).to(BF16)
+    _, slots, doc_len = hsa.hsa_page_plan(torch.zeros(1, dtype=torch.int64, device=DEV), torch.tensor([doc], dtype=torch.int32, device=DEV),
+                                          doc_table, ring, pool, doc)
+    hsa.hsa_page_append(kv[0], kv[1], slots, Kp, Vp)
+    lens = torch.zeros(B, dtype=torch.int64, device=DEV)
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    new = torch.ones(B, dtype=torch.int32, device=DEV)
+    rows = torch.randn(steps, 2, T, Hkv, D, generator=gen, device=DEV).to(BF16)
+    qs = torch.randn(steps, B, H, D, generator=gen, device=DEV).to(BF16)
+    row, q = torch.empty_like(rows[0]), torch.empty_like(qs[0])
+    cu, slots = torch.empty(B + 1, dtype=torch.int32, device=DEV), torch.empty(T, dtype=torch.int64, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(B, H, device=DEV)
+    ws = workspace(q[:, :, None], Kp, doc_table, table)
+
+    def step():
+        hsa.hsa_page_plan(lens, new, table, ring, pool, T, cu_new=cu, slots=slots, total_len=lens)
+        hsa.hsa_page_append(row[0], row[1], slots, Kp, Vp)
+        hsa.hsa_prefix_decode(q, Kp, Vp, doc_table.view(-1), doc_len, table, lens, out=out, lse=lse, workspace=ws)
+
+    torch.cuda.synchronize()
+    if graph:
+        recorded = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(recorded):
+            step()
+    got = []
+    for k in range(steps):
+        row.copy_(rows[k])
+        q.copy_(qs[k])
+        recorded.replay() if graph else step()
+        got.append((out.clone(), lse.clone()))
+    hsa.hsa_workspace_status(ws)
+    assert lens.tolist() == [steps] * B and int(pool[2]) == 0
+    for k in (0, 1, 5, steps - 1):
+        ref = plain_decode(qs[k][:, :, None], Kp, Vp, doc_table.view(-1)[:79], doc, table, torch.full((B,), k + 1, device=DEV))
+        tol, tol_lse = paged.prefix_tolerance(ref, D)
+        assert (np.abs(got[k][0].double().cpu().numpy()[:, :, None] - ref["out"]) <= tol).all()
+        assert (np.abs(got[k][1].double().cpu().numpy()[:, :, None] - ref["lse"]) <= tol_lse).all()

@@ -333,7 +333,7 @@ hsa_status hsa_prefix_decode(const hsa_bf16 *q, const hsa_bf16 *Kp, const hsa_bf
 /* ---------------------------------------------------------------------------------------------
  * Self-test of the bounded device waits (no counterpart on the pages; failure detection).
  *
- * Every kernel waits on mbarriers with a bounded number of probes; a wait that runs out records the
+ * Every kernel waits on mbarriers for a bounded number of probes or time; a wait that runs out records the
  * failure in the status flag of the call's workspace, lets the kernel unwind (its copies finish, its
  * TMEM is freed) and returns, so hsa_workspace_status() reports HSA_ERR_TIMEOUT instead of the device
  * hanging. In a healthy run no wait runs out, so this call makes one run out on purpose: it clears the
@@ -345,6 +345,13 @@ hsa_status hsa_prefix_decode(const hsa_bf16 *q, const hsa_bf16 *Kp, const hsa_bf
  * HSA_ERR_INVALID_ARG (host checks, nothing launched) or HSA_ERR_CUDA.
  * ------------------------------------------------------------------------------------------- */
 hsa_status hsa_selftest_bounded_wait(void *workspace, size_t workspace_bytes, unsigned probes, void *stream);
+
+/* The same for the wait that rightly lasts as long as another warp has work (hsa_prefix_decode's copies of the queries): a warp
+ * waits, with a limit of `limit_us` microseconds, while another moves a counter `steps` times, `period_us` apart, and then makes the
+ * expected arrival (arrive != 0) or not. It runs out when the counter has stood still for the limit, however long it moved
+ * before. 1 <= limit_us, period_us <= 100000, steps <= 1000, period_us * steps <= 1000000. */
+hsa_status hsa_selftest_progress_wait(void *workspace, size_t workspace_bytes, unsigned limit_us, unsigned period_us,
+                                      unsigned steps, int arrive, void *stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Measurement hooks (no counterpart on the pages; used to time each kernel live).

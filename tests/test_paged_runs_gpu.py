@@ -315,3 +315,50 @@ def test_serving_loop_of_a_wide_batch_without_a_pause(graph):
         tol, tol_lse = paged.prefix_tolerance(ref, D)
         assert (np.abs(got[k][0].double().cpu().numpy()[:, :, None] - ref["out"]) <= tol).all()
         assert (np.abs(got[k][1].double().cpu().numpy()[:, :, None] - ref["lse"]) <= tol_lse).all()
+
+
+@pytest.mark.parametrize("limit,period,steps,arrive,ok", [
+    (4000, 1000, 30, 1, True),      # 30 ms of work under a limit of 4
+    (4000, 1000, 30, 0, False),     # the work ends and nobody arrives
+    (2000, 1, 0, 0, False), (100000, 1, 1, 1, True),
+])
+def test_wait_goes_on_while_the_other_warp_has_work(limit, period, steps, arrive, ok):
+    ws = torch.empty(4096, dtype=torch.uint8, device=DEV)
+    assert hsa.lib().hsa_selftest_progress_wait(ws.data_ptr(), 4096, limit, period, steps, arrive, torch.cuda.current_stream().cuda_stream) == 0
+    if ok:
+        hsa.hsa_workspace_status(ws)
+    else:
+        with pytest.raises(hsa.HSAError, match="HSA_ERR_TIMEOUT"):
+            hsa.hsa_workspace_status(ws)
+
+
+@pytest.mark.parametrize("B,H,tokens", [(4, 8, 1 << 28), (24, 32, 1 << 26)])
+def test_prefix_of_many_millions_of_tokens(B, H, tokens):
+    """Segments that take tens of milliseconds each: the warp that copies queries waits that long for the next one, a request's
+    own tokens, and copies the right ones then. The prefix is 64 pages in turn; the own tokens outweigh it by far in half of the
+    requests, so that they are held to their rounding, and count for nothing in the others, which are held to the rounding of
+    sums of that many terms."""
+    D, Hkv, pages = 128, 8, 64
+    q, Kp, Vp, pre, _, table, own = run_case(56, B=B, H=H, Hkv=Hkv, D=D, prefix=pages * 64, own=torch.arange(B) % 5 * 70 + 60, pages=pages)
+    pre = torch.arange(tokens // 64, device=DEV, dtype=torch.int32) % pages
+    ws = workspace(q, Kp, pre, table)
+    big = torch.arange(B, device=DEV) % 2 == 0
+    mine = torch.unique(table[big][table[big] >= 0].long())
+    Kp[mine, :, :, 1] = 100.0 * D ** 0.5 / 8
+    q[..., 1] = 8.0
+    out, lse = hsa.hsa_prefix_decode(q, Kp, Vp, pre, torch.tensor([tokens], device=DEV), table, own, workspace=ws)
+    hsa.hsa_workspace_status(ws)    # no wait ran out
+    _, run, _ = division(ws)
+    more = math.log(tokens / (pages * 64))
+    rows = np.arange(B) % 2 == 0
+    # a request whose own tokens outweigh the prefix: the prefix seen once, or as often as it is there, makes no difference
+    ref = plain_decode(q, Kp, Vp, pre[:pages], pages * 64, table, own)
+    tol, tol_lse = paged.prefix_tolerance(ref, D)
+    got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (np.abs(got[rows] - ref["out"][rows]) <= tol[rows]).all() and (np.abs(got_lse[rows] - ref["lse"][rows]) <= tol_lse[rows]).all()
+    # the others: own tokens are a few parts in a million of the sum. A thread's sums grow by one term a tile, the output's by
+    # eight products of sixteen keys, whose accumulator may cut instead of rounding
+    alone = plain_decode(q[~big], Kp, Vp, pre[:pages], pages * 64, table[~big], torch.zeros(B // 2, dtype=torch.int64, device=DEV))
+    assert (np.abs(got_lse[~rows] - alone["lse"] - more) <= run * 2.0**-24 + 1e-4).all()
+    tol = paged.prefix_tolerance(alone, D)[0] + (run * (8 * 2.0**-23 + 2.0**-24) + 1e-4) * alone["mean_abs"]
+    assert (np.abs(got[~rows] - alone["out"]) <= tol).all()

@@ -269,8 +269,37 @@ __device__ __forceinline__ bool mbar_wait_n(uint32_t mbar, uint32_t parity, uint
     }
     return false;
 }
-// The kernels' bound: about 2^22 probes, seconds of wall time.
+// Most kernels' bound: 2^22 probes. A probe took 88 ns where one thread waited alone (5000 in 440 us), so 0.4 s; among many
+// that wait on an SM it takes longer.
 __device__ __forceinline__ bool mbar_wait(uint32_t mbar, uint32_t parity) { return mbar_wait_n(mbar, parity, 1u << 22); }
+
+// Bounded by time: `limit` nanoseconds, below 2^31, of the global timer, read once for every 64 probes that failed.
+__device__ __forceinline__ uint32_t timer_ns() {  // (its lower half, for differences)
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+__device__ __forceinline__ bool mbar_wait_ns(uint32_t mbar, uint32_t parity, uint32_t limit) {
+    uint32_t t0 = 0;  // (one loop with one probe: with a second one for the slow path, out of line too, the kernels took 3 to 17% longer)
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_wait_n(mbar, parity, 1)) return true;
+        if (i % 64 == 63) {
+            const uint32_t t = timer_ns();
+            if (i == 63) t0 = t;
+            if (t - t0 >= limit) return false;
+        }
+    }
+}
+// The same by a whole warp, with one answer for all lanes, for a wait that rightly lasts as long as another role has work: it runs
+// out when `count`, which that role moves with everything that it does, has stood still for the limit.
+__device__ __forceinline__ bool mbar_wait_while(uint32_t mbar, uint32_t parity, const volatile int *count, uint32_t limit) {
+    for (int seen = *count;;) {
+        if (__all_sync(0xffffffffu, mbar_wait_ns(mbar, parity, limit))) return true;
+        const int now = __shfl_sync(0xffffffffu, *count, 0);
+        if (__all_sync(0xffffffffu, now == seen)) return false;
+        seen = now;
+    }
+}
 
 // Non-blocking probe: has the phase with parity `parity` completed?
 __device__ __forceinline__ bool mbar_test(uint32_t mbar, uint32_t parity) {

@@ -63,3 +63,39 @@ def test_selftest_progress_wait_checks_its_arguments_on_host(kw, status):
     args = dict(ws=1 << 20, size=4096, limit=1000, period=1000, steps=4, arrive=1, stream=None)
     args.update(kw)
     assert hsa.lib().hsa_selftest_progress_wait(*args.values()) == status and hsa.hsa_last_error() != ""
+
+
+def meta(*shape, dtype):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("width,ring,tokens", [(4, 9, (1 << 32) + 5), (4, (1 << 32) + 9, 8), ((1 << 32) + 1, 9, 8), (4, 9, 1 << 31)])
+def test_page_plan_refuses_sizes_past_32_bits(calls, width, ring, tokens):
+    """The C call takes them as int: a larger one would arrive as another size."""
+    with pytest.raises(ValueError, match="2\\^31"):
+        hsa.hsa_page_plan(meta(2, dtype=torch.int64), meta(2, dtype=torch.int32), meta(2, width, dtype=torch.int32), meta(ring, dtype=torch.int32),
+                          meta(3, dtype=torch.int64), tokens)
+    assert not calls
+
+
+def test_page_append_refuses_sizes_past_32_bits(calls):
+    n, pages = (1 << 32) + 1, (1 << 32) + 3
+    for n, pages in ((n, 3), (1, pages)):
+        K, pool = meta(n, 1, 64, dtype=BF16), meta(pages, 1, 64, 64, dtype=BF16)
+        with pytest.raises(ValueError, match="2\\^31"):
+            hsa.hsa_page_append(K, K, meta(n, dtype=torch.int64), pool, pool)
+    assert not calls
+
+
+@pytest.mark.parametrize("kw", [dict(npre=1 << 32), dict(width=(1 << 32) + 1), dict(pages=(1 << 32) + 3)])
+def test_prefix_decode_refuses_sizes_past_32_bits(calls, kw):
+    def args(B=2, H=2, Hkv=1, D=64, pages=3, npre=1, width=2):
+        pool = meta(pages, Hkv, 64, D, dtype=BF16)
+        return (meta(B, H, D, dtype=BF16), pool, pool, meta(npre, dtype=torch.int32), meta(1, dtype=torch.int64),
+                meta(B, width, dtype=torch.int32), meta(B, dtype=torch.int64))
+
+    with pytest.raises(ValueError, match="2\\^31"):
+        hsa.hsa_prefix_decode(*args(**kw), workspace=meta(1 << 20, dtype=torch.uint8))
+    assert not calls
+    hsa.hsa_prefix_decode(*args(), workspace=meta(1 << 20, dtype=torch.uint8))
+    assert len(calls) == 1

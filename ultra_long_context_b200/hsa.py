@@ -432,6 +432,10 @@ def _fits(t, name, dtype, shape, dev):
         _need(t, name, dtype, shape, dev)
 
 
+def _past_int(sizes):
+    raise ValueError(f"sizes must stay below 2^31, got {sizes}")  # ctypes would cut them to 32 bits
+
+
 def hsa_page_plan(cache_len, new_len, block_table, free_pages, pool, max_tokens, cu_new=None, slots=None,
                   total_len=None, pool_out=None, stream=None):
     """Block tables and slot maps of one serving step, from the requests' lengths, all on the device.
@@ -449,6 +453,8 @@ def hsa_page_plan(cache_len, new_len, block_table, free_pages, pool, max_tokens,
                                  pool_out)
     B, width = block_table.shape
     num_free = free_pages.numel()
+    if max(width, num_free, max_tokens) >> 31:
+        _past_int((width, num_free, max_tokens))
     if pool_out is None:
         pool_out = pool
     _fits(cache_len, "cache_len", _I64T, (B,), dev)
@@ -504,6 +510,8 @@ def hsa_page_append(K, V, slots, Kp, Vp, stream=None):
             return hsa_page_append(K, V, slots, Kp, Vp)
     n, Hkv, D = K.shape
     pages = Kp.shape[0]
+    if max(n, pages) >> 31:
+        _past_int((n, pages))
     ks, vs = _rows(K, "K", dev), _rows(V, "V", dev)
     if V.shape != K.shape:
         raise ValueError(f"V must have shape {(n, Hkv, D)}, got {tuple(V.shape)}")
@@ -542,6 +550,8 @@ def hsa_prefix_decode(q, Kp, Vp, prefix_table, prefix_len, block_table, own_len,
     Tq = shape[2] if len(shape) == 4 else 1
     pages, Hkv = Kp.shape[:2]
     npre, width = prefix_table.numel(), block_table.shape[1]
+    if max(pages, npre, width) >> 31:
+        _past_int((pages, npre, width))
     _fits(q, "q", _BF16, (B, H, D) if len(shape) == 3 else (B, H, Tq, D), dev)
     _fits(Kp, "Kp", _BF16, (pages, Hkv, 64, D), dev)
     _fits(Vp, "Vp", _BF16, (pages, Hkv, 64, D), dev)

@@ -99,3 +99,17 @@ def test_prefix_decode_refuses_sizes_past_32_bits(calls, kw):
     assert not calls
     hsa.hsa_prefix_decode(*args(), workspace=meta(1 << 20, dtype=torch.uint8))
     assert len(calls) == 1
+
+
+def test_a_stream_of_another_device_is_refused(calls):
+    """The call would have run on the tensors' device, on its current stream, in no order with the one that was asked for."""
+    other = types.SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0)
+    q, Kp, Vp, pre, plen, table, own = decode_args()
+    K = torch.zeros(4, 1, 64, dtype=BF16)
+    with pytest.raises(ValueError, match="stream"):
+        hsa.hsa_prefix_decode(q, Kp, Vp, pre, plen, table, own, workspace=torch.empty(1 << 16, dtype=torch.uint8), stream=other)
+    with pytest.raises(ValueError, match="stream"):
+        hsa.hsa_page_append(K, K, torch.zeros(4, dtype=torch.int64), Kp, Vp, stream=other)
+    with pytest.raises(ValueError, match="stream"):
+        hsa.hsa_page_plan(own, own.int(), table, pre, torch.zeros(3, dtype=torch.int64), 4, stream=other)
+    assert not calls

@@ -420,6 +420,8 @@ def _elsewhere(dev, stream):
     """The context that the call has to be made in, so that what it allocates belongs to its device and stream;
     None if that is the present one."""
     if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream must be one of {dev}, got one of {stream.device}")
         return torch.cuda.stream(stream)
     if dev.type == "cuda" and dev.index != torch.cuda.current_device():
         return torch.cuda.device(dev)

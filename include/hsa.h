@@ -317,7 +317,7 @@ hsa_status hsa_page_append(const hsa_bf16 *K, int64_t k_stride, const hsa_bf16 *
  * an empty row of a padded batch. Rows that see nothing get out = 0, lse = -inf. Lengths beyond the
  * tables are cut to them (P <= 0: no prefix); the tokens of a page whose id is outside [0, num_pages) are left out. What
  * lies behind a length in its last page may be anything, NaN included; visible tokens must be finite, their logits
- * too, and their values in V below 2^28 (the fp32 sums carry factors of up to 2^69 over up to 2^30 keys).
+ * too, and their values in V below 2^28 (the fp32 sums take up to 2^64 times that for each of up to 2^31 keys).
  * max_prefix_pages or max_pages may be 0 (its table may then be NULL). H / Hkv * Tq <= 1024, 1 <= Tq <= 64,
  * tables of less than 2^24 pages, B * max_pages < 2^30.
  * Each prefix page is read once for up to 64 or 256 rows (request, query head, token) of its key head.

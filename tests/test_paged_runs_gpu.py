@@ -211,6 +211,15 @@ def test_wide_batches_over_long_runs(c, shape, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("c,wide", [(FEW[4], False), (WIDE[5], True)])
+def test_values_up_to_their_bound(c, wide, D):
+    """|V| just below 2^28 with logits that climb over the references by as much as they may."""
+    case = list(run_case(57, D=D, prefix=long_prefix(c, D, wide), own=own_of(c, 6), shape="up", **c))
+    case[2] = (case[2].float() * 2.0**26).clamp(-2.0**27.9, 2.0**27.9).to(BF16)
+    check(case, wide=wide, room=60000 if wide else 0, moved=True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("shape", ["flat", "up"])
 @pytest.mark.parametrize("c,wide", [(FEW[2], False), (FEW[4], False), (WIDE[1], True), (WIDE[4], True), (WIDE[5], True)])
 def test_bad_pages_late_in_long_runs(c, wide, shape, D):

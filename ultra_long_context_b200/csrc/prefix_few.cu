@@ -7,10 +7,10 @@
 //   O^T += V^T P^T (D x N, fp32 in TMEM; thread = dim)
 // The reference m of a row need not be its maximum: the final quotient cancels it, and P (bf16) and the fp32 sums keep
 // their relative precision as long as nothing leaves their range. So m is the logit of the first key that the row sees
-// in the segment, and moves only when a later one exceeds it by more than 2^64 (a term stays below 2^69, its sum over 2^30
-// keys, times V below 2^28, below 2^127; what is 2^126 below m is less than 2^-126 of the sum, which is at least 1). Then the
-// warpgroup reduces the maxima over the keys, rescales O^T in TMEM and does the tile again; every other tile costs a
-// thread one exponential per row and one barrier with a vote. Row sums stay per thread until the segment ends.
+// in the segment, and moves only when a later one exceeds it by more than 2^59 (a term stays below 2^64, its sum over the 2^31
+// keys of a prefix and a request, times V below 2^28, below 2^123; what is 2^126 below m is less than 2^-126 of the sum, which is at
+// least 1). Then the warpgroup reduces the maxima over the keys, rescales O^T in TMEM and does the tile again; every other tile
+// costs a thread one exponential per row and one barrier with a vote. Row sums stay per thread until the segment ends.
 //
 // Measured, per tile of 128 keys and SM: D = 128, 16 rows 1.39 us = 64 KB at 7.0 TB/s over 148 SMs, out of L2 0.60 us; 64 rows
 // 1.43 us, out of L2 0.77; D = 64, 16 rows 0.64 us, 64 rows 0.76, out of L2 0.75: there the softmax bounds it (1400
@@ -39,7 +39,7 @@ namespace hsa {
 
 constexpr int kFwSWarp = 8, kFwOWarp = 9, kFwTmaWarp = 10, kFwQWarp = 11;
 constexpr int kFwThreads = 32 * (kFwQWarp + 1);
-constexpr float kFwGrow = 64.0f, kFwSumMax = 0x1p69f;  // a sum of 32 terms of at most 2^64
+constexpr float kFwGrow = 59.0f, kFwSumMax = 0x1p64f;  // a sum of 32 terms of at most 2^59
 
 template <int D, int NR>  // NR: rows per segment at most
 struct FwSmem {

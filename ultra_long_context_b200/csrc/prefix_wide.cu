@@ -4,7 +4,8 @@
 // S = Q K^T (128 rows x 128 keys, fp32 in TMEM), P = exp2(S scale' - m) as bf16 over S in TMEM, which is the A operand
 // of O += P V (128 x D, fp32 in TMEM). The reference m of a row need not be its maximum (see prefix_few.cu): it is the
 // logit of the first key that the row sees in the segment, so no maximum is taken at all; a tile whose row sum exceeds
-// 2^70 moves it (rarely): the pair of warps then reduces the maximum, rescales O in TMEM and does the tile again.
+// 2^70 moves it (rarely): the pair of warps then reduces the maximum, rescales O in TMEM and does the tile again. (Half a tile, 64
+// keys, adds up to 2^70 at most, so a sum over 2^31 keys, times V below 2^28, stays below 2^123.)
 //
 // Measured, per tile of 128 keys and 256 rows on an SM: D = 128 1.89 us out of L2 (1.32 PFLOP/s over 148 SMs), 2.43 us out of
 // HBM; D = 64 1.50 and 1.56. Tensor cores and exponentials are busy half of that time each: a stream's chain bounds it,

@@ -110,12 +110,15 @@ def prefix_tolerance(ref, D):
     """Elementwise error bounds (out, lse) of a kernel that takes bf16 inputs, sums in fp32 and rounds the
     probabilities and the result to bf16.
 
-    A logit is a sum of D exact products (off by at most D 2^-24 reach, also after the scale and its fused
-    multiply-add) less a maximum that is itself such a sum, and its exponential is off by 2^-22 and by the
-    rounding of its argument (2^-23 |argument|, and arguments below -30 weigh nothing): e relative. Numerator
-    and denominator both carry e and the rounding of a sum of ``keys`` terms; the numerator's terms are rounded to
-    bf16 (2^-8), and so is the result."""
-    e = 2 * D * 2.0**-24 * ref["reach"] + 2.0**-22 + 30 * 2.0**-23
+    A logit is a sum of D exact products, off by at most D 2^-24 reach, also after the scale and its fused multiply-add. It is
+    taken relative to a reference that need not be the row's maximum: some visible logit as the kernel has it, the same number in
+    numerator and denominator, added to lse in the end. The difference y, in powers of two, is rounded once, which makes
+    ln 2 2^-24 |y| of the exponential, and so is each factor by which sums are brought to another reference. A term is at most 2^70 over
+    its reference; one that counts in the end is scaled down by at most that and the 24 bits below which it is lost, and references only
+    rise, so the arguments of its factors are 70 + 70 + 24 at most in all: 57 2^-23. The exponentials themselves are off by 2^-22 each, two
+    of them: e relative. Numerator and denominator both carry e and the rounding of a sum of ``keys`` terms; the
+    numerator's terms are rounded to bf16 (2^-8), and so is the result."""
+    e = 2 * D * 2.0**-24 * ref["reach"] + 2 * 2.0**-22 + 57 * 2.0**-23
     sums = (ref["keys"] + 64) * 2.0**-24
     rel = 2 * (e + sums)
     out = (2.0**-8 + rel)[..., None] * ref["mean_abs"] + 2.0**-8 * np.abs(ref["out"])

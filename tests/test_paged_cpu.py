@@ -143,3 +143,33 @@ def test_prefix_decode_workspace_size():
     assert 0 < a <= b
     assert hsa.hsa_prefix_decode_workspace_size(0, 8, 8, 128, 64, 8) == 0
     assert hsa.hsa_prefix_decode_workspace_size(4, 8, 3, 128, 64, 8) == 0
+
+
+# ---- the wide kernel's exponential of its own ----
+def test_polynomial_exponential_is_as_good_as_its_comment_says():
+    """The coefficients as they stand in the source, the kernel's steps in fp32 (a fused multiply-add is one rounding; in fp64 the
+    product is exact and the sum nearly so): off by 2^-22 at most, and the clamped ends."""
+    import os
+    import re
+
+    src = open(os.path.join(os.path.dirname(hsa.__file__), "csrc", "prefix_wide.cu")).read()
+    body = src[src.index("pf_exp2_fma(float2 y) {"):]
+    coefficients = [np.float32(float.fromhex(a)) for a, b in re.findall(r"\{(0x[0-9a-fp.+-]+)f, (0x[0-9a-fp.+-]+)f\}", body[:body.index("return")]) if a == b]
+    assert len(coefficients) == 6
+
+    def exp2(y):
+        y = np.clip(y.astype(np.float32), np.float32(-126), np.float32(127))
+        t = (y + np.float32(12582912)).astype(np.float32)
+        n = (t - np.float32(12582912)).astype(np.float32)
+        f = (y.astype(np.float64) - n).astype(np.float32)
+        p = np.full_like(f, coefficients[0])
+        for c in coefficients[1:]:
+            p = (p.astype(np.float64) * f + c).astype(np.float32)
+        return (p.view(np.int32) + (t.view(np.int32) << 23)).view(np.float32)
+
+    rng = np.random.default_rng(8)
+    y = np.concatenate([rng.uniform(-126, 127, 400000), rng.uniform(-1, 1, 200000), np.arange(-126, 128), np.arange(-126, 127) + 0.5]).astype(np.float32)
+    true = np.exp2(y.astype(np.float64))
+    assert np.abs(exp2(y) / true - 1).max() <= 2.0**-22
+    assert exp2(np.array([-np.inf, -1000.0]))[0] <= 2.0**-126 * 1.000001
+    assert (exp2(np.array([128.0, 1e30, np.inf])) >= 2.0**126).all()

@@ -311,7 +311,8 @@ hsa_status hsa_page_append(const hsa_bf16 *K, int64_t k_stride, const hsa_bf16 *
  *   Kp, Vp        [num_pages, Hkv, 64, D]   the pools
  *   prefix_table  [max_prefix_pages] int32  the prefix's pages; prefix_len [1] int64 its tokens, P
  *   block_table   [B, max_pages] int32      each request's own pages; own_len [B] int64 its own tokens, n
- *   out           [B, H, Tq, D] bf16        softmax(scale q K^T) V, rounded to nearest-even from fp32
+ *   out           [B, H, Tq, D] bf16        softmax(scale q K^T) V; logits and sums are fp32, each probability is rounded
+ *                                           to bf16 before its product with V, the result to nearest-even from fp32
  *   lse           [B, H, Tq] fp32           optional (NULL): log of the sum of exp(scale q K^T)
  * Token i sits at position P + n - Tq + i and sees the positions up to its own. A request with n < 0 is
  * an empty row of a padded batch. Rows that see nothing get out = 0, lse = -inf. Lengths beyond the
@@ -320,7 +321,10 @@ hsa_status hsa_page_append(const hsa_bf16 *K, int64_t k_stride, const hsa_bf16 *
  * too, and their values in V below 2^28 (the fp32 sums take up to 2^64 times that for each of up to 2^31 keys).
  * max_prefix_pages or max_pages may be 0 (its table may then be NULL). H / Hkv * Tq <= 1024, 1 <= Tq <= 64,
  * tables of less than 2^24 pages, B * max_pages < 2^30.
- * Each prefix page is read once for up to 64 or 256 rows (request, query head, token) of its key head.
+ * Each prefix page is read once for up to 64 or 256 rows (request, query head, token) of its key head: one of two kernels
+ * takes the prefix, chosen by the sizes, max_prefix_pages among them, since the length is on the device. So a table far larger than
+ * its prefix has a price with more than 64 rows per key head: 32 requests x 32 query heads (8 key heads) x 128 over 2048 tokens
+ * take 21.5 us with a table of their own size, 29 us with one for 2^20 tokens.
  * The workspace's size is 0 for sizes that the call refuses. */
 size_t hsa_prefix_decode_workspace_size(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages, int max_pages);
 

@@ -7,16 +7,18 @@
 // token with pos % 64 == 0 is then one of the new ones, so one pass over the packed tokens writes both
 // the slots and the table entries: a token finds its request by binary search in the running sums.
 // It is bound by latency: two dependent loads, one block scan of three sums (a second one only where the slot map is too
-// short), one search. One thread-block cluster of up to 8 blocks does all of it in one launch: every block scans all the
-// lengths for itself (at most 96 KB out of L2), and the cluster barrier stands between the last read of `cache_len` and
-// `pool` and the first write of what may be the same memory. A thread takes a run of up to 16 consecutive tokens, one search
+// short), a load and a store for each finished request that a team of warps has, one after the other, one search.
+// One thread-block cluster of up to 8 blocks does all of it in one launch: every block scans all the lengths for itself (at
+// most 96 KB out of L2), and the cluster barrier stands between the last read of `cache_len` and `pool` and the first write
+// of what may be the same memory. A thread takes a run of up to 16 consecutive tokens, one search
 // for all, four lookups in flight; finished requests are listed by the block that owns them (request % blocks) and
-// copied by eight warps each. One block of 1024 threads before a second one: a cluster's barrier costs more than
-// four warps' work (1500 requests 14 us in clusters of small blocks, 9). Measured: 64 requests that add a token each 4.9 us, 1500
-// requests 9.0 us, 256 prompts of 87,000 tokens 14.3 us (0.75 MB; 0.12 us at the HBM's rate).
+// copied by eight warps each. Blocks of 1024 threads before a second block, since a cluster's barrier costs more than
+// four warps' work (1500 requests and as many tokens 14 us in clusters of small blocks, 9 in one of four of 1024). Measured: 64
+// requests that add a token each, three finished, 5.0 us, 1500 requests 9.2 us, 256 with prompts of 87,000 tokens 14.4 us (0.75 MB;
+// 0.12 us at the HBM's rate).
 //
 // Append. A copy: each 16-byte vector is read and written once, two steps in flight, bound by HBM: 32768 tokens x 8 heads x
-// 128 (263 MB) 45.1 us = 5.84 TB/s; 3001 tokens 2.5 us and 64 tokens 1.8 us, bound by latency.
+// 128 (263 MB) 45.1 us = 5.84 TB/s; 3001 tokens 2.5 us and 64 tokens 2.0 us, bound by latency.
 #include <cooperative_groups.h>
 
 #include "common.cuh"

@@ -61,7 +61,8 @@ struct PfDims {
     // larger tiles to fill: 15 us (8). Both sides measured, D = 128: 512 rows x 4 heads over 14208 / 28416 / 56832 tokens
     // 38 / 61 / 110 us and 43 / 56 / 81, 1024 rows 66 / 110 / 208 and 63 / 89 / 135, 128 rows x 8 heads over 28416 / 59136
     // 42 / 67 and 48 / 66; D = 64: 512 rows 36 / 54 / 93 and 37 / 46 / 65. The tiles are those of the table, since the
-    // length is not known here.
+    // length is not known here: a short prefix in a long table pays for the wide kernel's start (128 rows x 8 heads over 2048
+    // tokens 21.5 us with a table of their size, 29 with one for 2^20).
     static bool pf_wide(int Rp, int Hkv, int D, int tiles) {
         const bool d128 = D == 128;
         const double per_sm = (double)Hkv * tiles / kPfCtas;

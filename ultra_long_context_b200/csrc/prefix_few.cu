@@ -5,6 +5,9 @@
 // part of an MMA or of the softmax is spent on padding rows:
 //   S^T = K Q^T    (128 keys x N, fp32 in TMEM; thread = key)       P^T = exp2(S^T scale' - m) (bf16, to shared memory)
 //   O^T += V^T P^T (D x N, fp32 in TMEM; thread = dim)
+// P is rounded to bf16, here and in the wide kernel, because both operands of a product have one type and V's is bf16: a term is off
+// by up to 2^-8, which averages out over the keys (the result's error against 64 bits is 1.4 times that of its own rounding). P in
+// two parts would double the products and P's way through shared memory. The row sums add the terms before their rounding.
 // The reference m of a row need not be its maximum: the final quotient cancels it, and P (bf16) and the fp32 sums keep
 // their relative precision as long as nothing leaves their range. So m is the logit of the first key that the row sees
 // in the segment, and moves only when a later one exceeds it by more than 2^59 (a term stays below 2^64, its sum over the 2^31

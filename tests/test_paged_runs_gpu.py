@@ -371,3 +371,50 @@ def test_prefix_of_many_millions_of_tokens(B, H, tokens):
     assert (np.abs(got_lse[~rows] - alone["lse"] - more) <= run * 2.0**-24 + 1e-4).all()
     tol = paged.prefix_tolerance(alone, D)[0] + (run * (8 * 2.0**-23 + 2.0**-24) + 1e-4) * alone["mean_abs"]
     assert (np.abs(got[~rows] - alone["out"]) <= tol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("c,wide", [(FEW[1], False), (FEW[4], False), (WIDE[1], True), (WIDE[5], True)])
+def test_queries_that_are_no_numbers_stay_in_their_rows(c, wide, D):
+    """NaN and infinities in the queries of a live request, of the empty rows of a padded batch and of rows that see nothing."""
+    own = own_of(c, 7)
+    q, Kp, Vp, pre, P, table, own = run_case(58, D=D, prefix=5000, own=own, **c)
+    pre = torch.cat([pre, torch.full((60000 if wide else 0,), -1, dtype=torch.int32, device=DEV)])
+    plen, nothing = torch.tensor([P], device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    want = hsa.hsa_prefix_decode(q, Kp, Vp, pre, plen, table, own)
+    bad = q.clone()
+    bad[own < 0] = math.nan
+    bad[2] = math.nan
+    bad[4, :, :, ::3] = math.inf
+    got = hsa.hsa_prefix_decode(bad, Kp, Vp, pre, plen, table, own)
+    none = hsa.hsa_prefix_decode(torch.full_like(q, math.nan), Kp, Vp, pre, nothing, table, own.clamp(max=0))
+    torch.cuda.synchronize()
+    keep = torch.ones(c["B"], dtype=torch.bool, device=DEV)
+    keep[[2, 4]] = False
+    assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1][keep], want[1][keep])
+    assert (got[0][own < 0] == 0).all() and (got[1][own < 0] == -math.inf).all()
+    assert (none[0] == 0).all() and (none[1] == -math.inf).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_captured_call_that_allocates_its_own_workspace(wide):
+    """Two calls of one graph, each with outputs and a workspace out of the graph's memory, replayed over changed lengths."""
+    c = WIDE[5] if wide else FEW[4]
+    q, Kp, Vp, pre, P, table, own = run_case(59, D=128, prefix=7001, own=own_of(c, 8), **c)
+    pre = torch.cat([pre, torch.full((60000 if wide else 0,), -1, dtype=torch.int32, device=DEV)])
+    plen, mine, x = torch.tensor([P], device=DEV), own.clone(), torch.roll(q, 1, 0)
+    hsa.hsa_prefix_decode(q, Kp, Vp, pre, plen, table, mine)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a = hsa.hsa_prefix_decode(q, Kp, Vp, pre, plen, table, mine)
+        b = hsa.hsa_prefix_decode(x, Kp, Vp, pre, plen, table, mine)
+    for n, lens in ((P, own), (64, own.clamp(max=40)), (0, own), (6999, own.clamp(max=0))):
+        plen.fill_(n)
+        mine.copy_(lens)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for y, got in ((q, a), (x, b)):
+            want = hsa.hsa_prefix_decode(y, Kp, Vp, pre, plen, table, mine)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

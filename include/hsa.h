@@ -324,7 +324,7 @@ hsa_status hsa_page_append(const hsa_bf16 *K, int64_t k_stride, const hsa_bf16 *
  * Each prefix page is read once for up to 64 or 256 rows (request, query head, token) of its key head: one of two kernels
  * takes the prefix, chosen by the sizes, max_prefix_pages among them, since the length is on the device. So a table far larger than
  * its prefix has a price with more than 64 rows per key head: 32 requests x 32 query heads (8 key heads) x 128 over 2048 tokens
- * take 21.5 us with a table of their own size, 29 us with one for 2^20 tokens.
+ * take 21 to 25 us with a table of their own size, 29 to 31 with one for 2^20 tokens.
  * The workspace's size is 0 for sizes that the call refuses. */
 size_t hsa_prefix_decode_workspace_size(int B, int H, int Hkv, int Tq, int D, int max_prefix_pages, int max_pages);
 

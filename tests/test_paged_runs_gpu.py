@@ -418,3 +418,36 @@ def test_captured_call_that_allocates_its_own_workspace(wide):
         for y, got in ((q, a), (x, b)):
             want = hsa.hsa_prefix_decode(y, Kp, Vp, pre, plen, table, mine)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H,prefix,own,wide", [
+    (4, 8, 1 << 26, 0, False), (24, 32, 1 << 26, 0, True), (32, 64, 1 << 26, 0, True),    # the prefix
+    (2, 8, 0, 1 << 27, False), (1, 16, 100, (1 << 27) + 77, False),                       # a request's own tokens
+])
+def test_sums_over_very_many_tokens_do_not_drift(B, H, prefix, own, wide, D):
+    """V is one everywhere, so the output is one: products accumulate in fp32 by cutting, which took 0.8% off 2^26 tokens summed in one
+    go. In runs of 512 tiles, eight products a tile, each cut by 2^-23 at most, 2^-11 are lost at most, which with the rounding to
+    bf16 (half a step below one is 2^-9) leaves no other number."""
+    Hkv, pages = 8, 64
+    q, Kp, Vp, _, _, table, _ = run_case(60, B=B, H=H, Hkv=Hkv, D=D, prefix=pages * 64, own=torch.zeros(B, dtype=torch.int64), pages=pages)
+    Vp.fill_(1.0)
+    Kp.mul_(0.5)
+    pre = torch.arange(-(-prefix // 64), device=DEV, dtype=torch.int32) % pages
+    if own:
+        table = (torch.arange(B * -(-own // 64), device=DEV, dtype=torch.int32) % pages).view(B, -1)
+    lens = torch.full((B,), own, device=DEV)
+    ws = workspace(q, Kp, pre, table)
+
+    def call():
+        return hsa.hsa_prefix_decode(q, Kp, Vp, pre, torch.tensor([prefix], device=DEV), table, lens, workspace=ws)
+
+    (out, lse), names = kernels_of(call)
+    hsa.hsa_workspace_status(ws)
+    assert ("prefix_wide" in names) == wide
+    assert (out == 1).all(), (float(out.float().min()), float(out.float().max()))
+    # the sum of the exponentials: 64 pages, as often as they are there (what is over counts for less than a part in 100,000)
+    few = torch.arange(pages, device=DEV, dtype=torch.int32)
+    ref = plain_decode(q, Kp, Vp, few, pages * 64, table[:, :0], torch.zeros(B, dtype=torch.int64, device=DEV))
+    more = math.log((prefix + own) / (pages * 64))
+    assert (np.abs(lse.double().cpu().numpy() - ref["lse"] - more) <= 512 * 2.0**-24 + 1e-4).all()

@@ -21,6 +21,12 @@ constexpr int kPfFewRows = 64;    // rows per segment at most: in the few-rows k
 constexpr int kPfWideRows = 256;  // in the wide kernel
 constexpr int kPfCtas = 148;      // at most: one per SM; the workspace is sized for it
 constexpr int kPfItems = 4 * kPfCtas;  // prefix segments at most (or one per head and row group)
+// Tiles that are summed in the products' accumulator at most. It adds by cutting: 2^-24 of the sum are lost with each product, eight
+// a tile (V = 1: 0.8% over 14,000 tiles, 8% over 114,000). A longer run is walked in pieces, each of which is added to
+// the partial that is there, in fp32 by rounding. 512 tiles lose some 2^-12, a sixteenth of the result's rounding, and
+// take 300 us and more, so that a piece's start and end do not show. Even, so that every piece's items alternate between the
+// wide kernel's streams alike.
+constexpr int kPfPiece = 512;
 // Costs in half tiles: a tile, and what a segment's start and end take beside its tiles, some 5000 cycles (24 requests x 4
 // tokens over 20K: 35.7 us; with 3 and 4 for the two 36.2, with 3 and 5 40.8; other shapes within 1%)
 constexpr int kPfTileCost = 2, kPfPrefixCost = 5, kPfOwnCost = 5;
@@ -62,7 +68,7 @@ struct PfDims {
     // 38 / 61 / 110 us and 43 / 56 / 81, 1024 rows 66 / 110 / 208 and 63 / 89 / 135, 128 rows x 8 heads over 28416 / 59136
     // 42 / 67 and 48 / 66; D = 64: 512 rows 36 / 54 / 93 and 37 / 46 / 65. The tiles are those of the table, since the
     // length is not known here: a short prefix in a long table pays for the wide kernel's start (128 rows x 8 heads over 2048
-    // tokens 21.5 us with a table of their size, 29 with one for 2^20).
+    // tokens 21 to 25 us with a table of their size, 29 to 31 with one for 2^20).
     static bool pf_wide(int Rp, int Hkv, int D, int tiles) {
         const bool d128 = D == 128;
         const double per_sm = (double)Hkv * tiles / kPfCtas;
@@ -111,8 +117,10 @@ struct PfSeg {
     int r0, nr;          // its rows among the key head's (prefix) or the request's (own)
     int tile0, nt;       // run of tiles
     int len;             // tokens of the sequence
-    int part;            // index of its partials
+    int part;            // index of its partials; ~index in a later piece of its run, which is added to what stands there
     const int32_t *table;
+    __device__ bool added() const { return part < 0; }
+    __device__ int place() const { return part < 0 ? ~part : part; }
 };
 
 // Which of the 32 pages of a segment's tiles t .. t + 15 are there? A warp's lanes look one up each and vote; fetch() of the
@@ -159,9 +167,10 @@ struct PfWalk {
     const int32_t *bcum;
     const PfDims &d;
     int item, lane, blk, len, weight, before;
+    int rest;  // tiles of the present run behind its piece
     int64_t x, end;
     __device__ PfWalk(const PrefixArgs &a_, const PfPlan &p_, const int32_t *bcum_, const PfDims &d_)
-        : a(a_), p(p_), bcum(bcum_), d(d_), item(blockIdx.x), lane(threadIdx.x & 31), blk(-1), len(0), weight(0), before(0),
+        : a(a_), p(p_), bcum(bcum_), d(d_), item(blockIdx.x), lane(threadIdx.x & 31), blk(-1), len(0), weight(0), before(0), rest(0),
           x(p_.start(blockIdx.x)), end(p_.start(blockIdx.x + 1)) {}
     __device__ void load_block(int k) {
         blk = k;
@@ -177,7 +186,23 @@ struct PfWalk {
         }
         before = bcum[k] + sum - weight;
     }
+    // `s`: the segment before, and then the next one
     __device__ bool next(PfSeg &s) {
+        if (rest > 0) {
+            s.tile0 += s.nt;
+            s.part = ~s.place();
+            s.nt = min(rest, kPfPiece);
+            rest -= s.nt;
+            return true;
+        }
+        if (!next_run(s)) return false;
+        if (s.nt > kPfPiece) {
+            rest = s.nt - kPfPiece;
+            s.nt = kPfPiece;
+        }
+        return true;
+    }
+    __device__ bool next_run(PfSeg &s) {
         if (item < p.items) {
             const int units = a.Hkv * d.Rgp, k = item / units, u = item - k * units;
             s.h = d.Rgp == 1 ? u : u / d.Rgp;
@@ -248,6 +273,17 @@ __device__ __forceinline__ void pf_copy_q(const PrefixArgs &a, const PfDims &d, 
                 cp_async16_u32(dst(r0 + rr, ch), from >= 0 ? a.q + (int64_t)from * D + ch * 8 : a.q, from >= 0 ? 16 : 0);
         }
     }
+}
+
+// Two partials of a row: the reference of their sum and the factors that bring each to it. (0 for one that has seen nothing: what
+// stands there may be anything.)
+struct PfSum {
+    float m, f0, f1;
+    __device__ PfSum(float m0, float m1)
+        : m(fmaxf(m0, m1)), f0(m0 > -INFINITY ? ex2_approx(m0 - m) : 0.0f), f1(m1 > -INFINITY ? ex2_approx(m1 - m) : 0.0f) {}
+};
+__device__ __forceinline__ float pf_add(float x0, float f0, float x1, float f1) {
+    return (f0 > 0.0f ? f0 * x0 : 0.0f) + (f1 > 0.0f ? f1 * x1 : 0.0f);
 }
 
 // 32 bytes in one store: a whole sector, where two of 16 make the memory system handle it twice.

@@ -546,17 +546,39 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 }
             }
             if (lane < H) s_red[wq * H + lane] = l[0];
-            const int64_t at = (int64_t)seg.part * (seg.b < 0 ? d.strideP : d.strideO) + row0;
+            const int64_t at = (int64_t)seg.place() * (seg.b < 0 ? d.strideP : d.strideO) + row0;
             float *O = (seg.b < 0 ? w.Op : w.Oo) + at * D;
             fw_bar(bid);
             if (r < rows) {
                 const float sum = (s_red[r] + s_red[H + r]) + (s_red[2 * H + r] + s_red[3 * H + r]);
-                reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo)[at + r] = make_float2(-nms[r], sum);
+                float2 *ml = reinterpret_cast<float2 *>(seg.b < 0 ? w.mlp : w.mlo) + at + r;
+                if (seg.added()) {
+                    const float2 old = *ml;
+                    const PfSum both(old.x, -nms[r]);
+                    *ml = make_float2(both.m, pf_add(old.y, both.f0, sum, both.f1));
+                    s_fac[r] = both.f0;
+                    nms[r] = both.f1;
+                } else {
+                    *ml = make_float2(-nms[r], sum);
+                }
             }
             const int last = g.n0 + seg.nt - 1;
             if (!pf_wait(bar(SM::kODone + last % NB), (uint32_t)(last / NB))) s_bad[half] = 1;  // seen at the next barrier
             tc::fence_after();
-            if (rows > 0) {
+            if (seg.added()) {
+                fw_bar(bid);  // the factors
+#pragma unroll 1
+                for (int c = 0; c < rows; c += 8) {
+                    float o[8];
+                    tc::tmem_ld8(tO + c, o);
+                    if (r < D) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (c + i < rows) O[(size_t)(c + i) * D + r] = pf_add(O[(size_t)(c + i) * D + r], s_fac[c + i], o[i], nms[c + i]);
+                    }
+                    __syncwarp();
+                }
+            } else if (rows > 0) {
                 float o[H];
                 fw_ld<H>(tO, o);
                 if (r < D) {

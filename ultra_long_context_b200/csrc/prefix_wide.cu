@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         const int pages_all = a.num_pages;
         int n = 0, items = 0;
         bool more = true;
+        PfNote g;
         while (ok && more) {
-            PfNote g;
             more = walk.next(g.s);
             if (!more) g.s.nr = 0;
             g.n0 = n;
@@ -496,6 +496,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
             if (!rest) s_badp[pid - 1] = 1;
             if (!active && !rest) continue;
             if (active) {
+                const int64_t at = (int64_t)seg.place() * d.strideP + (both ? rr : turn * seg.nr + rr);
+                float2 *ml = reinterpret_cast<float2 *>(w.mlp) + at;
+                float2 old = {-INFINITY, 0.0f};
+                if (seg.added() && mine) old = *ml;
                 s_row[128 * half] = l;
                 pf_pair_bar(pid);
                 if (s_badp[pid - 1]) {
@@ -503,12 +507,26 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                     break;
                 }
                 tc::fence_after();
-                const int64_t at = (int64_t)seg.part * d.strideP + (both ? rr : turn * seg.nr + rr);
                 float *O = w.Op + at * D + half * (D / 2);
-                if (mine && half == 0)
-                    reinterpret_cast<float2 *>(w.mlp)[at] = make_float2(ms, s_row[0] + s_row[128]);
+                if (seg.added()) {
+                    const PfSum sum(old.x, ms);
+                    if (mine && half == 0) *ml = make_float2(sum.m, pf_add(old.y, sum.f0, s_row[0] + s_row[128], sum.f1));
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 32) {
+                    for (int c = 0; c < D / 2; c += 8) {
+                        float o[8];
+                        __syncwarp();
+                        tc::tmem_ld8(tO + c, o);
+                        if (mine) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = pf_add(O[c + i], sum.f0, o[i], sum.f1);
+                            pf_store8(O + c, o);
+                        }
+                    }
+                } else if (mine && half == 0) {
+                    *ml = make_float2(ms, s_row[0] + s_row[128]);
+                }
+#pragma unroll 1
+                for (int c = 0; !seg.added() && c < D / 2; c += 32) {
                     float o[32];
                     __syncwarp();  // the lanes without a row skip the stores
                     tc::tmem_ld32(tO + c, o);

@@ -451,3 +451,49 @@ def test_sums_over_very_many_tokens_do_not_drift(B, H, prefix, own, wide, D):
     ref = plain_decode(q, Kp, Vp, few, pages * 64, table[:, :0], torch.zeros(B, dtype=torch.int64, device=DEV))
     more = math.log((prefix + own) / (pages * 64))
     assert (np.abs(lse.double().cpu().numpy() - ref["lse"] - more) <= 512 * 2.0**-24 + 1e-4).all()
+
+
+@pytest.mark.parametrize("shape", ["flat", "up", "down"])
+@pytest.mark.parametrize("D,B,H,wide", [(64, 3, 8, False), (128, 5, 24, False), (64, 10, 72, True), (128, 6, 136, True)])
+def test_pieces_of_runs_longer_than_the_accumulator_sums(D, B, H, wide, shape):
+    """Runs of 700 tiles are walked in pieces of 512 and what is left: the second is added to the first, both with references that
+    moved, with bad pages at the joint; some requests see all, some nothing."""
+    c = dict(B=B, H=H, Hkv=8)
+    P = 37 * 700 * TILE + 61
+    n = -(-P // 64)
+    bad = sorted({*range(1023, n, 1400), *range(1024, n, 2800), *range(7, n, 9001)})
+    check(run_case(61, D=D, prefix=P, own=own_of(c, 9), shape=shape, bad=bad, **c), wide=wide, room=0, min_run=513, moved=shape != "flat")
+
+
+def test_threads_that_call_at_once():
+    """Four host threads with a stream each and batches of several kernels and sizes: each gets what it gets alone."""
+    import threading
+
+    cases = [run_case(62 + k, D=D, prefix=P, own=own_of(c, 10 + k), **c) + (room,)
+             for k, (c, D, P, room) in enumerate([(FEW[0], 64, 700, 0), (FEW[4], 128, 9000, 0), (WIDE[5], 128, 4000, 60000), (WIDE[2], 64, 9000, 60000)])]
+    calls = []
+    for q, Kp, Vp, pre, P, table, own, room in cases:
+        pre = torch.cat([pre, torch.full((room,), -1, dtype=torch.int32, device=DEV)])
+        calls.append((q, Kp, Vp, pre, torch.tensor([P], device=DEV), table, own))
+    want = [hsa.hsa_prefix_decode(*a) for a in calls]
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in calls], []
+
+    def work(k):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(25):
+                got[k].append(hsa.hsa_prefix_decode(*calls[k], stream=s))
+            s.synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for w, g in zip(want, got):
+        assert len(g) == 25 and all(torch.equal(o, w[0]) and torch.equal(l, w[1]) for o, l in g)

@@ -350,12 +350,10 @@ hsa_status hsa_prefix_decode(const hsa_bf16 *q, const hsa_bf16 *Kp, const hsa_bf
  * ------------------------------------------------------------------------------------------- */
 hsa_status hsa_selftest_bounded_wait(void *workspace, size_t workspace_bytes, unsigned probes, void *stream);
 
-/* The same for the wait that rightly lasts as long as another warp has work (hsa_prefix_decode's copies of the queries): a warp
- * waits, with a limit of `limit_us` microseconds, while another moves a counter `steps` times, `period_us` apart, and then makes the
- * expected arrival (arrive != 0) or not. It runs out when the counter has stood still for the limit, however long it moved
- * before. 1 <= limit_us, period_us <= 100000, steps <= 1000, period_us * steps <= 1000000. */
-hsa_status hsa_selftest_progress_wait(void *workspace, size_t workspace_bytes, unsigned limit_us, unsigned period_us,
-                                      unsigned steps, int arrive, void *stream);
+/* The same for the wait that time bounds (hsa_prefix_decode's): a warp waits, for `limit_us` microseconds at most, while another
+ * makes the expected arrival after `after_us` (arrive != 0) or none. 1 <= limit_us <= 1000000, after_us <= 1000000. */
+hsa_status hsa_selftest_timed_wait(void *workspace, size_t workspace_bytes, unsigned limit_us, unsigned after_us, int arrive,
+                                   void *stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Measurement hooks (no counterpart on the pages; used to time each kernel live).

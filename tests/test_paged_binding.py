@@ -56,13 +56,12 @@ def test_prefix_decode_workspace_size_is_zero_for_sizes_that_the_call_refuses(ar
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(ws=None), -3), (dict(ws=(1 << 20) + 16), -3), (dict(size=128), -3), (dict(limit=0), -1), (dict(limit=100001), -1), (dict(period=0), -1),
-    (dict(period=100001, steps=1), -1), (dict(steps=1001), -1), (dict(period=100000, steps=11), -1),
+    (dict(ws=None), -3), (dict(ws=(1 << 20) + 16), -3), (dict(size=128), -3), (dict(limit=0), -1), (dict(limit=1000001), -1), (dict(after=1000001), -1),
 ])
-def test_selftest_progress_wait_checks_its_arguments_on_host(kw, status):
-    args = dict(ws=1 << 20, size=4096, limit=1000, period=1000, steps=4, arrive=1, stream=None)
+def test_selftest_timed_wait_checks_its_arguments_on_host(kw, status):
+    args = dict(ws=1 << 20, size=4096, limit=1000, after=1000, arrive=1, stream=None)
     args.update(kw)
-    assert hsa.lib().hsa_selftest_progress_wait(*args.values()) == status and hsa.hsa_last_error() != ""
+    assert hsa.lib().hsa_selftest_timed_wait(*args.values()) == status and hsa.hsa_last_error() != ""
 
 
 def meta(*shape, dtype):

@@ -326,25 +326,27 @@ def test_serving_loop_of_a_wide_batch_without_a_pause(graph):
         assert (np.abs(got[k][1].double().cpu().numpy()[:, :, None] - ref["lse"]) <= tol_lse).all()
 
 
-@pytest.mark.parametrize("limit,period,steps,arrive,ok", [
-    (4000, 1000, 30, 1, True),      # 30 ms of work under a limit of 4
-    (4000, 1000, 30, 0, False),     # the work ends and nobody arrives
-    (2000, 1, 0, 0, False), (100000, 1, 1, 1, True),
-])
-def test_wait_goes_on_while_the_other_warp_has_work(limit, period, steps, arrive, ok):
+@pytest.mark.parametrize("limit,after,arrive,ok", [(50000, 10000, 1, True), (50000, 0, 1, True), (4000, 0, 0, False), (1, 0, 0, False)])
+def test_timed_wait_ends_with_the_arrival_or_at_its_limit(limit, after, arrive, ok):
     ws = torch.empty(4096, dtype=torch.uint8, device=DEV)
-    assert hsa.lib().hsa_selftest_progress_wait(ws.data_ptr(), 4096, limit, period, steps, arrive, torch.cuda.current_stream().cuda_stream) == 0
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ev[0].record()
+    assert hsa.lib().hsa_selftest_timed_wait(ws.data_ptr(), 4096, limit, after, arrive, torch.cuda.current_stream().cuda_stream) == 0
+    ev[1].record()
     if ok:
         hsa.hsa_workspace_status(ws)
     else:
         with pytest.raises(hsa.HSAError, match="HSA_ERR_TIMEOUT"):
             hsa.hsa_workspace_status(ws)
+    torch.cuda.synchronize()
+    # (64 probes stand between two looks at the time, each some tens of microseconds at most)
+    assert (after if ok else limit) * 0.9 <= ev[0].elapsed_time(ev[1]) * 1e3 <= (after if ok else limit) + 50000
 
 
 @pytest.mark.parametrize("B,H,tokens", [(4, 8, 1 << 28), (24, 32, 1 << 26)])
 def test_prefix_of_many_millions_of_tokens(B, H, tokens):
-    """Segments that take tens of milliseconds each: the warp that copies queries waits that long for the next one, a request's
-    own tokens, and copies the right ones then. The prefix is 64 pages in turn; the own tokens outweigh it by far in half of the
+    """Runs that take tens of milliseconds each, in many pieces: the warp that copies queries waits through every piece, and at the end of
+    all of them copies those of the requests' own tokens. The prefix is 64 pages in turn; the own tokens outweigh it by far in half of the
     requests, so that they are held to their rounding, and count for nothing in the others, which are held to the rounding of
     sums of that many terms."""
     D, Hkv, pages = 128, 8, 64

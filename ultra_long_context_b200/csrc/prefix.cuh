@@ -413,10 +413,9 @@ __device__ __forceinline__ void pf_prefetch_tmap(const CUtensorMap *m) {
 // A bounded wait of a whole warp, with one answer for all lanes: the warp is converged behind it, which the
 // aligned tcgen05 loads and stores that follow need. All lanes wait: where one did it for the others the warp was not put to
 // sleep, and twelve such warps took the issue slots of the softmax (every case 1.3 to 1.9 times slower).
-// The limit is time, since a probe may take 88 ns or tens of microseconds. All these waits are for work on a tile or two, which
+// The limit is time, since a probe may take 88 ns or tens of microseconds. These waits are for work on a tile or two, which
 // takes microseconds, but one: the warp that copies queries is done with its segment at once and waits for the next one's
-// announcement, which comes when the last tile of this one is on its way, 2^23 tiles of some 2 us later for a prefix of 2^30
-// tokens that is not split. It waits for as long as tiles are being copied.
+// announcement, which comes when the last tile of this one is on its way, 512 tiles of up to 2.4 us later.
 constexpr uint32_t kPfWaitNs = 2000000000;
 __device__ __forceinline__ bool pf_wait(uint32_t mbar, uint32_t parity) {
     return __all_sync(0xffffffffu, tc::mbar_wait_ns(mbar, parity & 1u, kPfWaitNs)) != 0;

@@ -66,8 +66,8 @@ struct FwSmem {
     static constexpr uint32_t LIM = MS + NR * 4;                          // int[NR]: keys that the row sees
     static constexpr uint32_t RED = LIM + NR * 4;                         // float[4][NR]: of a row and a warp's keys (maxima, sums)
     static constexpr uint32_t FAC = RED + 4 * NR * 4;                     // float[NR]: rescaling
-    static constexpr uint32_t MISC = FAC + NR * 4;                        // TMEM base, bad[3], tiles on their way
-    static constexpr uint32_t PLAN = (MISC + 20 + 15) / 16 * 16;
+    static constexpr uint32_t MISC = FAC + NR * 4;                        // TMEM base, bad[3]
+    static constexpr uint32_t PLAN = (MISC + 16 + 15) / 16 * 16;
     static constexpr uint32_t BCUM = PLAN + (sizeof(PfPlan) + 15) / 16 * 16;  // int[blocks + 1]
     static constexpr size_t dyn(int blocks) { return BCUM + 4 * ((size_t)blocks + 1) + 1024; }  // slack: 1 KB alignment
     static constexpr uint32_t S_COL = 0, O_COL = NB * 64, TMEM_COLS = NB == 4 ? 512 : 256;
@@ -109,7 +109,6 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
     unsigned char *s = smem_raw + (sb - raw);
     PfNote *s_ring = reinterpret_cast<PfNote *>(s + SM::RING);
     volatile int *s_bad = reinterpret_cast<volatile int *>(s + SM::MISC) + 1;  // [2] per warpgroup, [1] any other warp's, too
-    volatile int *s_copied = s_bad + 3;
     PfPlan *s_plan = reinterpret_cast<PfPlan *>(s + SM::PLAN);
     int32_t *s_bcum = reinterpret_cast<int32_t *>(s + SM::BCUM);
     auto bar = [&](int i) { return sb + SM::BAR + 8u * (uint32_t)i; };
@@ -121,7 +120,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         pf_prefetch_tmap(&tmV);
     }
     if (tid == 0) {
-        s_bad[0] = s_bad[1] = s_bad[2] = *s_copied = 0;
+        s_bad[0] = s_bad[1] = s_bad[2] = 0;
         for (int i = 0; i < KS; ++i) {
             tc::mbar_init(bar(SM::kKFull + i), 1);
             tc::mbar_init(bar(SM::kKEmpty + i), 1);
@@ -161,16 +160,15 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
 
     // the next announced segment; nr = 0 ends the walk
     int seg_no = 0;
-    auto take_after = [&](PfNote &g, auto wait) {
+    auto take = [&](PfNote &g) {
         const int slot = seg_no % kPfRing;
-        if (!wait(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kPfRing) & 1u)) return false;
+        if (!pf_wait(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kPfRing) & 1u)) return false;
         g = s_ring[slot];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(SM::kSegEmpty + slot));
         ++seg_no;
         return true;
     };
-    auto take = [&](PfNote &g) { return take_after(g, [](uint32_t m, uint32_t parity) { return pf_wait(m, parity); }); };
 
     if (warp == kFwTmaWarp) {
         // ================= the walk, K and V tiles =================
@@ -202,7 +200,6 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
                 }
                 const int p0 = __shfl_sync(0xffffffffu, ids, 2 * (t & 15)), p1 = __shfl_sync(0xffffffffu, ids, 2 * (t & 15) + 1);
                 if (lane == 0) {
-                    *s_copied = n;
                     const bool g0 = p0 >= 0 && p0 < pages_all, g1 = p1 >= 0 && p1 < pages_all;
                     // a page that is not there lies behind the pool's last row: it is filled with zeros
                     const int y0 = ((g0 ? p0 : pages_all) * a.Hkv + (g0 ? seg.h : 0)) * kChunk;
@@ -247,7 +244,7 @@ __global__ void __launch_bounds__(kFwThreads, 1) prefix_few_kernel(const PrefixA
         while (true) {
             const int q = seg_no & 1;
             const uint32_t use = (uint32_t)(seg_no >> 1);
-            ok = take_after(g, [&](uint32_t m, uint32_t parity) { return tc::mbar_wait_while(m, parity, s_copied, kPfWaitNs); });
+            ok = take(g);
             if (!ok || g.s.nr == 0) break;
             ok = pf_wait(bar(SM::kQEmpty + q), (use & 1u) ^ 1u);
             if (!ok) break;

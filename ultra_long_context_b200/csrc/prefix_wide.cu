@@ -53,8 +53,7 @@ struct PfSmem {
     static constexpr uint32_t BADP = ROW + 2 * 2 * 128 * 4;  // int[8]: a wait of the pair of warps ran out
     static constexpr uint32_t TMEM = BADP + 32;
     static constexpr uint32_t BAD = TMEM + 4;
-    static constexpr uint32_t COPIED = BAD + 4;  // int: tiles on their way
-    static constexpr uint32_t PLAN = (COPIED + 4 + 15) / 16 * 16;
+    static constexpr uint32_t PLAN = (BAD + 4 + 15) / 16 * 16;
     static constexpr uint32_t BCUM = PLAN + (sizeof(PfPlan) + 15) / 16 * 16;  // int[blocks + 1]
     static constexpr size_t dyn(int blocks) { return BCUM + 4 * ((size_t)blocks + 1) + 1024; }  // slack: 1 KB alignment
     static constexpr uint32_t S_COL = 0, O_COL = 2 * kPfTile, TMEM_COLS = 512;
@@ -108,7 +107,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     unsigned char *s = smem_raw + (sb - raw);
     PfNote *s_ring = reinterpret_cast<PfNote *>(s + SM::RING);
     volatile int *s_badp = reinterpret_cast<volatile int *>(s + SM::BADP), *s_bad = reinterpret_cast<volatile int *>(s + SM::BAD);
-    volatile int *s_copied = reinterpret_cast<volatile int *>(s + SM::COPIED);
     PfPlan *s_plan = reinterpret_cast<PfPlan *>(s + SM::PLAN);
     int32_t *s_bcum = reinterpret_cast<int32_t *>(s + SM::BCUM);
     auto bar = [&](int i) { return sb + SM::BAR + 8u * (uint32_t)i; };
@@ -120,7 +118,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         pf_prefetch_tmap(&tmV);
     }
     if (tid == 0) {
-        *s_bad = *s_copied = 0;
+        *s_bad = 0;
         for (int i = 0; i < 8; ++i) s_badp[i] = 0;
         for (int i = 0; i < KS; ++i) {
             tc::mbar_init(bar(SM::kKFull + i), 1);
@@ -155,16 +153,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
     bool ok = true;
 
     int seg_no = 0;  // the next announced segment
-    auto take_after = [&](PfNote &g, auto wait) {
+    auto take = [&](PfNote &g) {
         const int slot = seg_no % kPfRing;
-        if (!wait(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kPfRing) & 1u)) return false;
+        if (!pf_wait(bar(SM::kSegFull + slot), (uint32_t)(seg_no / kPfRing) & 1u)) return false;
         g = s_ring[slot];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(SM::kSegEmpty + slot));
         ++seg_no;
         return true;
     };
-    auto take = [&](PfNote &g) { return take_after(g, [](uint32_t m, uint32_t parity) { return pf_wait(m, parity); }); };
 
     if (warp == kPfTmaWarp) {
         // ================= the walk, K and V tiles =================
@@ -202,7 +199,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
                 }
                 const int p0 = __shfl_sync(0xffffffffu, ids, 2 * (t & 15)), p1 = __shfl_sync(0xffffffffu, ids, 2 * (t & 15) + 1);
                 if (lane == 0) {
-                    *s_copied = n;
                     const bool g0 = p0 >= 0 && p0 < pages_all, g1 = p1 >= 0 && p1 < pages_all;
                     // a page that is not there lies behind the pool's last row: it is filled with zeros
                     const int y0 = ((g0 ? p0 : pages_all) * a.Hkv + (g0 ? seg.h : 0)) * kChunk;
@@ -243,7 +239,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefix_wide_kernel(const Prefix
         int turn = 0;
         PfNote g;
         while (true) {
-            ok = take_after(g, [&](uint32_t m, uint32_t parity) { return tc::mbar_wait_while(m, parity, s_copied, kPfWaitNs); });
+            ok = take(g);
             if (!ok || g.s.nr == 0) break;
             const PfSeg &seg = g.s;
             const bool both = pf_both(seg);

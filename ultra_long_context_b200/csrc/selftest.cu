@@ -1,4 +1,4 @@
-// selftest.cu -- hsa_selftest_bounded_wait and hsa_selftest_progress_wait: the kernels' bounded device waits on their own.
+// selftest.cu -- hsa_selftest_bounded_wait and hsa_selftest_timed_wait: the kernels' bounded device waits on their own.
 //
 // Every kernel of the library waits on mbarriers (TMA copies landing, tensor-core products completing,
 // one warp role handing a buffer to another) with a bounded number of probes. A wait that runs out
@@ -8,8 +8,8 @@
 // purpose, safely: one warp allocates TMEM as the operator kernels do, waits with the same helper on
 // an mbarrier whose single expected arrival is never made (a short probe limit instead of the
 // kernels' own), records the timeout exactly as they do, frees its TMEM and exits. No
-// copy is in flight, nothing faults, and the context stays usable. hsa_selftest_progress_wait does the same with the wait that
-// goes on while another warp's counter moves (tc::mbar_wait_while).
+// copy is in flight, nothing faults, and the context stays usable. hsa_selftest_timed_wait does the
+// same with the wait that time bounds (tc::mbar_wait_ns).
 #include <string>
 
 #include "../../include/hsa.h"
@@ -41,27 +41,22 @@ __global__ void __launch_bounds__(32) bounded_wait_selftest_kernel(int32_t *err,
     hsa::tc::tmem_dealloc(tmem, 32);
 }
 
-__global__ void __launch_bounds__(64) progress_wait_selftest_kernel(int32_t *err, unsigned limit_ns, unsigned period_ns, unsigned steps, bool arrive) {
+__global__ void __launch_bounds__(64) timed_wait_selftest_kernel(int32_t *err, unsigned limit_ns, unsigned after_ns, bool arrive) {
     __shared__ __align__(8) uint64_t bar;
-    __shared__ volatile int count;
     const uint32_t mbar = hsa::smem_u32(&bar);
     if (threadIdx.x == 0) {
-        count = 0;
         hsa::tc::mbar_init(mbar, 1);
         hsa::tc::fence_mbar_init();
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        const bool ok = hsa::tc::mbar_wait_while(mbar, 0, &count, limit_ns);
+        const bool ok = __all_sync(0xffffffffu, hsa::tc::mbar_wait_ns(mbar, 0, limit_ns)) != 0;
         if (!ok && threadIdx.x == 0) atomicOr(err, 1);
-    } else if (threadIdx.x == 32) {
-        for (unsigned i = 0; i < steps; ++i) {
-            const uint32_t t0 = hsa::tc::timer_ns();
-            // (bounded, should the timer stand still: a sleep takes up to twice its time)
-            for (unsigned n = 0; n < period_ns / 500 + 1 && hsa::tc::timer_ns() - t0 < period_ns; ++n) __nanosleep(1000);
-            count = (int)i + 1;
-        }
-        if (arrive) hsa::tc::mbar_arrive(mbar);
+    } else if (threadIdx.x == 32 && arrive) {
+        const uint32_t t0 = hsa::tc::timer_ns();
+        // (bounded, should the timer stand still)
+        for (unsigned n = 0; n < after_ns / 500 + 1 && hsa::tc::timer_ns() - t0 < after_ns; ++n) __nanosleep(1000);
+        hsa::tc::mbar_arrive(mbar);
     }
 }
 
@@ -73,21 +68,20 @@ hsa_status check_workspace(const char *name, void *workspace, size_t workspace_b
 
 }  // namespace
 
-extern "C" hsa_status hsa_selftest_progress_wait(void *workspace, size_t workspace_bytes, unsigned limit_us,
-                                                 unsigned period_us, unsigned steps, int arrive, void *stream) {
+extern "C" hsa_status hsa_selftest_timed_wait(void *workspace, size_t workspace_bytes, unsigned limit_us,
+                                              unsigned after_us, int arrive, void *stream) {
     hsa::set_last_error("");
-    const hsa_status st = check_workspace("hsa_selftest_progress_wait", workspace, workspace_bytes);
+    const hsa_status st = check_workspace("hsa_selftest_timed_wait", workspace, workspace_bytes);
     if (st != HSA_OK) return st;
-    if (limit_us < 1 || limit_us > 100000 || period_us < 1 || period_us > 100000 || steps > 1000 ||
-        (uint64_t)period_us * steps > 1000000) {
-        hsa::set_last_error("hsa_selftest_progress_wait: limit_us and period_us must be in [1, 100000], steps in [0, 1000], their product at most 1000000");
+    if (limit_us < 1 || limit_us > 1000000 || after_us > 1000000) {
+        hsa::set_last_error("hsa_selftest_timed_wait: limit_us must be in [1, 1000000], after_us in [0, 1000000]");
         return HSA_ERR_INVALID_ARG;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int32_t *err = static_cast<int32_t *>(workspace);
     cudaError_t e = cudaMemsetAsync(err, 0, sizeof(int32_t), s);
     if (e == cudaSuccess) {
-        progress_wait_selftest_kernel<<<1, 64, 0, s>>>(err, limit_us * 1000u, period_us * 1000u, steps, arrive != 0);
+        timed_wait_selftest_kernel<<<1, 64, 0, s>>>(err, limit_us * 1000u, after_us * 1000u, arrive != 0);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess) return HSA_OK;

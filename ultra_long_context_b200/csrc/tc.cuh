@@ -290,16 +290,6 @@ __device__ __forceinline__ bool mbar_wait_ns(uint32_t mbar, uint32_t parity, uin
         }
     }
 }
-// The same by a whole warp, with one answer for all lanes, for a wait that rightly lasts as long as another role has work: it runs
-// out when `count`, which that role moves with everything that it does, has stood still for the limit.
-__device__ __forceinline__ bool mbar_wait_while(uint32_t mbar, uint32_t parity, const volatile int *count, uint32_t limit) {
-    for (int seen = *count;;) {
-        if (__all_sync(0xffffffffu, mbar_wait_ns(mbar, parity, limit))) return true;
-        const int now = __shfl_sync(0xffffffffu, *count, 0);
-        if (__all_sync(0xffffffffu, now == seen)) return false;
-        seen = now;
-    }
-}
 
 // Non-blocking probe: has the phase with parity `parity` completed?
 __device__ __forceinline__ bool mbar_test(uint32_t mbar, uint32_t parity) {

@@ -54,7 +54,7 @@ SIGNATURES = {
     "hsa_prefix_decode": ([_P, _P, _P, _I, _P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P],
                           _I),
     "hsa_selftest_bounded_wait": ([_P, _SZ, _U, _P], _I),
-    "hsa_selftest_progress_wait": ([_P, _SZ, _U, _U, _U, _I, _P], _I),
+    "hsa_selftest_timed_wait": ([_P, _SZ, _U, _U, _I, _P], _I),
     "hsa_profile_enable": ([_I], _I),
     "hsa_profile_summary": ([ctypes.c_char_p, _SZ], _I),
 }

@@ -1,6 +1,7 @@
 """The shared-prefix decode over long runs: segments of more than 32 tiles of keys, whose partial sums, references and rings
 of buffers go round, in both kernels and in the launch order that a user's call has. The plain form here runs in fp64 on the GPU,
-and page ids repeat in the prefix's table, so that a long prefix needs a small pool only."""
+and page ids repeat in the prefix's table, so that a long prefix needs a small pool only. At the end, large calls of the plan and the
+append."""
 import math
 
 import numpy as np
@@ -499,3 +500,37 @@ def test_threads_that_call_at_once():
     assert not errors, errors
     for w, g in zip(want, got):
         assert len(g) == 25 and all(torch.equal(o, w[0]) and torch.equal(l, w[1]) for o, l in g)
+
+
+def test_append_of_rows_past_two_to_the_30_vectors():
+    """Rows of 8.6e9 elements, where vectors are counted in 64 bits; all but a few rows are skipped."""
+    n, Hkv, D, pages = (1 << 22) + 3, 16, 128, 3
+    K = torch.empty(n, Hkv, D, dtype=BF16, device=DEV)
+    rows = torch.tensor([0, 1, (1 << 20) - 1, 1 << 20, (1 << 21) + 5, (1 << 22) - 1, 1 << 22, n - 1], device=DEV)
+    K[rows] = torch.randn(len(rows), Hkv, D, device=DEV).to(BF16)
+    slots = torch.full((n,), -1, dtype=torch.int64, device=DEV)
+    at = torch.tensor([191, 0, 64, 5, 63, 127, 100, 130], device=DEV)
+    slots[rows] = at
+    Kp, Vp = (torch.zeros(pages, Hkv, 64, D, dtype=BF16, device=DEV) for _ in range(2))
+    hsa.hsa_page_append(K, K, slots, Kp, Vp)
+    torch.cuda.synchronize()
+    want = torch.zeros_like(Kp)
+    want[at // 64, :, at % 64] = K[rows]
+    assert torch.equal(Kp, want) and torch.equal(Vp, want)
+
+
+def test_plan_of_a_prompt_that_fills_its_table_and_more():
+    """One request of 2^24 tokens and one that does not fit behind it: as many slots as a map holds, in one call."""
+    n = 1 << 24
+    width = n // 64
+    table = torch.full((2, width), -1, dtype=torch.int32, device=DEV)
+    ring = torch.randperm(width + 5, device=DEV).to(torch.int32)
+    pool = torch.tensor([3, 3 + width + 5, 0], device=DEV)
+    before = ring.clone()
+    cu, slots, total = hsa.hsa_page_plan(torch.zeros(2, dtype=torch.int64, device=DEV), torch.tensor([n, 6 * 64], dtype=torch.int32, device=DEV),
+                                         table, ring, pool, n + 6 * 64)
+    torch.cuda.synchronize()
+    ids = before.roll(-3)[:width]
+    assert torch.equal(table[0], ids) and (table[1] == -1).all() and torch.equal(ring, before)
+    assert torch.equal(slots[:n], (ids.long()[:, None] * 64 + torch.arange(64, device=DEV)).view(-1)) and (slots[n:] == -1).all()
+    assert cu.tolist() == [0, n, n + 384] and total.tolist() == [n, 0] and pool.tolist() == [3 + width, 3 + width + 5, 1]
